@@ -31,6 +31,7 @@ TT_EOFFSETS = -7
 TT_ETOOBIG = -8
 TT_ESTALE = -9
 TT_EUNSUPPORTED = -10
+TT_ENOBLOCKS = -11
 
 _lib = None
 
@@ -320,3 +321,8 @@ def profile_read(cap=64):
 
 def free():
     lib().tt_free()
+
+
+from .serve import (STATE_DEAD, STATE_FREE, BlockTable, Grammar, TokenStrings, grammar_advance_into,  # noqa: E402
+                    grammar_bits, grammar_bits_into, plan_blocks_into, release_blocks_into, shape_logits,
+                    shape_logits_into, token_bits, token_bits_into)

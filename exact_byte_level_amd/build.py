@@ -33,6 +33,7 @@ def build(verbose=False):
     cmd = ["hipcc"] + HIPCC_FLAGS + [
         "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", GEN,
         os.path.join(CSRC, "tt_kernels.hip"), os.path.join(CSRC, "tt_api.cpp"),
+        os.path.join(CSRC, "tt_serve_kernels.hip"), os.path.join(CSRC, "tt_serve_api.cpp"),
         "-o", tmp,
     ]
     if verbose:

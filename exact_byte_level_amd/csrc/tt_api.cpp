@@ -11,6 +11,7 @@
 
 #include "tt.h"
 #include "tt_kernels.h"
+#include "tt_serve.h"
 #include "unicode_table.inc"
 
 namespace {
@@ -280,6 +281,43 @@ int session_full(tt_session* s, int64_t n, hipStream_t st) {
       launch_session_full(s->text, n, s->tail, g.w, s->info_dev, s->info_map, st) != hipSuccess)
     return TT_EHIP;
   return session_read_info(s, st);
+}
+
+// Sizes of the loaded tokenizer's token strings and, if asked for, the
+// strings, put together from the operands of every merge.
+int vocab_strings(int64_t* n_tokens, int64_t* n_bytes, uint8_t* bytes, int32_t* offsets) {
+  const int rc = check_stream_state();
+  if (rc != TT_OK) return rc;
+  try {
+    const size_t M = (size_t)g.n_merges;
+    std::vector<uint64_t> kids(M);
+    if (M && hipMemcpy(kids.data(), g.d_kids, M * 8, hipMemcpyDeviceToHost) != hipSuccess) return TT_EHIP;
+    // where each token's string starts; operands come before the token
+    std::vector<int64_t> at(256 + M + 1);
+    for (size_t t = 0; t < 256 + M; ++t) {
+      int64_t len = 1;
+      if (t >= 256) {
+        const size_t x = (uint32_t)kids[t - 256], y = kids[t - 256] >> 32;
+        len = (at[x + 1] - at[x]) + (at[y + 1] - at[y]);
+      }
+      at[t + 1] = at[t] + len;
+      if (at[t + 1] > 0x7FFFFFFF) return TT_ETOOBIG;
+    }
+    *n_tokens = (int64_t)(256 + M);
+    *n_bytes = at[256 + M];
+    if (!bytes) return TT_OK;
+    for (size_t t = 0; t < 256; ++t) bytes[t] = (uint8_t)t;
+    for (size_t t = 256; t < 256 + M; ++t) {
+      const size_t x = (uint32_t)kids[t - 256], y = kids[t - 256] >> 32;
+      const size_t lx = (size_t)(at[x + 1] - at[x]), ly = (size_t)(at[y + 1] - at[y]);
+      std::memcpy(bytes + at[t], bytes + at[x], lx);
+      std::memcpy(bytes + at[t] + lx, bytes + at[y], ly);
+    }
+    for (size_t t = 0; t <= 256 + M; ++t) offsets[t] = (int32_t)at[t];
+  } catch (const std::bad_alloc&) {
+    return TT_ENOMEM;
+  }
+  return TT_OK;
 }
 
 }  // namespace
@@ -895,6 +933,19 @@ int tt_profile_read(const char** names, float* ms, int cap) {
   return k;
 }
 
+int tt_vocab_size(int64_t* n_tokens, int64_t* n_bytes) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (!n_tokens || !n_bytes) return TT_EINVAL;
+  return vocab_strings(n_tokens, n_bytes, nullptr, nullptr);
+}
+
+int tt_vocab_strings(uint8_t* bytes, int32_t* offsets) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (!bytes || !offsets) return TT_EINVAL;
+  int64_t n_tokens = 0, n_bytes = 0;
+  return vocab_strings(&n_tokens, &n_bytes, bytes, offsets);
+}
+
 void tt_free(void) {
   std::lock_guard<std::mutex> lock(g_mu);
   (void)hipDeviceSynchronize();
@@ -915,6 +966,7 @@ const char* tt_strerror(int code) {
     case TT_ETOOBIG: return "size beyond library limits";
     case TT_ESTALE: return "tokenizer replaced since the session began";
     case TT_EUNSUPPORTED: return "input case not decided by the o200k-style GPU rules";
+    case TT_ENOBLOCKS: return "not enough free blocks";
     default: return "unknown error";
   }
 }

@@ -1,0 +1,530 @@
+// tt_serve_kernels.hip -- block tables, token sets, grammar masks and the
+// shaping of logits (declared in include/tt_serve.h).
+#include "tt_serve_kernels.h"
+
+namespace tt {
+namespace {
+
+constexpr int WAVE = 64;
+
+__host__ __device__ inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+__host__ __device__ inline uint32_t div_up32(uint32_t a, uint32_t b) { return a / b + (a % b != 0); }
+
+// ---------------------------------------------------------------- block tables
+
+constexpr int BT_THREADS = 256;
+constexpr int BT_WAVES = BT_THREADS / WAVE;
+
+// Data errors, as bits; the lowest one set is reported.
+constexpr uint32_t BAD_OFFSETS = 1, BAD_FREE = 2, BAD_SIZE = 4, BAD_NONE_LEFT = 8;
+
+__device__ inline int64_t fault_code(uint32_t bad) {
+  if (bad & BAD_OFFSETS) return TT_EOFFSETS;
+  if (bad & BAD_FREE) return TT_EINVAL;
+  if (bad & BAD_SIZE) return TT_ETOOBIG;
+  return TT_ENOBLOCKS;
+}
+
+__device__ inline int64_t wave_sum(int64_t v) {
+  for (int d = WAVE / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// Sums of K values over the workgroup (in every thread), and the union of bits.
+template <int K>
+__device__ inline void block_sums(int64_t (&v)[K], uint32_t& bits, int64_t* lds) {
+  for (int d = WAVE / 2; d > 0; d >>= 1) bits |= (uint32_t)__shfl_xor((int)bits, d);
+  const int w = threadIdx.x / WAVE;
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
+  if (threadIdx.x % WAVE == 0) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) lds[w * (K + 1) + k] = v[k];
+    lds[w * (K + 1) + K] = (int64_t)bits;
+  }
+  __syncthreads();
+  bits = 0;
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = 0;
+  for (int i = 0; i < BT_WAVES; ++i) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += lds[i * (K + 1) + k];
+    bits |= (uint32_t)lds[i * (K + 1) + K];
+  }
+  __syncthreads();
+}
+
+// Exclusive sum of v over the workgroup; *total receives the sum.
+__device__ inline uint32_t block_exclusive(uint32_t v, uint32_t* total, uint32_t* lds) {
+  const int lane = threadIdx.x % WAVE, w = threadIdx.x / WAVE;
+  uint32_t inc = v;
+  for (int d = 1; d < WAVE; d <<= 1) {
+    const uint32_t o = (uint32_t)__shfl_up((int)inc, d);
+    if (lane >= d) inc += o;
+  }
+  if (lane == WAVE - 1) lds[w] = inc;
+  __syncthreads();
+  uint32_t before = 0, all = 0;
+  for (int i = 0; i < BT_WAVES; ++i) {
+    if (i < w) before += lds[i];
+    all += lds[i];
+  }
+  __syncthreads();
+  *total = all;
+  return before + inc - v;
+}
+
+// One row of a plan: where its new tokens start, how many they are, the
+// blocks it has and the ones it needs.
+struct RowPlan {
+  int32_t length;  // as given
+  uint32_t start, held, need;
+  int64_t count;
+};
+
+__device__ inline RowPlan row_plan(const tt_plan_args& a, int64_t r, uint32_t& bad) {
+  RowPlan p;
+  p.length = a.lengths[r];
+  const int64_t start = p.length > 0 ? p.length : 0;
+  p.count = p.length >= 0;
+  if (a.offsets) {
+    p.count = a.offsets[r + 1] - a.offsets[r];
+    if (p.count < 0) {
+      bad |= BAD_OFFSETS;
+      p.count = 0;
+    }
+  }
+  p.start = (uint32_t)start;
+  p.held = p.need = 0;
+  const int64_t room = a.width * a.block_size - start;  // width * block_size < 2^31
+  if (p.count > room) {
+    bad |= BAD_SIZE;
+    p.count = 0;
+    return p;
+  }
+  const uint32_t bs = (uint32_t)a.block_size;
+  p.held = div_up32(p.start, bs);
+  p.need = div_up32(p.start + (uint32_t)p.count, bs) - p.held;
+  return p;
+}
+
+// Every workgroup sums up all rows by itself (a few KB from L2), so that one
+// launch is enough: no workgroup waits for another one's sums.
+// Bytes bound it: 16 written for a token.
+template <bool SINGLE>
+__global__ __launch_bounds__(BT_THREADS) void k_plan(tt_plan_args a, int64_t per_block, bool finish) {
+  __shared__ int64_t sums[BT_WAVES * 5];
+  __shared__ uint32_t scan[BT_WAVES];
+  __shared__ int32_t s_off[BT_THREADS + 1];
+  __shared__ uint32_t s_start[BT_THREADS], s_held[BT_THREADS], s_base[BT_THREADS];
+  const int tid = threadIdx.x;
+  const int64_t t0 = min((int64_t)blockIdx.x * per_block, a.places);
+  const int64_t t1 = min(t0 + per_block, a.places);
+  // all blocks needed; those of the rows that end at or before t0, and how many rows that are; tokens
+  int64_t v[4] = {0, 0, 0, 0};
+  uint32_t bad = 0;
+  for (int64_t r = tid; r < a.rows; r += BT_THREADS) {
+    const RowPlan p = row_plan(a, r, bad);
+    const bool before = (SINGLE ? r + 1 : a.offsets[r + 1]) <= t0;
+    v[0] += p.need;
+    v[1] += before ? p.need : 0;
+    v[2] += before;
+    v[3] += p.count;
+  }
+  const int64_t n_free = *a.n_free;
+  if (!SINGLE) {
+    if (a.offsets[0] != 0) bad |= BAD_OFFSETS;
+    if (a.offsets[a.rows] > a.places) bad |= BAD_SIZE;
+  }
+  if (n_free < 0 || n_free > a.free_cap) bad |= BAD_FREE;
+  block_sums(v, bad, sums);
+  if (v[0] > n_free) bad |= BAD_NONE_LEFT;
+  const int64_t total = bad ? 0 : (SINGLE ? a.rows : v[3]);  // places that may hold a token
+  const uint32_t bs = (uint32_t)a.block_size;
+  const int64_t end = min(t1, total);
+  uint32_t carry = (uint32_t)v[1];
+  for (int64_t c0 = v[2]; t0 < end && c0 < a.rows; c0 += BT_THREADS) {
+    const int64_t r = c0 + tid;
+    RowPlan p{-1, 0, 0, 0, 0};
+    if (r < a.rows) p = row_plan(a, r, bad);
+    uint32_t chunk;
+    const uint32_t base = carry + block_exclusive(p.need, &chunk, scan);
+    carry += chunk;
+    s_start[tid] = p.start;
+    s_held[tid] = p.held;
+    s_base[tid] = base;
+    if (!SINGLE) {
+      s_off[tid] = (int32_t)a.offsets[min(r, a.rows)];
+      if (tid == 0) s_off[BT_THREADS] = (int32_t)a.offsets[min(c0 + BT_THREADS, a.rows)];
+    } else {
+      s_off[tid] = p.length;
+    }
+    __syncthreads();
+    const int64_t lo = SINGLE ? max(t0, c0) : max(t0, (int64_t)s_off[0]);
+    const int64_t hi = min(end, SINGLE ? c0 + BT_THREADS : (int64_t)s_off[BT_THREADS]);
+    int i = 0;
+    for (int64_t t = lo + tid; t < hi; t += BT_THREADS) {
+      uint32_t place;
+      if (SINGLE) {
+        i = (int)(t - c0);
+        place = s_start[i];
+      } else {
+        if (s_off[i + 1] <= t) {  // the last row that starts at or before t
+          int b = BT_THREADS;
+          while (b - i > 1) {
+            const int m = (i + b) >> 1;
+            if (s_off[m] <= t) i = m;
+            else b = m;
+          }
+        }
+        place = s_start[i] + (uint32_t)(t - s_off[i]);
+      }
+      const int64_t row = c0 + i;
+      const uint32_t blk = place / bs, in = place - blk * bs, held = s_held[i];
+      int64_t slot = -1;
+      const bool live = !SINGLE || s_off[i] >= 0;
+      if (live) {
+        int32_t id;
+        if (blk >= held) {
+          id = a.free_blocks[n_free - 1 - (int64_t)(s_base[i] + (blk - held))];
+          if (in == 0) a.table[row * a.table_stride + blk] = id;
+        } else {
+          id = a.table[row * a.table_stride + blk];
+        }
+        if (id >= 0) slot = (int64_t)id * bs + in;
+      }
+      a.slots[t] = slot;
+      if (a.positions) a.positions[t] = live ? (int32_t)place : -1;
+      if (a.row_of) a.row_of[t] = live ? (int32_t)row : -1;
+    }
+    if (hi >= end) break;
+    __syncthreads();
+  }
+  for (int64_t t = max(t0, total) + tid; t < t1; t += BT_THREADS) {
+    a.slots[t] = -1;
+    if (a.positions) a.positions[t] = -1;
+    if (a.row_of) a.row_of[t] = -1;
+  }
+  if (!finish || blockIdx.x != 0) return;
+  __syncthreads();  // out_lengths may be lengths
+  uint32_t unused = 0;
+  for (int64_t r = tid; r < a.rows; r += BT_THREADS) {
+    const RowPlan p = row_plan(a, r, unused);
+    a.out_lengths[r] = bad || p.count == 0 ? p.length : (int32_t)(p.start + (uint32_t)p.count);
+  }
+  if (tid == 0) {
+    *a.out_n_free = (int32_t)(bad ? n_free : n_free - v[0]);
+    *a.out_n = bad ? fault_code(bad) : v[3];
+  }
+}
+
+// The blocks that row r gives back.
+__device__ inline uint32_t row_release(const ReleaseArgs& a, int64_t r, uint32_t& bad) {
+  const int32_t length = a.lengths[r];
+  if (!a.done[r] || length < 0) return 0;
+  const uint32_t m = div_up32((uint32_t)length, (uint32_t)a.block_size);
+  if (m > a.width) {
+    bad |= BAD_SIZE;
+    return 0;
+  }
+  return m;
+}
+
+// As k_plan: each workgroup sums up all rows, then copies its part of the
+// blocks that come back.
+__global__ __launch_bounds__(BT_THREADS) void k_release(ReleaseArgs a, bool fill, bool finish) {
+  __shared__ int64_t sums[BT_WAVES * 2];
+  __shared__ uint32_t scan[BT_WAVES];
+  __shared__ uint32_t s_base[BT_THREADS + 1];
+  const int tid = threadIdx.x;
+  int64_t v[1] = {0};
+  uint32_t bad = 0;
+  for (int64_t r = tid; r < a.rows; r += BT_THREADS) v[0] += row_release(a, r, bad);
+  const int64_t n_free = *a.n_free;
+  if (n_free < 0 || n_free > a.free_cap) bad |= BAD_FREE;
+  block_sums(v, bad, sums);
+  if (!(bad & BAD_FREE) && n_free + v[0] > a.free_cap) bad |= BAD_SIZE;
+  if (fill && !bad) {
+    const int64_t total = v[0], per = div_up(total, gridDim.x);
+    const int64_t o0 = min((int64_t)blockIdx.x * per, total), o1 = min(o0 + per, total);
+    int64_t carry = 0;
+    for (int64_t c0 = 0; c0 < a.rows && carry < o1; c0 += BT_THREADS) {
+      const int64_t r = c0 + tid;
+      uint32_t chunk;
+      const uint32_t base = block_exclusive(r < a.rows ? row_release(a, r, bad) : 0, &chunk, scan);
+      s_base[tid] = base;
+      if (tid == 0) s_base[BT_THREADS] = chunk;
+      __syncthreads();
+      const int64_t lo = max(o0, carry), hi = min(o1, carry + chunk);
+      int i = 0;
+      for (int64_t o = lo + tid; o < hi; o += BT_THREADS) {
+        const uint32_t t = (uint32_t)(o - carry);
+        if (s_base[i + 1] <= t) {
+          int b = BT_THREADS;
+          while (b - i > 1) {
+            const int m = (i + b) >> 1;
+            if (s_base[m] <= t) i = m;
+            else b = m;
+          }
+        }
+        a.free_blocks[n_free + o] = a.table[(c0 + i) * a.table_stride + (t - s_base[i])];
+      }
+      carry += chunk;
+      __syncthreads();
+    }
+  }
+  if (!finish || blockIdx.x != 0) return;
+  __syncthreads();  // out_lengths may be lengths
+  for (int64_t r = tid; r < a.rows; r += BT_THREADS) {
+    const int32_t length = a.lengths[r];
+    a.out_lengths[r] = !bad && a.done[r] && length >= 0 ? -1 : length;
+  }
+  if (tid == 0) {
+    *a.out_n_free = (int32_t)(bad ? n_free : n_free + v[0]);
+    *a.out_n = bad ? fault_code(bad) : v[0];
+  }
+}
+
+// ---------------------------------------------------------------- token sets
+
+constexpr int TB_THREADS = 1024;
+constexpr int TB_WORDS = 16384;  // words of a set that one workgroup holds in LDS
+
+__global__ __launch_bounds__(TB_THREADS) void k_token_bits(const int32_t* ids, int64_t n, const int64_t* offsets,
+                                                           int64_t vocab, int32_t* bits, int64_t stride, int tiles,
+                                                           bool add) {
+  extern __shared__ uint32_t set[];
+  const int64_t r = blockIdx.x / tiles, words = div_up(vocab, 32);
+  const int64_t w0 = (int64_t)(blockIdx.x % tiles) * TB_WORDS;
+  const int here = (int)min((int64_t)TB_WORDS, words - w0);
+  for (int i = threadIdx.x; i < here; i += TB_THREADS) set[i] = 0;
+  __syncthreads();
+  const int64_t lo = offsets ? min(max(offsets[r], (int64_t)0), n) : 0;
+  const int64_t hi = offsets ? min(max(offsets[r + 1], (int64_t)0), n) : n;
+  const uint32_t v0 = (uint32_t)(w0 * 32), v1 = (uint32_t)min(vocab, (w0 + here) * 32);
+  for (int64_t i = lo + threadIdx.x; i < hi; i += TB_THREADS) {
+    const uint32_t id = (uint32_t)ids[i];
+    if (id >= v0 && id < v1) atomicOr(&set[(id - v0) >> 5], 1u << (id & 31));
+  }
+  __syncthreads();
+  uint32_t* out = reinterpret_cast<uint32_t*>(bits) + r * stride + w0;
+  for (int i = threadIdx.x; i < here; i += TB_THREADS) out[i] = add ? out[i] | set[i] : set[i];
+}
+
+// ------------------------------------------------------------------- grammars
+
+constexpr int GR_THREADS = 256;
+
+// The bytes of a token, kept inside the strings whatever its offsets say.
+__device__ inline void token_span(const tt_grammar& g, int64_t v, int64_t& at, int& len) {
+  const int64_t a = g.string_offsets[v], b = g.string_offsets[v + 1];
+  at = min(max(a, (int64_t)0), g.n_bytes);
+  len = (int)(min(max(b, at), g.n_bytes) - at);
+}
+
+__global__ __launch_bounds__(GR_THREADS) void k_grammar_bits(tt_grammar g, const int32_t* states, int64_t vocab,
+                                                             int32_t* bits, int64_t stride, int tiles) {
+  __shared__ uint8_t cls[256];
+  for (int i = threadIdx.x; i < 256; i += GR_THREADS) cls[i] = (uint8_t)min((int)g.classes[i], (int)g.n_classes - 1);
+  __syncthreads();
+  const int64_t r = blockIdx.x / tiles;
+  const int64_t v = (int64_t)(blockIdx.x % tiles) * GR_THREADS + threadIdx.x;
+  const int32_t q0 = states[r];
+  const uint32_t n = (uint32_t)g.n_states, nc = (uint32_t)g.n_classes;
+  bool ok = false;
+  if (v < vocab) {
+    if (q0 == TT_STATE_FREE) {
+      ok = true;
+    } else if ((uint32_t)q0 < n) {
+      if (v == g.end_id) {
+        ok = g.accept[q0] != 0;
+      } else if (v < g.n_tokens) {
+        int64_t at;
+        int len;
+        token_span(g, v, at, len);
+        uint32_t q = (uint32_t)q0;
+        for (int k = 0; k < len && q < n; ++k) q = (uint32_t)(int32_t)g.next[q * nc + cls[g.strings[at + k]]];
+        ok = len > 0 && q < n;
+      }
+    }
+  }
+  const uint64_t m = __ballot(ok);
+  const int lane = threadIdx.x % WAVE;
+  const int64_t word = v / 32;
+  if (lane % 32 == 0 && word < div_up(vocab, 32)) bits[r * stride + word] = (int32_t)(uint32_t)(m >> lane);
+}
+
+__global__ void k_grammar_advance(tt_grammar g, const int32_t* states, const int32_t* tokens, int64_t rows,
+                                  int32_t* out) {
+  const int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (r >= rows) return;
+  const int32_t q0 = states[r], t = tokens[r];
+  const uint32_t n = (uint32_t)g.n_states, nc = (uint32_t)g.n_classes;
+  int32_t q = q0;
+  if (t >= 0 && q0 != TT_STATE_FREE) {
+    q = TT_STATE_DEAD;
+    if ((uint32_t)q0 < n && t != g.end_id && t < g.n_tokens) {
+      int64_t at;
+      int len;
+      token_span(g, t, at, len);
+      uint32_t s = len > 0 ? (uint32_t)q0 : n;
+      for (int k = 0; k < len && s < n; ++k)
+        s = (uint32_t)(int32_t)g.next[s * nc + min((uint32_t)g.classes[g.strings[at + k]], nc - 1)];
+      if (s < n) q = (int32_t)s;
+    }
+  }
+  out[r] = q;
+}
+
+// --------------------------------------------------------------------- logits
+
+constexpr int SH_THREADS = 256;
+constexpr int SH_VEC = 8;  // tokens of a thread: one byte of a token set
+constexpr int SH_TILE = 4096;
+
+// A vector that may start at any element.
+template <class T>
+struct Pack {
+  typedef T type __attribute__((ext_vector_type(SH_VEC), aligned(sizeof(T))));
+};
+
+template <class I, class O>
+__global__ __launch_bounds__(SH_THREADS) void k_shape(tt_shape_args a, int tiles) {
+  __shared__ uint32_t s_count[SH_TILE];  // times generated
+  __shared__ uint32_t s_bias[SH_TILE];   // 1 + the last bias entry that names the token
+  const int64_t r = blockIdx.x / tiles;
+  const uint32_t v0 = (uint32_t)(blockIdx.x % tiles) * SH_TILE;
+  const uint32_t here = (uint32_t)min((int64_t)SH_TILE, a.vocab - v0);
+  const int tid = threadIdx.x;
+  for (int i = tid; i < SH_TILE; i += SH_THREADS) s_count[i] = s_bias[i] = 0;
+  __syncthreads();
+  if (a.generated) {
+    const int64_t cap = a.generated_cap;
+    const int64_t n = a.n_generated ? min(max((int64_t)a.n_generated[r], (int64_t)0), cap) : cap;
+    const int32_t* gen = a.generated + r * a.generated_stride;
+    for (int64_t i = tid; i < n; i += SH_THREADS) {
+      const uint32_t at = (uint32_t)gen[i] - v0;
+      if (at < here) atomicAdd(&s_count[at], 1u);
+    }
+  }
+  int64_t b0 = 0;
+  if (a.bias_offsets) {
+    b0 = min(max(a.bias_offsets[r], (int64_t)0), a.n_bias);
+    const int64_t b1 = min(max(a.bias_offsets[r + 1], b0), a.n_bias);
+    for (int64_t i = b0 + tid; i < b1; i += SH_THREADS) {
+      const uint32_t at = (uint32_t)a.bias_ids[i] - v0;
+      if (at < here) atomicMax(&s_bias[at], (uint32_t)(i - b0) + 1u);
+    }
+  }
+  __syncthreads();
+  const float rho = a.repetition ? a.repetition[r] : 1.0f;
+  const float phi = a.frequency ? a.frequency[r] : 0.0f;
+  const float pi = a.presence ? a.presence[r] : 0.0f;
+  const float temp = a.temperature ? a.temperature[r] : 0.0f;
+  const uint8_t* seen = a.seen ? reinterpret_cast<const uint8_t*>(a.seen + r * a.seen_stride) : nullptr;
+  const uint8_t* allowed = nullptr;
+  bool none = false;  // nothing is allowed
+  if (a.allowed) {
+    const int64_t at = a.allowed_rows ? a.allowed_rows[r] : r;
+    none = at != TT_STATE_FREE && (at < 0 || at >= a.allowed_count);
+    if (at >= 0 && !none) allowed = reinterpret_cast<const uint8_t*>(a.allowed + at * a.allowed_stride);
+  }
+  const I* src = static_cast<const I*>(a.logits) + r * a.logits_stride + v0;
+  O* dst = static_cast<O*>(a.out) + r * a.out_stride + v0;
+  for (uint32_t i = tid * SH_VEC; i < here; i += SH_THREADS * SH_VEC) {
+    const bool whole = i + SH_VEC <= here;
+    typename Pack<I>::type x{};
+    if (whole) {
+      x = *reinterpret_cast<const typename Pack<I>::type*>(src + i);
+    } else {
+      for (uint32_t k = 0; k < here - i; ++k) x[k] = src[i + k];
+    }
+    const uint32_t sb = seen ? seen[(v0 + i) >> 3] : 0u;
+    const uint32_t ab = none ? 0u : allowed ? allowed[(v0 + i) >> 3] : 255u;
+    typename Pack<O>::type y;
+#pragma unroll
+    for (int k = 0; k < SH_VEC; ++k) {
+      float f = (float)x[k];
+      const uint32_t c = s_count[i + k], b = s_bias[i + k];
+      if (c || (sb >> k & 1)) f = f > 0.0f ? f / rho : f * rho;
+      if (c) f = f - phi * (float)c - pi;
+      if (b) f += a.bias_values[b0 + b - 1];
+      if (!(ab >> k & 1)) f = -__builtin_inff();
+      if (temp > 0.0f) f = f / temp;
+      y[k] = (O)f;
+    }
+    if (whole) {
+      *reinterpret_cast<typename Pack<O>::type*>(dst + i) = y;
+    } else {
+      for (uint32_t k = 0; k < here - i; ++k) dst[i + k] = y[k];
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_plan(const tt_plan_args& a, hipStream_t st) {
+  // at least 1,024 places for a workgroup, and at most 1,024 workgroups: each sums up all rows
+  int64_t per = div_up(div_up(a.places, 1024), BT_THREADS) * BT_THREADS;
+  if (per < 1024) per = 1024;
+  const int64_t grid = a.places > 0 ? div_up(a.places, per) : 1;
+  // lengths must outlive the reads of every workgroup: written by a launch of
+  // its own where several read what one would write over
+  const bool apart = grid > 1 && (a.out_lengths == a.lengths || a.out_n_free == a.n_free);
+  auto* k = a.offsets ? k_plan<false> : k_plan<true>;
+  hipLaunchKernelGGL(k, dim3((uint32_t)grid), dim3(BT_THREADS), 0, st, a, per, !apart);
+  if (apart) {
+    tt_plan_args f = a;  // no places to fill; the check of offsets against places has to stay
+    hipLaunchKernelGGL(k, dim3(1), dim3(BT_THREADS), 0, st, f, (int64_t)0, true);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_release(const ReleaseArgs& a, hipStream_t st) {
+  // 8,192 entries of the table for a workgroup, at most 512 workgroups
+  int64_t grid = a.rows * a.width / 8192 + 1;
+  if (grid > 512) grid = 512;
+  const bool apart = grid > 1 && (a.out_lengths == a.lengths || a.out_n_free == a.n_free);
+  hipLaunchKernelGGL(k_release, dim3((uint32_t)grid), dim3(BT_THREADS), 0, st, a, true, !apart);
+  if (apart) hipLaunchKernelGGL(k_release, dim3(1), dim3(BT_THREADS), 0, st, a, false, true);
+  return hipGetLastError();
+}
+
+hipError_t launch_token_bits(const int32_t* ids, int64_t n, const int64_t* offsets, int64_t rows, int64_t vocab,
+                             int32_t* bits, int64_t stride, bool add, hipStream_t st) {
+  const int64_t words = div_up(vocab, 32), tiles = div_up(words, TB_WORDS);
+  const size_t lds = (size_t)(words < TB_WORDS ? words : TB_WORDS) * 4;
+  hipLaunchKernelGGL(k_token_bits, dim3((uint32_t)(rows * tiles)), dim3(TB_THREADS), lds, st, ids, n, offsets, vocab,
+                     bits, stride, (int)tiles, add);
+  return hipGetLastError();
+}
+
+hipError_t launch_grammar_bits(const tt_grammar& g, const int32_t* states, int64_t rows, int32_t* bits,
+                               int64_t stride, int64_t vocab, hipStream_t st) {
+  const int64_t tiles = div_up(vocab, GR_THREADS);
+  hipLaunchKernelGGL(k_grammar_bits, dim3((uint32_t)(rows * tiles)), dim3(GR_THREADS), 0, st, g, states, vocab, bits,
+                     stride, (int)tiles);
+  return hipGetLastError();
+}
+
+hipError_t launch_grammar_advance(const tt_grammar& g, const int32_t* states, const int32_t* tokens, int64_t rows,
+                                  int32_t* out, hipStream_t st) {
+  hipLaunchKernelGGL(k_grammar_advance, dim3((uint32_t)div_up(rows, 64)), dim3(64), 0, st, g, states, tokens, rows,
+                     out);
+  return hipGetLastError();
+}
+
+hipError_t launch_shape(const tt_shape_args& a, hipStream_t st) {
+  const int64_t tiles = div_up(a.vocab, SH_TILE);
+  const dim3 grid((uint32_t)(a.rows * tiles)), block(SH_THREADS);
+  const int64_t kind = a.in_type * 4 + a.out_type;
+  void (*k)(tt_shape_args, int) = k_shape<float, float>;
+  if (kind == TT_F16 * 4 + TT_F16) k = k_shape<_Float16, _Float16>;
+  if (kind == TT_F16 * 4 + TT_F32) k = k_shape<_Float16, float>;
+  if (kind == TT_BF16 * 4 + TT_BF16) k = k_shape<__bf16, __bf16>;
+  if (kind == TT_BF16 * 4 + TT_F32) k = k_shape<__bf16, float>;
+  hipLaunchKernelGGL(k, grid, block, 0, st, a, (int)tiles);
+  return hipGetLastError();
+}
+
+}  // namespace tt
