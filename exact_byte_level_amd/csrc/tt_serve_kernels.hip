@@ -379,8 +379,9 @@ __global__ void k_grammar_advance(tt_grammar g, const int32_t* states, const int
 // --------------------------------------------------------------------- logits
 
 constexpr int SH_THREADS = 256;
-constexpr int SH_VEC = 8;  // tokens of a thread: one byte of a token set
-constexpr int SH_TILE = 4096;
+constexpr int SH_VEC = 8;    // tokens of a load: one byte of a token set
+constexpr int SH_BATCH = 8;  // generated tokens that a thread has on their way at a time
+constexpr int SH_WAVES = 6;  // a SIMD
 
 // A vector that may start at any element.
 template <class T>
@@ -388,77 +389,200 @@ struct Pack {
   typedef T type __attribute__((ext_vector_type(SH_VEC), aligned(sizeof(T))));
 };
 
-template <class I, class O>
-__global__ __launch_bounds__(SH_THREADS) void k_shape(tt_shape_args a, int tiles) {
-  __shared__ uint32_t s_count[SH_TILE];  // times generated
-  __shared__ uint32_t s_bias[SH_TILE];   // 1 + the last bias entry that names the token
+// Bit k of bits ? a : b, in two instructions.
+__device__ inline float pick(uint32_t bits, int k, float a, float b) {
+  const uint32_t m = (uint32_t)__builtin_amdgcn_sbfe((int)bits, k, 1);
+  return __uint_as_float((m & __float_as_uint(a)) | (~m & __float_as_uint(b)));
+}
+
+// A workgroup shapes one tile of a row: N * SH_VEC tokens a thread.  The
+// tile's logits and set bytes are loaded first; while they arrive the
+// generated tokens that fall into the tile are counted in LDS, each workgroup
+// of a row reading the whole (short) list.  A tile that a bias entry names then
+// uses the same words again to find each token's last entry; the others skip that.
+template <class I, class O, int N>
+__global__ __launch_bounds__(SH_THREADS, SH_WAVES) void k_shape(tt_shape_args a, int tiles) {
+  constexpr int TOKENS = SH_THREADS * SH_VEC * N;  // of a tile
+  __shared__ __attribute__((aligned(16))) uint32_t s_word[TOKENS];
+  __shared__ int s_hit[2];  // some entry names a token of the tile; some generated token is in it
   const int64_t r = blockIdx.x / tiles;
-  const uint32_t v0 = (uint32_t)(blockIdx.x % tiles) * SH_TILE;
-  const uint32_t here = (uint32_t)min((int64_t)SH_TILE, a.vocab - v0);
   const int tid = threadIdx.x;
-  for (int i = tid; i < SH_TILE; i += SH_THREADS) s_count[i] = s_bias[i] = 0;
-  __syncthreads();
-  if (a.generated) {
-    const int64_t cap = a.generated_cap;
-    const int64_t n = a.n_generated ? min(max((int64_t)a.n_generated[r], (int64_t)0), cap) : cap;
-    const int32_t* gen = a.generated + r * a.generated_stride;
-    for (int64_t i = tid; i < n; i += SH_THREADS) {
-      const uint32_t at = (uint32_t)gen[i] - v0;
-      if (at < here) atomicAdd(&s_count[at], 1u);
-    }
+  const uint32_t vocab = (uint32_t)a.vocab, v0 = blockIdx.x % tiles * (uint32_t)TOKENS;
+  const uint32_t here = min((uint32_t)TOKENS, vocab - v0);
+
+  // Vectors that would leave the row are loaded from its end and put right
+  // where they are used.  Without a set, bytes of the row itself are loaded in
+  // its place, which costs less than a branch.
+  typedef typename Pack<I>::type Vec;
+  const I* row = static_cast<const I*>(a.logits) + r * a.logits_stride;
+  const uint8_t* seen = a.seen ? reinterpret_cast<const uint8_t*>(a.seen + r * a.seen_stride)
+                               : reinterpret_cast<const uint8_t*>(row);
+  Vec x[N];
+  uint32_t sb[N], ab[N], byte[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t v = v0 + (uint32_t)(j * SH_THREADS + tid) * SH_VEC;
+    byte[j] = min(v, vocab - 1) >> 3;
+    x[j] = 0;
+    if (vocab >= SH_VEC) x[j] = *reinterpret_cast<const Vec*>(row + min(v, vocab - SH_VEC));
+    sb[j] = seen[byte[j]];
   }
-  int64_t b0 = 0;
-  if (a.bias_offsets) {
-    b0 = min(max(a.bias_offsets[r], (int64_t)0), a.n_bias);
-    const int64_t b1 = min(max(a.bias_offsets[r + 1], b0), a.n_bias);
-    for (int64_t i = b0 + tid; i < b1; i += SH_THREADS) {
-      const uint32_t at = (uint32_t)a.bias_ids[i] - v0;
-      if (at < here) atomicMax(&s_bias[at], (uint32_t)(i - b0) + 1u);
-    }
-  }
-  __syncthreads();
+  // the row's parameters: all loads before the first use, so that they wait once
+  const int64_t entry_at = a.bias_offsets ? a.bias_offsets[r] : 0, entry_to = a.bias_offsets ? a.bias_offsets[r + 1] : 0;
+  const int n_gen_at = a.n_generated ? a.n_generated[r] : 0x7FFFFFFF;
+  const int set = a.allowed_rows ? a.allowed_rows[r] : (int)r;
   const float rho = a.repetition ? a.repetition[r] : 1.0f;
   const float phi = a.frequency ? a.frequency[r] : 0.0f;
   const float pi = a.presence ? a.presence[r] : 0.0f;
   const float temp = a.temperature ? a.temperature[r] : 0.0f;
-  const uint8_t* seen = a.seen ? reinterpret_cast<const uint8_t*>(a.seen + r * a.seen_stride) : nullptr;
-  const uint8_t* allowed = nullptr;
-  bool none = false;  // nothing is allowed
-  if (a.allowed) {
-    const int64_t at = a.allowed_rows ? a.allowed_rows[r] : r;
-    none = at != TT_STATE_FREE && (at < 0 || at >= a.allowed_count);
-    if (at >= 0 && !none) allowed = reinterpret_cast<const uint8_t*>(a.allowed + at * a.allowed_stride);
+  const int n_gen = a.generated ? min(max(n_gen_at, 0), (int)a.generated_cap) : 0;
+  const int64_t b0 = min(max(entry_at, (int64_t)0), a.n_bias);
+  const int n_bias = (int)(min(max(entry_to, b0), a.n_bias) - b0);
+  const bool masked = a.allowed && set != TT_STATE_FREE;
+  const bool none = masked && (set < 0 || set >= a.allowed_count);  // nothing is allowed
+  const uint8_t* allowed = masked && !none ? reinterpret_cast<const uint8_t*>(a.allowed + set * a.allowed_stride)
+                                           : reinterpret_cast<const uint8_t*>(row);
+#pragma unroll
+  for (int j = 0; j < N; ++j) ab[j] = allowed[byte[j]];
+
+  // the first generated tokens and entries, on their way with the logits
+  const int32_t* gen = a.generated + r * a.generated_stride;
+  uint32_t ids[SH_BATCH], entry = 0;
+  auto take = [&](int base) {
+#pragma unroll
+    for (int k = 0; k < SH_BATCH; ++k) ids[k] = (uint32_t)gen[min(base + k * SH_THREADS + tid, n_gen - 1)];
+  };
+  if (n_gen > 0) take(0);
+  if (n_bias > 0) entry = (uint32_t)a.bias_ids[b0 + min(tid, n_bias - 1)];
+#pragma unroll
+  for (int j = 0; j < 2 * N; ++j) reinterpret_cast<uint4*>(s_word)[j * SH_THREADS + tid] = make_uint4(0, 0, 0, 0);
+  if (tid < 2) s_hit[tid] = 0;
+  __syncthreads();
+
+  for (int base = 0; base < n_gen; base += SH_BATCH * SH_THREADS) {
+    if (base) take(base);
+#pragma unroll
+    for (int k = 0; k < SH_BATCH; ++k)
+      if (base + k * SH_THREADS + tid < n_gen && ids[k] - v0 < here) {
+        atomicAdd(&s_word[ids[k] - v0], 1u);
+        s_hit[1] = 1;
+      }
   }
-  const I* src = static_cast<const I*>(a.logits) + r * a.logits_stride + v0;
-  O* dst = static_cast<O*>(a.out) + r * a.out_stride + v0;
-  for (uint32_t i = tid * SH_VEC; i < here; i += SH_THREADS * SH_VEC) {
-    const bool whole = i + SH_VEC <= here;
-    typename Pack<I>::type x{};
-    if (whole) {
-      x = *reinterpret_cast<const typename Pack<I>::type*>(src + i);
-    } else {
-      for (uint32_t k = 0; k < here - i; ++k) x[k] = src[i + k];
+  for (int i = tid; i < n_bias; i += SH_THREADS) {
+    if (i >= SH_THREADS) entry = (uint32_t)a.bias_ids[b0 + i];
+    if (entry - v0 < here) s_hit[0] = 1;
+  }
+  __syncthreads();
+  const bool biased = s_hit[0] != 0, counted = s_hit[1] != 0;
+  uint32_t n[N][SH_VEC];
+  float add[N][SH_VEC];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+    if (counted) {
+      const uint4* w = reinterpret_cast<const uint4*>(s_word) + 2 * (j * SH_THREADS + tid);
+      lo = w[0];
+      hi = w[1];
     }
-    const uint32_t sb = seen ? seen[(v0 + i) >> 3] : 0u;
-    const uint32_t ab = none ? 0u : allowed ? allowed[(v0 + i) >> 3] : 255u;
-    typename Pack<O>::type y;
+    n[j][0] = lo.x, n[j][1] = lo.y, n[j][2] = lo.z, n[j][3] = lo.w, n[j][4] = hi.x, n[j][5] = hi.y, n[j][6] = hi.z, n[j][7] = hi.w;
+#pragma unroll
+    for (int k = 0; k < SH_VEC; ++k) add[j][k] = 0.0f;
+  }
+  if (biased) {  // the words again, now for the last entry that names each token
+#pragma unroll
+    for (int j = 0; j < 2 * N; ++j) reinterpret_cast<uint4*>(s_word)[2 * N * tid + j] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for (int i = tid; i < n_bias; i += SH_THREADS) {
+      const uint32_t t = (uint32_t)a.bias_ids[b0 + i] - v0;
+      if (t < here) atomicMax(&s_word[t], (uint32_t)i + 1u);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int k = 0; k < SH_VEC; ++k) {
+        const uint32_t w = s_word[(j * SH_THREADS + tid) * SH_VEC + k];
+        if (w) add[j][k] = a.bias_values[b0 + w - 1];
+      }
+  }
+
+  // x / rho and x / temperature as products with the reciprocal, which is at
+  // most one step of 32 bits off instead of half a one.  Where the result
+  // stays in 32 bits the quotient by rho, which is not the last operation, is put
+  // right by its remainder, as a division does.  Where a reciprocal is not an
+  // ordinary number both are divisions.
+  const float inv_rho = 1.0f / rho, inv_temp = 1.0f / temp;
+  const bool plain_rho = !(fabsf(rho) >= 0x1p-100f && fabsf(rho) <= 0x1p100f);
+  const bool plain_temp = temp > 0.0f && !(temp >= 0x1p-100f && temp <= 0x1p100f);
+  const float scale = temp > 0.0f && !plain_temp ? inv_temp : 1.0f;
+  O* dst = static_cast<O*>(a.out) + r * a.out_stride + v0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const uint32_t i = (uint32_t)(j * SH_THREADS + tid) * SH_VEC;
+    if (here < TOKENS && i + SH_VEC > here) {
+#pragma unroll
+      for (int k = 0; k < SH_VEC; ++k)
+        if (i + k < here) x[j][k] = row[v0 + i + k];
+    }
+    uint32_t was = a.seen ? sb[j] : 0u;
+    const uint32_t may = none ? 0u : masked ? ab[j] : 255u;
+    float f[SH_VEC];
+    uint32_t some = 0;
 #pragma unroll
     for (int k = 0; k < SH_VEC; ++k) {
-      float f = (float)x[k];
-      const uint32_t c = s_count[i + k], b = s_bias[i + k];
-      if (c || (sb >> k & 1)) f = f > 0.0f ? f / rho : f * rho;
-      if (c) f = f - phi * (float)c - pi;
-      if (b) f += a.bias_values[b0 + b - 1];
-      if (!(ab >> k & 1)) f = -__builtin_inff();
-      if (temp > 0.0f) f = f / temp;
-      y[k] = (O)f;
+      f[k] = (float)x[j][k];
+      some |= (n[j][k] != 0) << k;
     }
-    if (whole) {
+    was |= some;
+    if (was && !plain_rho) {
+#pragma unroll
+      for (int k = 0; k < SH_VEC; ++k) {
+        float q = f[k] * inv_rho;
+        if (sizeof(O) == 4) {
+          const float fixed = fmaf(fmaf(-q, rho, f[k]), inv_rho, q);
+          q = fabsf(q) < __builtin_inff() ? fixed : q;  // an infinity has no remainder
+        }
+        f[k] = pick(was, k, f[k] > 0.0f ? q : f[k] * rho, f[k]);
+      }
+    }
+    if (was && plain_rho) {
+#pragma unroll
+      for (int k = 0; k < SH_VEC; ++k) f[k] = pick(was, k, f[k] > 0.0f ? f[k] / rho : f[k] * rho, f[k]);
+    }
+    if (some) {
+#pragma unroll
+      for (int k = 0; k < SH_VEC; ++k)
+        if (n[j][k]) f[k] = f[k] - phi * (float)n[j][k] - pi;
+    }
+    typename Pack<O>::type y;
+#pragma unroll
+    for (int k = 0; k < SH_VEC; ++k) f[k] += add[j][k];
+    if (plain_temp) {
+#pragma unroll
+      for (int k = 0; k < SH_VEC; ++k) f[k] /= temp;
+    }
+#pragma unroll
+    for (int k = 0; k < SH_VEC; ++k) {
+      f[k] *= scale;
+      y[k] = (O)pick(may, k, f[k], -__builtin_inff());
+    }
+    if (i + SH_VEC <= here) {
       *reinterpret_cast<typename Pack<O>::type*>(dst + i) = y;
     } else {
-      for (uint32_t k = 0; k < here - i; ++k) dst[i + k] = y[k];
+#pragma unroll
+      for (int k = 0; k < SH_VEC; ++k)
+        if (i + k < here) dst[i + k] = y[k];
     }
   }
+}
+
+template <class I, class O>
+void enqueue_shape(const tt_shape_args& a, hipStream_t st) {
+  const int64_t small = div_up(a.vocab, SH_THREADS * SH_VEC), large = div_up(a.vocab, SH_THREADS * SH_VEC * 2);
+  if (a.rows * large >= 1024)
+    hipLaunchKernelGGL((k_shape<I, O, 2>), dim3((uint32_t)(a.rows * large)), dim3(SH_THREADS), 0, st, a, (int)large);
+  else
+    hipLaunchKernelGGL((k_shape<I, O, 1>), dim3((uint32_t)(a.rows * small)), dim3(SH_THREADS), 0, st, a, (int)small);
 }
 
 }  // namespace
@@ -515,15 +639,12 @@ hipError_t launch_grammar_advance(const tt_grammar& g, const int32_t* states, co
 }
 
 hipError_t launch_shape(const tt_shape_args& a, hipStream_t st) {
-  const int64_t tiles = div_up(a.vocab, SH_TILE);
-  const dim3 grid((uint32_t)(a.rows * tiles)), block(SH_THREADS);
-  const int64_t kind = a.in_type * 4 + a.out_type;
-  void (*k)(tt_shape_args, int) = k_shape<float, float>;
-  if (kind == TT_F16 * 4 + TT_F16) k = k_shape<_Float16, _Float16>;
-  if (kind == TT_F16 * 4 + TT_F32) k = k_shape<_Float16, float>;
-  if (kind == TT_BF16 * 4 + TT_BF16) k = k_shape<__bf16, __bf16>;
-  if (kind == TT_BF16 * 4 + TT_F32) k = k_shape<__bf16, float>;
-  hipLaunchKernelGGL(k, grid, block, 0, st, a, (int)tiles);
+  const bool wide = a.out_type == TT_F32;
+  if (a.in_type == TT_F32) enqueue_shape<float, float>(a, st);
+  else if (a.in_type == TT_F16 && wide) enqueue_shape<_Float16, float>(a, st);
+  else if (a.in_type == TT_F16) enqueue_shape<_Float16, _Float16>(a, st);
+  else if (wide) enqueue_shape<__bf16, float>(a, st);
+  else enqueue_shape<__bf16, __bf16>(a, st);
   return hipGetLastError();
 }
 
