@@ -2,6 +2,8 @@
 // shaping of logits (declared in include/tt_serve.h).
 #include "tt_serve_kernels.h"
 
+#include <type_traits>
+
 namespace tt {
 namespace {
 
@@ -378,10 +380,8 @@ __global__ void k_grammar_advance(tt_grammar g, const int32_t* states, const int
 
 // --------------------------------------------------------------------- logits
 
-constexpr int SH_THREADS = 256;
 constexpr int SH_VEC = 8;    // tokens of a load: one byte of a token set
 constexpr int SH_BATCH = 8;  // generated tokens that a thread has on their way at a time
-constexpr int SH_WAVES = 6;  // a SIMD
 
 // A vector that may start at any element.
 template <class T>
@@ -389,10 +389,19 @@ struct Pack {
   typedef T type __attribute__((ext_vector_type(SH_VEC), aligned(sizeof(T))));
 };
 
-// Bit k of bits ? a : b, in two instructions.
+// Bit k of bits ? a : b, in two instructions (written as a select it becomes four).
 __device__ inline float pick(uint32_t bits, int k, float a, float b) {
-  const uint32_t m = (uint32_t)__builtin_amdgcn_sbfe((int)bits, k, 1);
-  return __uint_as_float((m & __float_as_uint(a)) | (~m & __float_as_uint(b)));
+  const int m = __builtin_amdgcn_sbfe((int)bits, k, 1);
+  float d;
+  asm("v_bfi_b32 %0, %1, %2, %3" : "=v"(d) : "v"(m), "v"(a), "v"(b));
+  return d;
+}
+
+// Element i of a row, by a 32-bit offset (rows are shorter than 2^32 bytes).
+template <class T>
+__device__ inline T* from(T* row, uint32_t i) {
+  typedef typename std::conditional<std::is_const<T>::value, const char, char>::type Byte;
+  return reinterpret_cast<T*>(reinterpret_cast<Byte*>(row) + (uint32_t)(i * sizeof(T)));
 }
 
 // A workgroup shapes one tile of a row: N * SH_VEC tokens a thread.  The
@@ -400,9 +409,9 @@ __device__ inline float pick(uint32_t bits, int k, float a, float b) {
 // generated tokens that fall into the tile are counted in LDS, each workgroup
 // of a row reading the whole (short) list.  A tile that a bias entry names then
 // uses the same words again to find each token's last entry; the others skip that.
-template <class I, class O, int N>
-__global__ __launch_bounds__(SH_THREADS, SH_WAVES) void k_shape(tt_shape_args a, int tiles) {
-  constexpr int TOKENS = SH_THREADS * SH_VEC * N;  // of a tile
+template <class I, class O, int T, int N>
+__global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles) {
+  constexpr int TOKENS = T * SH_VEC * N;  // of a tile
   __shared__ __attribute__((aligned(16))) uint32_t s_word[TOKENS];
   __shared__ int s_hit[2];  // some entry names a token of the tile; some generated token is in it
   const int64_t r = blockIdx.x / tiles;
@@ -421,10 +430,10 @@ __global__ __launch_bounds__(SH_THREADS, SH_WAVES) void k_shape(tt_shape_args a,
   uint32_t sb[N], ab[N], byte[N];
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const uint32_t v = v0 + (uint32_t)(j * SH_THREADS + tid) * SH_VEC;
+    const uint32_t v = v0 + (uint32_t)(j * T + tid) * SH_VEC;
     byte[j] = min(v, vocab - 1) >> 3;
     x[j] = 0;
-    if (vocab >= SH_VEC) x[j] = *reinterpret_cast<const Vec*>(row + min(v, vocab - SH_VEC));
+    if (vocab >= SH_VEC) x[j] = *reinterpret_cast<const Vec*>(from(row, min(v, vocab - SH_VEC)));
     sb[j] = seen[byte[j]];
   }
   // the row's parameters: all loads before the first use, so that they wait once
@@ -447,30 +456,31 @@ __global__ __launch_bounds__(SH_THREADS, SH_WAVES) void k_shape(tt_shape_args a,
 
   // the first generated tokens and entries, on their way with the logits
   const int32_t* gen = a.generated + r * a.generated_stride;
-  uint32_t ids[SH_BATCH], entry = 0;
+  uint32_t ids[SH_BATCH], first = 0;
   auto take = [&](int base) {
 #pragma unroll
-    for (int k = 0; k < SH_BATCH; ++k) ids[k] = (uint32_t)gen[min(base + k * SH_THREADS + tid, n_gen - 1)];
+    for (int k = 0; k < SH_BATCH; ++k)
+      if (base + k * T < n_gen) ids[k] = (uint32_t)gen[min(base + k * T + tid, n_gen - 1)];
   };
   if (n_gen > 0) take(0);
-  if (n_bias > 0) entry = (uint32_t)a.bias_ids[b0 + min(tid, n_bias - 1)];
+  if (n_bias > 0) first = (uint32_t)a.bias_ids[b0 + min(tid, n_bias - 1)];
 #pragma unroll
-  for (int j = 0; j < 2 * N; ++j) reinterpret_cast<uint4*>(s_word)[j * SH_THREADS + tid] = make_uint4(0, 0, 0, 0);
+  for (int j = 0; j < 2 * N; ++j) reinterpret_cast<uint4*>(s_word)[j * T + tid] = make_uint4(0, 0, 0, 0);
   if (tid < 2) s_hit[tid] = 0;
   __syncthreads();
 
-  for (int base = 0; base < n_gen; base += SH_BATCH * SH_THREADS) {
+  for (int base = 0; base < n_gen; base += SH_BATCH * T) {
     if (base) take(base);
 #pragma unroll
     for (int k = 0; k < SH_BATCH; ++k)
-      if (base + k * SH_THREADS + tid < n_gen && ids[k] - v0 < here) {
+      if (base + k * T < n_gen && base + k * T + tid < n_gen && ids[k] - v0 < here) {
         atomicAdd(&s_word[ids[k] - v0], 1u);
         s_hit[1] = 1;
       }
   }
-  for (int i = tid; i < n_bias; i += SH_THREADS) {
-    if (i >= SH_THREADS) entry = (uint32_t)a.bias_ids[b0 + i];
-    if (entry - v0 < here) s_hit[0] = 1;
+  for (int i = tid; i < n_bias; i += T) {
+    const uint32_t t = (i < T ? first : (uint32_t)a.bias_ids[b0 + i]) - v0;
+    if (t < here) s_hit[0] = 1;
   }
   __syncthreads();
   const bool biased = s_hit[0] != 0, counted = s_hit[1] != 0;
@@ -480,7 +490,7 @@ __global__ __launch_bounds__(SH_THREADS, SH_WAVES) void k_shape(tt_shape_args a,
   for (int j = 0; j < N; ++j) {
     uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
     if (counted) {
-      const uint4* w = reinterpret_cast<const uint4*>(s_word) + 2 * (j * SH_THREADS + tid);
+      const uint4* w = reinterpret_cast<const uint4*>(s_word) + 2 * (j * T + tid);
       lo = w[0];
       hi = w[1];
     }
@@ -492,8 +502,8 @@ __global__ __launch_bounds__(SH_THREADS, SH_WAVES) void k_shape(tt_shape_args a,
 #pragma unroll
     for (int j = 0; j < 2 * N; ++j) reinterpret_cast<uint4*>(s_word)[2 * N * tid + j] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    for (int i = tid; i < n_bias; i += SH_THREADS) {
-      const uint32_t t = (uint32_t)a.bias_ids[b0 + i] - v0;
+    for (int i = tid; i < n_bias; i += T) {
+      const uint32_t t = (i < T ? first : (uint32_t)a.bias_ids[b0 + i]) - v0;
       if (t < here) atomicMax(&s_word[t], (uint32_t)i + 1u);
     }
     __syncthreads();
@@ -501,7 +511,7 @@ __global__ __launch_bounds__(SH_THREADS, SH_WAVES) void k_shape(tt_shape_args a,
     for (int j = 0; j < N; ++j)
 #pragma unroll
       for (int k = 0; k < SH_VEC; ++k) {
-        const uint32_t w = s_word[(j * SH_THREADS + tid) * SH_VEC + k];
+        const uint32_t w = s_word[(j * T + tid) * SH_VEC + k];
         if (w) add[j][k] = a.bias_values[b0 + w - 1];
       }
   }
@@ -515,34 +525,38 @@ __global__ __launch_bounds__(SH_THREADS, SH_WAVES) void k_shape(tt_shape_args a,
   const bool plain_rho = !(fabsf(rho) >= 0x1p-100f && fabsf(rho) <= 0x1p100f);
   const bool plain_temp = temp > 0.0f && !(temp >= 0x1p-100f && temp <= 0x1p100f);
   const float scale = temp > 0.0f && !plain_temp ? inv_temp : 1.0f;
+  const float lowest = -__builtin_inff();
   O* dst = static_cast<O*>(a.out) + r * a.out_stride + v0;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    const uint32_t i = (uint32_t)(j * SH_THREADS + tid) * SH_VEC;
+    const uint32_t i = (uint32_t)(j * T + tid) * SH_VEC;
     if (here < TOKENS && i + SH_VEC > here) {
 #pragma unroll
       for (int k = 0; k < SH_VEC; ++k)
-        if (i + k < here) x[j][k] = row[v0 + i + k];
+        if (i + k < here) x[j][k] = *from(row, v0 + i + k);
     }
     uint32_t was = a.seen ? sb[j] : 0u;
     const uint32_t may = none ? 0u : masked ? ab[j] : 255u;
     float f[SH_VEC];
-    uint32_t some = 0;
 #pragma unroll
-    for (int k = 0; k < SH_VEC; ++k) {
-      f[k] = (float)x[j][k];
-      some |= (n[j][k] != 0) << k;
+    for (int k = 0; k < SH_VEC; ++k) f[k] = (float)x[j][k];
+    const uint32_t* c = n[j];
+    const bool some = (c[0] | c[1] | c[2] | c[3] | c[4] | c[5] | c[6] | c[7]) != 0;
+    if (some) {
+#pragma unroll
+      for (int k = 0; k < SH_VEC; ++k) was |= (c[k] != 0) << k;
     }
-    was |= some;
     if (was && !plain_rho) {
 #pragma unroll
       for (int k = 0; k < SH_VEC; ++k) {
-        float q = f[k] * inv_rho;
         if (sizeof(O) == 4) {
+          float q = f[k] * inv_rho;
           const float fixed = fmaf(fmaf(-q, rho, f[k]), inv_rho, q);
           q = fabsf(q) < __builtin_inff() ? fixed : q;  // an infinity has no remainder
+          f[k] = pick(was, k, f[k] > 0.0f ? q : f[k] * rho, f[k]);
+        } else {
+          f[k] = pick(was, k, f[k] * (f[k] > 0.0f ? inv_rho : rho), f[k]);
         }
-        f[k] = pick(was, k, f[k] > 0.0f ? q : f[k] * rho, f[k]);
       }
     }
     if (was && plain_rho) {
@@ -552,37 +566,43 @@ __global__ __launch_bounds__(SH_THREADS, SH_WAVES) void k_shape(tt_shape_args a,
     if (some) {
 #pragma unroll
       for (int k = 0; k < SH_VEC; ++k)
-        if (n[j][k]) f[k] = f[k] - phi * (float)n[j][k] - pi;
+        if (c[k]) f[k] = f[k] - phi * (float)c[k] - pi;
     }
-    typename Pack<O>::type y;
+    if (biased) {
 #pragma unroll
-    for (int k = 0; k < SH_VEC; ++k) f[k] += add[j][k];
+      for (int k = 0; k < SH_VEC; ++k) f[k] += add[j][k];
+    }
     if (plain_temp) {
 #pragma unroll
       for (int k = 0; k < SH_VEC; ++k) f[k] /= temp;
     }
+    typename Pack<O>::type y;
 #pragma unroll
-    for (int k = 0; k < SH_VEC; ++k) {
-      f[k] *= scale;
-      y[k] = (O)pick(may, k, f[k], -__builtin_inff());
-    }
+    for (int k = 0; k < SH_VEC; ++k) y[k] = (O)pick(may, k, f[k] * scale, lowest);
     if (i + SH_VEC <= here) {
-      *reinterpret_cast<typename Pack<O>::type*>(dst + i) = y;
+      *reinterpret_cast<typename Pack<O>::type*>(from(dst, i)) = y;
     } else {
 #pragma unroll
       for (int k = 0; k < SH_VEC; ++k)
-        if (i + k < here) dst[i + k] = y[k];
+        if (i + k < here) *from(dst, i + k) = y[k];
     }
   }
 }
 
+template <class I, class O, int T, int N>
+void enqueue_tiles(const tt_shape_args& a, hipStream_t st) {
+  const int64_t tiles = div_up(a.vocab, T * SH_VEC * N);
+  hipLaunchKernelGGL((k_shape<I, O, T, N>), dim3((uint32_t)(a.rows * tiles)), dim3(T), 0, st, a, (int)tiles);
+}
+
+// Tiles of 4,096 tokens once they fill the card, since every tile reads the
+// list of generated tokens: 250 rows of 260,003 bfloat16 with lists of up to
+// 16,000 take 85 us, with tiles of 2,048 110 us.  Fewer go by 2,048, which
+// spreads a row over twice the CUs: one row of 50,256 takes 4.4 us.
 template <class I, class O>
 void enqueue_shape(const tt_shape_args& a, hipStream_t st) {
-  const int64_t small = div_up(a.vocab, SH_THREADS * SH_VEC), large = div_up(a.vocab, SH_THREADS * SH_VEC * 2);
-  if (a.rows * large >= 1024)
-    hipLaunchKernelGGL((k_shape<I, O, 2>), dim3((uint32_t)(a.rows * large)), dim3(SH_THREADS), 0, st, a, (int)large);
-  else
-    hipLaunchKernelGGL((k_shape<I, O, 1>), dim3((uint32_t)(a.rows * small)), dim3(SH_THREADS), 0, st, a, (int)small);
+  if (a.rows * div_up(a.vocab, 4096) >= 1024) enqueue_tiles<I, O, 256, 2>(a, st);
+  else enqueue_tiles<I, O, 256, 1>(a, st);
 }
 
 }  // namespace
