@@ -356,6 +356,88 @@ __global__ __launch_bounds__(GR_THREADS) void k_grammar_bits(tt_grammar g, const
   if (lane % 32 == 0 && word < div_up(vocab, 32)) bits[r * stride + word] = (int32_t)(uint32_t)(m >> lane);
 }
 
+// The sets of many states at a time.  A workgroup takes 1,024 tokens and a
+// part of the states: each thread keeps the byte classes of its token in
+// registers, the automaton lies in LDS, and the states go by four at a time, so
+// that the first steps of four walks are on their way together.  Most walks of a
+// grammar end there, and a wavefront whose 64 tokens are all dead goes on to the
+// next state.  Lane i keeps the 64 bits of the i-th of 64 states, so that they are
+// written by one store.
+constexpr int GM_THREADS = 1024;
+constexpr int GM_ROWS = 4;    // states whose first steps go together
+constexpr int GM_KEEP = 16;   // bytes of a token that are kept as classes
+constexpr int GM_LDS = 144 * 1024;  // of the automaton, at most
+constexpr int GM_MIN_ROWS = 32;
+
+// The state after the bytes K .. GM_KEEP - 1 of each lane's token.
+template <int K>
+__device__ inline uint32_t walk(const int16_t* next, uint32_t n, uint32_t nc, const uint32_t (&c)[GM_KEEP / 4], int len,
+                                uint32_t s) {
+  if constexpr (K < GM_KEEP) {
+    const bool on = K < len && s < n;
+    if (!__any(on)) return s;
+    if (on) s = (uint32_t)(int32_t)next[s * nc + (c[K / 4] >> (8 * (K % 4)) & 255)];
+    return walk<K + 1>(next, n, nc, c, len, s);
+  }
+  return s;
+}
+
+__global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const int32_t* states, int64_t rows,
+                                                             int64_t vocab, int32_t* bits, int64_t stride, int tiles,
+                                                             int64_t per_block) {
+  extern __shared__ __attribute__((aligned(16))) int16_t s_next[];
+  __shared__ uint8_t cls[256];
+  const int tid = threadIdx.x, lane = tid % WAVE;
+  const uint32_t n = (uint32_t)g.n_states, nc = (uint32_t)g.n_classes;
+  for (int i = tid; i < 256; i += GM_THREADS) cls[i] = (uint8_t)min((int)g.classes[i], (int)nc - 1);
+  for (uint32_t i = tid; i < n * nc; i += GM_THREADS) s_next[i] = g.next[i];
+  __syncthreads();
+  const int64_t v = (int64_t)(blockIdx.x % tiles) * GM_THREADS + tid;
+  const int64_t r0 = blockIdx.x / tiles * per_block, r1 = min(r0 + per_block, rows);
+  const bool is_end = v == g.end_id && v < vocab;
+  int64_t at = 0;
+  int len = 0;
+  if (v < g.n_tokens && v < vocab && !is_end) token_span(g, v, at, len);
+  uint32_t c[GM_KEEP / 4] = {};
+#pragma unroll
+  for (int k = 0; k < GM_KEEP; ++k)
+    if (k < len) c[k / 4] |= (uint32_t)cls[g.strings[at + k]] << (8 * (k % 4));
+  const uint64_t below = __ballot(v < vocab);  // the bits that are tokens
+  const int64_t word = (v - lane) / 32, words = div_up(vocab, 32);
+  const bool two = word + 1 < words;
+  if (word >= words) return;
+
+  for (int64_t r = r0; r < r1; r += WAVE) {
+    const int count = (int)min((int64_t)WAVE, r1 - r);
+    const int32_t q_lane = lane < count ? states[r + lane] : TT_STATE_DEAD;
+    uint64_t mine = 0;
+    for (int j = 0; j < count; j += GM_ROWS) {
+      uint32_t q[GM_ROWS];
+      int32_t q0[GM_ROWS];
+#pragma unroll
+      for (int i = 0; i < GM_ROWS; ++i) {
+        q0[i] = __builtin_amdgcn_readlane(q_lane, j + i);  // j + i < 64: lanes past count hold the dead state
+        q[i] = n;
+        if (len > 0 && (uint32_t)q0[i] < n) q[i] = (uint32_t)(int32_t)s_next[(uint32_t)q0[i] * nc + (c[0] & 255)];
+      }
+#pragma unroll
+      for (int i = 0; i < GM_ROWS; ++i) {
+        uint32_t s = walk<1>(s_next, n, nc, c, len, q[i]);
+        for (int k = GM_KEEP; k < len && s < n; ++k) s = (uint32_t)(int32_t)s_next[s * nc + cls[g.strings[at + k]]];
+        bool ok = s < n;
+        if (is_end) ok = (uint32_t)q0[i] < n && g.accept[q0[i]] != 0;
+        const uint64_t m = q0[i] == TT_STATE_FREE ? below : __ballot(ok);
+        if (lane == j + i) mine = m;
+      }
+    }
+    if (lane < count) {
+      int32_t* out = bits + (r + lane) * stride + word;
+      out[0] = (int32_t)(uint32_t)mine;
+      if (two) out[1] = (int32_t)(uint32_t)(mine >> 32);
+    }
+  }
+}
+
 __global__ void k_grammar_advance(tt_grammar g, const int32_t* states, const int32_t* tokens, int64_t rows,
                                   int32_t* out) {
   const int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -645,6 +727,17 @@ hipError_t launch_token_bits(const int32_t* ids, int64_t n, const int64_t* offse
 
 hipError_t launch_grammar_bits(const tt_grammar& g, const int32_t* states, int64_t rows, int32_t* bits,
                                int64_t stride, int64_t vocab, hipStream_t st) {
+  const int64_t table = 2 * g.n_states * g.n_classes;
+  if (rows >= GM_MIN_ROWS && table <= GM_LDS) {
+    // two workgroups for a CU, each with 64 states at least
+    const int64_t tiles = div_up(vocab, GM_THREADS);
+    int64_t parts = div_up((int64_t)512, tiles);
+    if (parts > div_up(rows, WAVE)) parts = div_up(rows, WAVE);
+    const int64_t per = div_up(div_up(rows, parts), WAVE) * WAVE;
+    hipLaunchKernelGGL(k_grammar_many, dim3((uint32_t)(tiles * div_up(rows, per))), dim3(GM_THREADS), (size_t)table, st,
+                       g, states, rows, vocab, bits, stride, (int)tiles, per);
+    return hipGetLastError();
+  }
   const int64_t tiles = div_up(vocab, GR_THREADS);
   hipLaunchKernelGGL(k_grammar_bits, dim3((uint32_t)(rows * tiles)), dim3(GR_THREADS), 0, st, g, states, vocab, bits,
                      stride, (int)tiles);
