@@ -356,84 +356,184 @@ __global__ __launch_bounds__(GR_THREADS) void k_grammar_bits(tt_grammar g, const
   if (lane % 32 == 0 && word < div_up(vocab, 32)) bits[r * stride + word] = (int32_t)(uint32_t)(m >> lane);
 }
 
-// The sets of many states at a time.  A workgroup takes 1,024 tokens and a
-// part of the states: each thread keeps the byte classes of its token in
-// registers, the automaton lies in LDS, and the states go by four at a time, so
-// that the first steps of four walks are on their way together.  Most walks of a
-// grammar end there, and a wavefront whose 64 tokens are all dead goes on to the
-// next state.  Lane i keeps the 64 bits of the i-th of 64 states, so that they are
-// written by one store.
+// The sets of many states at a time.  A workgroup takes 2,048 tokens, puts them
+// in order of the class of their first byte, and keeps the byte classes of two
+// tokens in each thread's registers, so that the 64 tokens of a wavefront mostly
+// start alike.  Then, 64 states at a time, one lane tries the first byte
+// for each state: only the states that live on are walked with the 64 tokens, and
+// in most states of a grammar few first bytes are possible.  A token whose
+// further bytes all lead from a state back to it (the inside of a text) is
+// done after one look at two sets of classes.
 constexpr int GM_THREADS = 1024;
-constexpr int GM_ROWS = 4;    // states whose first steps go together
-constexpr int GM_KEEP = 16;   // bytes of a token that are kept as classes
-constexpr int GM_LDS = 144 * 1024;  // of the automaton, at most
-constexpr int GM_MIN_ROWS = 32;
+constexpr int GM_CHUNKS = 2;                       // tokens of a thread
+constexpr int GM_TOKENS = GM_THREADS * GM_CHUNKS;  // of a workgroup
+constexpr int GM_KEEP = 16;                        // bytes of a token that are kept as classes
+constexpr int GM_LDS = 112 * 1024;  // of the automaton, at most; beyond, it is read from L2
+
+typedef uint32_t Bytes16 __attribute__((ext_vector_type(4)));
+typedef uint32_t Bytes16Any __attribute__((ext_vector_type(4), aligned(1)));  // at any address
+
+// A token as its thread keeps it.
+struct KeptToken {
+  uint32_t c[GM_KEEP / 4];  // classes of its first bytes
+  uint64_t later;           // set of the classes of all bytes but the first, if there are at most 64 classes
+  int at, len;              // its bytes; len 0: none or not to be walked
+  int place;                // in the workgroup's tokens
+};
 
 // The state after the bytes K .. GM_KEEP - 1 of each lane's token.
 template <int K>
-__device__ inline uint32_t walk(const int16_t* next, uint32_t n, uint32_t nc, const uint32_t (&c)[GM_KEEP / 4], int len,
-                                uint32_t s) {
+__device__ inline uint32_t walk(const int16_t* next, uint32_t n, uint32_t nc, const KeptToken& t, uint32_t s, bool go) {
   if constexpr (K < GM_KEEP) {
-    const bool on = K < len && s < n;
+    const bool on = go && K < t.len && s < n;
     if (!__any(on)) return s;
-    if (on) s = (uint32_t)(int32_t)next[s * nc + (c[K / 4] >> (8 * (K % 4)) & 255)];
-    return walk<K + 1>(next, n, nc, c, len, s);
+    if (on) s = (uint32_t)(int32_t)next[s * nc + (t.c[K / 4] >> (8 * (K % 4)) & 255)];
+    return walk<K + 1>(next, n, nc, t, s, go);
   }
   return s;
 }
 
+template <bool IN_LDS>
 __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const int32_t* states, int64_t rows,
                                                              int64_t vocab, int32_t* bits, int64_t stride, int tiles,
                                                              int64_t per_block) {
-  extern __shared__ __attribute__((aligned(16))) int16_t s_next[];
+  extern __shared__ __attribute__((aligned(16))) uint64_t s_self[];  // [n] classes that lead from a state to itself
+  __shared__ uint32_t s_bits[WAVE][GM_TOKENS / 32];  // sets of the 64 states at hand; first, the tokens' order
   __shared__ uint8_t cls[256];
+  __shared__ uint32_t s_first[257];  // tokens by the class of their first byte
   const int tid = threadIdx.x, lane = tid % WAVE;
   const uint32_t n = (uint32_t)g.n_states, nc = (uint32_t)g.n_classes;
+  const bool sets = nc <= 64;
+  int16_t* s_next = reinterpret_cast<int16_t*>(s_self + (sets ? (n + 1) / 2 * 2 : 0));
+  const int16_t* next = IN_LDS ? s_next : g.next;
+  // the tokens in order of their first class; those that are not walked are left out
+  const int64_t v0 = (int64_t)(blockIdx.x % tiles) * GM_TOKENS;
+  uint16_t* order = reinterpret_cast<uint16_t*>(&s_bits[0][0]);
+  int first[GM_CHUNKS], nth[GM_CHUNKS];
+#pragma unroll
+  for (int j = 0; j < GM_CHUNKS; ++j) {
+    const int64_t v = v0 + j * GM_THREADS + tid;
+    int64_t at = 0;
+    int len = 0;
+    if (v < g.n_tokens && v < vocab && v != g.end_id) token_span(g, v, at, len);
+    first[j] = len > 0 ? g.strings[at] : -1;
+  }
   for (int i = tid; i < 256; i += GM_THREADS) cls[i] = (uint8_t)min((int)g.classes[i], (int)nc - 1);
-  for (uint32_t i = tid; i < n * nc; i += GM_THREADS) s_next[i] = g.next[i];
+  if (tid < 257) s_first[tid] = 0;
+  if (IN_LDS) {
+    const uint32_t whole = n * nc / 8;
+#pragma unroll 4
+    for (uint32_t i = tid; i < whole; i += GM_THREADS)
+      reinterpret_cast<Bytes16*>(s_next)[i] = reinterpret_cast<const Bytes16Any*>(g.next)[i];
+    for (uint32_t i = 8 * whole + tid; i < n * nc; i += GM_THREADS) s_next[i] = g.next[i];
+  }
   __syncthreads();
-  const int64_t v = (int64_t)(blockIdx.x % tiles) * GM_THREADS + tid;
-  const int64_t r0 = blockIdx.x / tiles * per_block, r1 = min(r0 + per_block, rows);
-  const bool is_end = v == g.end_id && v < vocab;
-  int64_t at = 0;
-  int len = 0;
-  if (v < g.n_tokens && v < vocab && !is_end) token_span(g, v, at, len);
-  uint32_t c[GM_KEEP / 4] = {};
 #pragma unroll
-  for (int k = 0; k < GM_KEEP; ++k)
-    if (k < len) c[k / 4] |= (uint32_t)cls[g.strings[at + k]] << (8 * (k % 4));
-  const uint64_t below = __ballot(v < vocab);  // the bits that are tokens
-  const int64_t word = (v - lane) / 32, words = div_up(vocab, 32);
-  const bool two = word + 1 < words;
-  if (word >= words) return;
-
-  for (int64_t r = r0; r < r1; r += WAVE) {
-    const int count = (int)min((int64_t)WAVE, r1 - r);
-    const int32_t q_lane = lane < count ? states[r + lane] : TT_STATE_DEAD;
-    uint64_t mine = 0;
-    for (int j = 0; j < count; j += GM_ROWS) {
-      uint32_t q[GM_ROWS];
-      int32_t q0[GM_ROWS];
+  for (int j = 0; j < GM_CHUNKS; ++j)
+    if (first[j] >= 0) {
+      first[j] = cls[first[j]];
+      nth[j] = (int)atomicAdd(&s_first[first[j] + 1], 1u);
+    }
+  if (sets)
+    for (uint32_t q = tid; q < n; q += GM_THREADS) {
+      uint64_t m = 0;
+      for (uint32_t k = 0; k < nc; ++k) m |= (uint64_t)((uint32_t)(int32_t)next[q * nc + k] == q) << k;
+      s_self[q] = m;
+    }
+  __syncthreads();
+  if (tid < WAVE) {  // inclusive sums of 256 counts by one wavefront, four to a lane
+    uint32_t c[4], sum = 0;
 #pragma unroll
-      for (int i = 0; i < GM_ROWS; ++i) {
-        q0[i] = __builtin_amdgcn_readlane(q_lane, j + i);  // j + i < 64: lanes past count hold the dead state
-        q[i] = n;
-        if (len > 0 && (uint32_t)q0[i] < n) q[i] = (uint32_t)(int32_t)s_next[(uint32_t)q0[i] * nc + (c[0] & 255)];
-      }
+    for (int k = 0; k < 4; ++k) c[k] = sum += s_first[1 + 4 * lane + k];
+    uint32_t inc = sum;
+    for (int d = 1; d < WAVE; d <<= 1) {
+      const uint32_t o = (uint32_t)__shfl_up((int)inc, d);
+      if (lane >= d) inc += o;
+    }
 #pragma unroll
-      for (int i = 0; i < GM_ROWS; ++i) {
-        uint32_t s = walk<1>(s_next, n, nc, c, len, q[i]);
-        for (int k = GM_KEEP; k < len && s < n; ++k) s = (uint32_t)(int32_t)s_next[s * nc + cls[g.strings[at + k]]];
-        bool ok = s < n;
-        if (is_end) ok = (uint32_t)q0[i] < n && g.accept[q0[i]] != 0;
-        const uint64_t m = q0[i] == TT_STATE_FREE ? below : __ballot(ok);
-        if (lane == j + i) mine = m;
+    for (int k = 0; k < 4; ++k) s_first[1 + 4 * lane + k] = inc - sum + c[k];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < GM_CHUNKS; ++j)
+    if (first[j] >= 0) order[s_first[first[j]] + nth[j]] = (uint16_t)(j * GM_THREADS + tid);
+  __syncthreads();
+  const int walked = (int)s_first[256];
+  KeptToken t[GM_CHUNKS];
+#pragma unroll
+  for (int j = 0; j < GM_CHUNKS; ++j) {
+    // a wavefront's chunks are 16 apart, so that all wavefronts share the long runs of one class
+    const int i = (j * (GM_THREADS / WAVE) + tid / WAVE) * WAVE + lane;
+    t[j] = KeptToken{};
+    if (i < walked) {
+      t[j].place = order[i];
+      int64_t at;
+      token_span(g, v0 + t[j].place, at, t[j].len);
+      t[j].at = (int)at;
+    }
+    Bytes16 b = 0;
+    if (t[j].len > 0) {
+      if (t[j].at + GM_KEEP <= g.n_bytes) {
+        b = *reinterpret_cast<const Bytes16Any*>(g.strings + t[j].at);
+      } else {  // at the end of the strings
+        for (int k = 0; k < min(t[j].len, GM_KEEP); ++k) b[k / 4] |= (uint32_t)g.strings[t[j].at + k] << (8 * (k % 4));
       }
     }
-    if (lane < count) {
-      int32_t* out = bits + (r + lane) * stride + word;
-      out[0] = (int32_t)(uint32_t)mine;
-      if (two) out[1] = (int32_t)(uint32_t)(mine >> 32);
+#pragma unroll
+    for (int k = 0; k < GM_KEEP; ++k) {
+      if (!__any(k < t[j].len)) continue;
+      const uint32_t c = cls[b[k / 4] >> (8 * (k % 4)) & 255];
+      t[j].c[k / 4] |= c << (8 * (k % 4));
+      if (k && k < t[j].len) t[j].later |= 1ull << (c & 63);
+    }
+    for (int k = GM_KEEP; k < t[j].len; ++k) t[j].later |= 1ull << (cls[g.strings[t[j].at + k]] & 63);
+  }
+
+  const int64_t r0 = blockIdx.x / tiles * per_block, r1 = min(r0 + per_block, rows);
+  const int64_t word0 = v0 / 32, words = min(div_up(vocab, 32) - word0, (int64_t)(GM_TOKENS / 32));
+  const int end = g.end_id >= v0 && g.end_id < min(v0 + GM_TOKENS, vocab) ? (int)(g.end_id - v0) : -1;
+  for (int64_t r = r0; r < r1; r += WAVE) {
+    const int count = (int)min((int64_t)WAVE, r1 - r);
+    __syncthreads();  // the order is read, or the sets before are written
+    for (int i = tid; i < WAVE * GM_TOKENS / 32; i += GM_THREADS) (&s_bits[0][0])[i] = 0;
+    __syncthreads();
+    const int32_t q_lane = lane < count ? states[r + lane] : TT_STATE_DEAD;
+    const bool good = (uint32_t)q_lane < n;
+    const uint64_t free = __ballot(q_lane == TT_STATE_FREE);
+#pragma unroll
+    for (int j = 0; j < GM_CHUNKS; ++j) {
+      // the states that some token's first byte leaves alive
+      uint64_t live = 0, left = __ballot(t[j].len > 0);
+      while (left) {
+        const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)(t[j].c[0] & 255), __builtin_ctzll(left));
+        live |= __ballot(good && (uint32_t)(int32_t)next[(good ? (uint32_t)q_lane : 0) * nc + c] < n);
+        left &= ~__ballot((t[j].c[0] & 255) == c);
+      }
+      while (live) {
+        const int i = __builtin_ctzll(live);
+        live &= live - 1;
+        const uint32_t q0 = (uint32_t)__builtin_amdgcn_readlane(q_lane, i);
+        uint32_t q = n;
+        if (t[j].len > 0) q = (uint32_t)(int32_t)next[q0 * nc + (t[j].c[0] & 255)];
+        bool go = q < n && t[j].len > 1;
+        if (sets && go && (t[j].later & ~s_self[q]) == 0) go = false;  // every further byte stays in it
+        q = walk<1>(next, n, nc, t[j], q, go);
+        for (int k = GM_KEEP; go && k < t[j].len && q < n; ++k)
+          q = (uint32_t)(int32_t)next[q * nc + cls[g.strings[t[j].at + k]]];
+        if (q < n) atomicOr(&s_bits[i][t[j].place >> 5], 1u << (t[j].place & 31));
+      }
+    }
+    if (end >= 0 && tid < count && good && g.accept[q_lane]) atomicOr(&s_bits[tid][end >> 5], 1u << (end & 31));
+    __syncthreads();
+    for (int i = tid; i < count * (GM_TOKENS / 32); i += GM_THREADS) {
+      const int row = i / (GM_TOKENS / 32), w = i % (GM_TOKENS / 32);
+      if (w >= words) continue;
+      uint32_t out = s_bits[row][w];
+      if (free >> row & 1) {
+        const int64_t rest = vocab - (word0 + w) * 32;
+        out = rest >= 32 ? 0xFFFFFFFFu : (1u << rest) - 1u;
+      }
+      bits[(r + row) * stride + word0 + w] = (int32_t)out;
     }
   }
 }
@@ -727,16 +827,19 @@ hipError_t launch_token_bits(const int32_t* ids, int64_t n, const int64_t* offse
 
 hipError_t launch_grammar_bits(const tt_grammar& g, const int32_t* states, int64_t rows, int32_t* bits,
                                int64_t stride, int64_t vocab, hipStream_t st) {
-  const int64_t table = 2 * g.n_states * g.n_classes;
-  if (rows >= GM_MIN_ROWS && table <= GM_LDS) {
-    // two workgroups for a CU, each with 64 states at least
-    const int64_t tiles = div_up(vocab, GM_THREADS);
-    int64_t parts = div_up((int64_t)512, tiles);
-    if (parts > div_up(rows, WAVE)) parts = div_up(rows, WAVE);
-    const int64_t per = div_up(div_up(rows, parts), WAVE) * WAVE;
-    hipLaunchKernelGGL(k_grammar_many, dim3((uint32_t)(tiles * div_up(rows, per))), dim3(GM_THREADS), (size_t)table, st,
-                       g, states, rows, vocab, bits, stride, (int)tiles, per);
-    return hipGetLastError();
+  if (rows >= WAVE) {
+    // a workgroup for every CU, each with 64 states at least
+    const int64_t tiles = div_up(vocab, GM_TOKENS);
+    const int64_t parts = min(div_up(rows, WAVE), max((int64_t)1, (int64_t)256 / tiles)), per = div_up(rows, parts);
+    const int64_t table = 2 * g.n_states * g.n_classes, self = g.n_classes <= 64 ? (g.n_states + 1) / 2 * 16 : 0;
+    const dim3 grid((uint32_t)(tiles * div_up(rows, per))), block(GM_THREADS);
+    if (table + self <= GM_LDS)
+      hipLaunchKernelGGL(k_grammar_many<true>, grid, block, (size_t)(table + self), st, g, states, rows, vocab, bits,
+                         stride, (int)tiles, per);
+    else if (self <= GM_LDS)
+      hipLaunchKernelGGL(k_grammar_many<false>, grid, block, (size_t)self, st, g, states, rows, vocab, bits, stride,
+                         (int)tiles, per);
+    if (self <= GM_LDS) return hipGetLastError();
   }
   const int64_t tiles = div_up(vocab, GR_THREADS);
   hipLaunchKernelGGL(k_grammar_bits, dim3((uint32_t)(rows * tiles)), dim3(GR_THREADS), 0, st, g, states, vocab, bits,

@@ -114,8 +114,9 @@ def random_strings(rng, n, longest):
 @pytest.mark.parametrize("states, classes, density, tokens, longest, vocab, rows, pad", [
     (1, 1, 1.0, 1, 3, 1, 1, 0), (2, 3, 0.8, 40, 6, 45, 4, 1), (300, 40, 0.9, 500, 20, 500, 33, 0),
     (30, 256, 0.7, 1000, 9, 1025, 7, 0), (5, 4, 0.5, 70, 0, 70, 3, 0), (4, 5, 0.97, 300, 300, 300, 5, 2),
-    (2000, 200, 0.95, 200, 40, 64, 64, 0), (700, 90, 0.9, 3000, 12, 3001, 100, 0), (32767, 3, 0.9, 100, 9, 100, 50, 0),
-    (12, 20, 1.0, 0, 0, 40, 3, 0)])
+    (2000, 200, 0.95, 200, 40, 64, 64, 0), (700, 90, 0.9, 3000, 12, 3001, 100, 0), (32767, 3, 0.9, 100, 9, 100, 50, 0), (32767, 3, 0.9, 100, 9, 100, 70, 0), (300, 40, 0.9, 500, 20, 500, 130, 0),
+    (12, 20, 1.0, 0, 0, 40, 3, 0), (12, 20, 1.0, 0, 0, 40, 64, 0), (3000, 50, 0.9, 700, 20, 700, 70, 0),
+    (60, 20, 0.97, 5000, 24, 5001, 65, 1), (64, 64, 0.9, 5000, 6, 4097, 64, 0), (65, 65, 0.9, 300, 6, 290, 65, 0)])
 def test_grammar_bits_and_advance(states, classes, density, tokens, longest, vocab, rows, pad):
     rng = np.random.default_rng(states + tokens)
     nxt, accept = random_grammar(rng, states, classes, density)
