@@ -38,7 +38,8 @@ def room(rows, words, pad, fill=0x5A5A5A5A):
 @pytest.mark.parametrize("add", [False, True])
 @pytest.mark.parametrize("rows, n, vocab, pad", [
     (1, 0, 40, 0), (1, 1, 1, 0), (1, 5000, 33, 2), (3, 100, 31, 1), (7, 3000, 32, 0), (64, 20000, 1000, 0),
-    (5, 400, 100_257, 3), (2, 300_000, 50_256, 0), (300, 9000, 5000, 0), (1, 700_000, 600_001, 0), (2, 5000, 1_200_000, 1)])
+    (5, 400, 100_257, 3), (2, 300_000, 50_256, 0), (300, 9000, 5000, 0), (1, 700_000, 600_001, 0), (2, 5000, 1_200_000, 1),
+    (1, 65_536, 5000, 0), (1500, 100_000, 20_000, 0), (3, 90_001, 1_200_000, 0), (12, 150_000, 60_000, 0), (5, 200_000, 33, 1), (2500, 70_000, 3000, 2)])
 def test_token_bits(rows, n, vocab, pad, add):
     rng = np.random.default_rng(rows * 7 + n)
     ids = np.minimum((rng.random(n) ** 3 * vocab).astype(np.int32), vocab - 1)
@@ -53,6 +54,21 @@ def test_token_bits(rows, n, vocab, pad, add):
     assert (wide[:, so.words(vocab):] == 0x5A5A5A5A).all()
 
 
+def test_token_bits_of_many_long_texts():
+    """More texts than a workgroup looks at in one go, long enough to be dealt out."""
+    rng = np.random.default_rng(1)
+    rows, n, vocab = 1030, 12_700_000, 70
+    ids = rng.integers(-1, vocab + 1, n).astype(np.int32)
+    cuts = np.sort(rng.integers(0, n, rows - 1))
+    cuts[5:300] = cuts[5]  # empty texts, and after them one of many ids
+    offsets = np.concatenate([[0], cuts, [n]]).astype(np.int64)
+    offsets[400] = offsets[399] + 1
+    member = np.zeros((rows, vocab), bool)
+    fine = (ids >= 0) & (ids < vocab)
+    member[(np.searchsorted(offsets, np.arange(n), side="right") - 1)[fine], ids[fine]] = True
+    assert np.array_equal(tt.token_bits(dev(ids), vocab, offsets=dev(offsets)).cpu().numpy(), so.pack(member))
+
+
 def test_token_bits_of_one_text_without_offsets():
     ids = np.arange(0, 900, 7, dtype=np.int32)
     got = tt.token_bits(dev(ids), 900)
@@ -65,6 +81,10 @@ def test_token_bits_bounds_are_kept():
     offsets = np.array([-5, 10, 4, 70, 2**62, -2**62, 64], np.int64)
     got = tt.token_bits(dev(ids), 64, offsets=dev(offsets))
     assert np.array_equal(got.cpu().numpy(), so.token_bits(ids, offsets, 64))
+    ids = np.arange(70_000, dtype=np.int32)
+    offsets = np.array([-5, 10_000, 4000, 71_000, 2**62, -2**62, 64], np.int64)
+    got = tt.token_bits(dev(ids), 65_000, offsets=dev(offsets))
+    assert np.array_equal(got.cpu().numpy(), so.token_bits(ids, offsets, 65_000))
 
 
 def test_token_bits_of_a_batch_call():
