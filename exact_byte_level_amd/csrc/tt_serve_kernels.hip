@@ -16,6 +16,8 @@ __host__ __device__ inline uint32_t div_up32(uint32_t a, uint32_t b) { return a 
 
 constexpr int BT_THREADS = 256;
 constexpr int BT_WAVES = BT_THREADS / WAVE;
+constexpr int BT_MANY = 4;                       // rows, places or blocks of a thread that are on their way together
+constexpr int BT_PART = BT_THREADS * BT_MANY;    // rows, places or blocks of a workgroup at a time
 
 // Data errors, as bits; the lowest one set is reported.
 constexpr uint32_t BAD_OFFSETS = 1, BAD_FREE = 2, BAD_SIZE = 4, BAD_NONE_LEFT = 8;
@@ -27,263 +29,344 @@ __device__ inline int64_t fault_code(uint32_t bad) {
   return TT_ENOBLOCKS;
 }
 
-__device__ inline int64_t wave_sum(int64_t v) {
-  for (int d = WAVE / 2; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+// v plus what the lanes `CTRL` says (of the rows of 16 in ROWS) hold of it.
+template <int CTRL, int ROWS>
+__device__ inline uint32_t plus_lanes(uint32_t v) {
+  return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
 }
 
-// Sums of K values over the workgroup (in every thread), and the union of bits.
+// Inclusive sums over the lanes of a row of 16, and of a wavefront: lane
+// shifts by 1, 2, 4, 8, then the last lanes of rows 0 and 2, then of row 1.
+__device__ inline uint32_t row_sums(uint32_t v) {
+  v = plus_lanes<0x111, 0xf>(v);
+  v = plus_lanes<0x112, 0xf>(v);
+  v = plus_lanes<0x114, 0xf>(v);
+  return plus_lanes<0x118, 0xf>(v);
+}
+__device__ inline uint32_t wave_sums(uint32_t v) {
+  return plus_lanes<0x143, 0xc>(plus_lanes<0x142, 0xa>(row_sums(v)));
+}
+
+// Inclusive sums of K values over the workgroup (modulo 2^32), with their totals.
 template <int K>
-__device__ inline void block_sums(int64_t (&v)[K], uint32_t& bits, int64_t* lds) {
-  for (int d = WAVE / 2; d > 0; d >>= 1) bits |= (uint32_t)__shfl_xor((int)bits, d);
-  const int w = threadIdx.x / WAVE;
-#pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
-  if (threadIdx.x % WAVE == 0) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) lds[w * (K + 1) + k] = v[k];
-    lds[w * (K + 1) + K] = (int64_t)bits;
-  }
-  __syncthreads();
-  bits = 0;
-#pragma unroll
-  for (int k = 0; k < K; ++k) v[k] = 0;
-  for (int i = 0; i < BT_WAVES; ++i) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] += lds[i * (K + 1) + k];
-    bits |= (uint32_t)lds[i * (K + 1) + K];
-  }
-  __syncthreads();
-}
-
-// Exclusive sum of v over the workgroup; *total receives the sum.
-__device__ inline uint32_t block_exclusive(uint32_t v, uint32_t* total, uint32_t* lds) {
+__device__ inline void block_sums(uint32_t (&v)[K], uint32_t (&total)[K], uint32_t (*lds)[BT_WAVES]) {
+  static_assert(BT_WAVES <= 16, "the wavefronts' totals fit a row of lanes");
   const int lane = threadIdx.x % WAVE, w = threadIdx.x / WAVE;
-  uint32_t inc = v;
-  for (int d = 1; d < WAVE; d <<= 1) {
-    const uint32_t o = (uint32_t)__shfl_up((int)inc, d);
-    if (lane >= d) inc += o;
-  }
-  if (lane == WAVE - 1) lds[w] = inc;
-  __syncthreads();
-  uint32_t before = 0, all = 0;
-  for (int i = 0; i < BT_WAVES; ++i) {
-    if (i < w) before += lds[i];
-    all += lds[i];
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = wave_sums(v[k]);
+  if (lane == WAVE - 1) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) lds[k][w] = v[k];
   }
   __syncthreads();
-  *total = all;
-  return before + inc - v;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const uint32_t all = row_sums(lane < BT_WAVES ? lds[k][lane] : 0);
+    total[k] = (uint32_t)__builtin_amdgcn_readlane((int)all, BT_WAVES - 1);
+    const int before = __builtin_amdgcn_readfirstlane(w) - 1;
+    v[k] += before >= 0 ? (uint32_t)__builtin_amdgcn_readlane((int)all, max(before, 0)) : 0;
+  }
 }
 
-// One row of a plan: where its new tokens start, how many they are, the
-// blocks it has and the ones it needs.
+// Sums of blocks, which may pass 32 bits, go as two: of 22 bits each, and of
+// the rest, up to 2^40 (more than any free list has) from a thread.
+constexpr int LOW = 22;
+static_assert(BT_THREADS << LOW <= 1u << 31 && (int64_t)BT_THREADS << (40 - LOW) <= 1u << 31, "both sums fit 32 bits");
+__device__ inline int64_t capped(int64_t v) { return min(v, (int64_t)1 << 40); }
+__device__ inline uint32_t low(int64_t v) { return (uint32_t)v & ((1u << LOW) - 1); }
+__device__ inline uint32_t high(int64_t v) { return (uint32_t)(v >> LOW); }
+__device__ inline int64_t joined(uint32_t lo, uint32_t hi) { return (int64_t)lo + ((int64_t)hi << LOW); }
+
+// For each t: the last of ROWS rows that starts at or before it.
+template <int ROWS>
+__device__ inline void last_rows(const uint32_t* start, const uint32_t (&t)[BT_MANY], int (&row)[BT_MANY]) {
+#pragma unroll
+  for (int k = 0; k < BT_MANY; ++k) row[k] = 0;
+#pragma unroll
+  for (int d = ROWS / 2; d > 0; d >>= 1)
+#pragma unroll
+    for (int k = 0; k < BT_MANY; ++k)
+      if (start[row[k] + d] <= t[k]) row[k] += d;
+}
+
+// One row of a plan: as given, where its new tokens start, how many they
+// are, the blocks it has and the ones it needs.
 struct RowPlan {
-  int32_t length;  // as given
+  int32_t length;
+  int64_t from, upto;  // its places
   uint32_t start, held, need;
   int64_t count;
 };
 
-__device__ inline RowPlan row_plan(const tt_plan_args& a, int64_t r, uint32_t& bad) {
+template <bool SINGLE>
+__device__ inline RowPlan row_loads(const tt_plan_args& a, int64_t r) {
   RowPlan p;
   p.length = a.lengths[r];
+  p.from = SINGLE ? r : a.offsets[r];
+  p.upto = SINGLE ? r + 1 : a.offsets[r + 1];
+  return p;
+}
+
+template <bool SINGLE>
+__device__ inline void row_plan(const tt_plan_args& a, RowPlan& p, uint32_t& bad) {
   const int64_t start = p.length > 0 ? p.length : 0;
-  p.count = p.length >= 0;
-  if (a.offsets) {
-    p.count = a.offsets[r + 1] - a.offsets[r];
-    if (p.count < 0) {
-      bad |= BAD_OFFSETS;
-      p.count = 0;
-    }
-  }
+  p.count = SINGLE ? p.length >= 0 : p.upto - p.from;
   p.start = (uint32_t)start;
   p.held = p.need = 0;
+  if (p.count < 0) {
+    bad |= BAD_OFFSETS;
+    p.count = 0;
+  }
   const int64_t room = a.width * a.block_size - start;  // width * block_size < 2^31
   if (p.count > room) {
     bad |= BAD_SIZE;
     p.count = 0;
-    return p;
+    return;
   }
   const uint32_t bs = (uint32_t)a.block_size;
   p.held = div_up32(p.start, bs);
   p.need = div_up32(p.start + (uint32_t)p.count, bs) - p.held;
-  return p;
+}
+
+__device__ inline void put_place(const tt_plan_args& a, int64_t t, int64_t slot, int32_t position, int32_t row) {
+  a.slots[t] = slot;
+  if (a.positions) a.positions[t] = position;
+  if (a.row_of) a.row_of[t] = row;
 }
 
 // Every workgroup sums up all rows by itself (a few KB from L2), so that one
-// launch is enough: no workgroup waits for another one's sums.
-// Bytes bound it: 16 written for a token.
+// launch is enough and no workgroup waits for another one's sums; up to 1,024
+// rows a thread reads its row once.  The 16 bytes written for a token bound it.
+// `finisher`: the workgroup that writes the lengths and counts; it may be one without places.
 template <bool SINGLE>
-__global__ __launch_bounds__(BT_THREADS) void k_plan(tt_plan_args a, int64_t per_block, bool finish) {
-  __shared__ int64_t sums[BT_WAVES * 5];
-  __shared__ uint32_t scan[BT_WAVES];
-  __shared__ int32_t s_off[BT_THREADS + 1];
-  __shared__ uint32_t s_start[BT_THREADS], s_held[BT_THREADS], s_base[BT_THREADS];
+__global__ __launch_bounds__(BT_THREADS) void k_plan(tt_plan_args a, int64_t per_block, int finisher) {
+  __shared__ uint32_t s_sums[2][5][BT_WAVES];
+  __shared__ uint32_t s_bad;
+  __shared__ uint32_t s_off[BT_THREADS + 1], s_start[BT_THREADS], s_held[BT_THREADS], s_base[BT_THREADS];
   const int tid = threadIdx.x;
   const int64_t t0 = min((int64_t)blockIdx.x * per_block, a.places);
   const int64_t t1 = min(t0 + per_block, a.places);
+  const bool few = a.rows <= BT_THREADS;
+  const int64_t n_free = *a.n_free, last = SINGLE ? a.rows : a.offsets[a.rows], first = SINGLE ? 0 : a.offsets[0];
+  if (tid == 0) s_bad = 0;
   // all blocks needed; those of the rows that end at or before t0, and how many rows that are; tokens
-  int64_t v[4] = {0, 0, 0, 0};
-  uint32_t bad = 0;
-  for (int64_t r = tid; r < a.rows; r += BT_THREADS) {
-    const RowPlan p = row_plan(a, r, bad);
-    const bool before = (SINGLE ? r + 1 : a.offsets[r + 1]) <= t0;
-    v[0] += p.need;
-    v[1] += before ? p.need : 0;
-    v[2] += before;
-    v[3] += p.count;
+  int64_t all = 0;
+  uint32_t before = 0, rows_before = 0, count = 0, bad = 0, unused = 0;
+  RowPlan mine{-1, 0, 0, 0, 0, 0, 0};
+  for (int64_t base = 0; base < a.rows; base += BT_PART) {
+    RowPlan p[BT_MANY];
+#pragma unroll
+    for (int k = 0; k < BT_MANY; ++k)
+      if (base + k * BT_THREADS < a.rows) p[k] = row_loads<SINGLE>(a, min(base + k * BT_THREADS + tid, a.rows - 1));
+#pragma unroll
+    for (int k = 0; k < BT_MANY; ++k)
+      if (base + k * BT_THREADS + tid < a.rows) {
+        row_plan<SINGLE>(a, p[k], bad);
+        const bool past = p[k].upto <= t0;
+        all += p[k].need;
+        before += past ? p[k].need : 0;
+        rows_before += past;
+        count += (uint32_t)p[k].count;
+        mine = p[k];  // the only one, of few rows
+      }
   }
-  const int64_t n_free = *a.n_free;
-  if (!SINGLE) {
-    if (a.offsets[0] != 0) bad |= BAD_OFFSETS;
-    if (a.offsets[a.rows] > a.places) bad |= BAD_SIZE;
-  }
+  if (first != 0) bad |= BAD_OFFSETS;
+  if (last > a.places) bad |= BAD_SIZE;
   if (n_free < 0 || n_free > a.free_cap) bad |= BAD_FREE;
-  block_sums(v, bad, sums);
-  if (v[0] > n_free) bad |= BAD_NONE_LEFT;
-  const int64_t total = bad ? 0 : (SINGLE ? a.rows : v[3]);  // places that may hold a token
+  __syncthreads();
+  if (bad) atomicOr(&s_bad, bad);
+  all = capped(all);
+  uint32_t v[5] = {low(all), high(all), before, rows_before, count}, total[5];
+  block_sums(v, total, s_sums[1]);
+  bad = s_bad;
+  const int64_t needed = joined(total[0], total[1]), tokens = SINGLE ? (int64_t)total[4] : last;
+  if (needed > n_free) bad |= BAD_NONE_LEFT;
+  const int64_t end = min(t1, bad ? 0 : last);  // of the places that may hold a token
   const uint32_t bs = (uint32_t)a.block_size;
-  const int64_t end = min(t1, total);
-  uint32_t carry = (uint32_t)v[1];
-  for (int64_t c0 = v[2]; t0 < end && c0 < a.rows; c0 += BT_THREADS) {
+  uint32_t carry = few ? 0 : total[2];
+  int turn = 0;
+  for (int64_t c0 = few ? 0 : total[3]; t0 < end && c0 < a.rows; c0 += BT_THREADS, ++turn) {
     const int64_t r = c0 + tid;
-    RowPlan p{-1, 0, 0, 0, 0};
-    if (r < a.rows) p = row_plan(a, r, bad);
-    uint32_t chunk;
-    const uint32_t base = carry + block_exclusive(p.need, &chunk, scan);
-    carry += chunk;
+    RowPlan p{-1, 0, 0, 0, 0, 0, 0};
+    uint32_t base;
+    if (few) {  // a thread has had one row: its sum is there
+      p = mine;
+      base = (uint32_t)joined(v[0], v[1]) - p.need;
+    } else {
+      if (r < a.rows) {
+        p = row_loads<SINGLE>(a, r);
+        row_plan<SINGLE>(a, p, unused);
+      }
+      uint32_t s[1] = {p.need}, chunk[1];
+      block_sums(s, chunk, s_sums[turn & 1]);
+      base = carry + s[0] - p.need;
+      carry += chunk[0];
+    }
+    if (SINGLE) {  // place r is row r's
+      if (r >= t0 && r < end) {
+        const uint32_t blk = p.start / bs, in = p.start - blk * bs;
+        int32_t id = -1;
+        if (p.need) a.table[r * a.table_stride + blk] = id = a.free_blocks[n_free - 1 - (int64_t)base];
+        else if (p.length >= 0) id = a.table[r * a.table_stride + blk];
+        const bool live = p.length >= 0;
+        put_place(a, r, live && id >= 0 ? (int64_t)id * bs + in : -1, live ? (int32_t)p.start : -1, live ? (int32_t)r : -1);
+      }
+      if (c0 + BT_THREADS >= end) break;
+      continue;
+    }
+    s_off[tid] = (uint32_t)(r < a.rows ? p.from : last);
+    if (tid == BT_THREADS - 1) s_off[BT_THREADS] = (uint32_t)(r < a.rows ? p.upto : last);
     s_start[tid] = p.start;
     s_held[tid] = p.held;
     s_base[tid] = base;
-    if (!SINGLE) {
-      s_off[tid] = (int32_t)a.offsets[min(r, a.rows)];
-      if (tid == 0) s_off[BT_THREADS] = (int32_t)a.offsets[min(c0 + BT_THREADS, a.rows)];
-    } else {
-      s_off[tid] = p.length;
-    }
     __syncthreads();
-    const int64_t lo = SINGLE ? max(t0, c0) : max(t0, (int64_t)s_off[0]);
-    const int64_t hi = min(end, SINGLE ? c0 + BT_THREADS : (int64_t)s_off[BT_THREADS]);
-    int i = 0;
-    for (int64_t t = lo + tid; t < hi; t += BT_THREADS) {
-      uint32_t place;
-      if (SINGLE) {
-        i = (int)(t - c0);
-        place = s_start[i];
-      } else {
-        if (s_off[i + 1] <= t) {  // the last row that starts at or before t
-          int b = BT_THREADS;
-          while (b - i > 1) {
-            const int m = (i + b) >> 1;
-            if (s_off[m] <= t) i = m;
-            else b = m;
-          }
-        }
-        place = s_start[i] + (uint32_t)(t - s_off[i]);
+    const uint32_t lo = max((uint32_t)t0, s_off[0]), hi = min((uint32_t)end, s_off[BT_THREADS]);
+    for (uint32_t t = lo; t < hi; t += BT_PART) {
+      uint32_t at[BT_MANY], in[BT_MANY];
+      int i[BT_MANY];
+      int32_t id[BT_MANY];
+#pragma unroll
+      for (int k = 0; k < BT_MANY; ++k) at[k] = min(t + k * BT_THREADS + tid, hi - 1);
+      last_rows<BT_THREADS>(s_off, at, i);
+      int32_t* entry[BT_MANY];  // of a new block that starts here
+#pragma unroll
+      for (int k = 0; k < BT_MANY; ++k) {
+        const uint32_t place = s_start[i[k]] + (at[k] - s_off[i[k]]), blk = place / bs, held = s_held[i[k]];
+        in[k] = place - blk * bs;
+        int32_t* own = a.table + (c0 + i[k]) * a.table_stride + blk;
+        const int32_t* from = blk >= held ? a.free_blocks + (n_free - 1 - (int64_t)(s_base[i[k]] + (blk - held))) : own;
+        id[k] = *from;
+        entry[k] = blk >= held && in[k] == 0 ? own : nullptr;
       }
-      const int64_t row = c0 + i;
-      const uint32_t blk = place / bs, in = place - blk * bs, held = s_held[i];
-      int64_t slot = -1;
-      const bool live = !SINGLE || s_off[i] >= 0;
-      if (live) {
-        int32_t id;
-        if (blk >= held) {
-          id = a.free_blocks[n_free - 1 - (int64_t)(s_base[i] + (blk - held))];
-          if (in == 0) a.table[row * a.table_stride + blk] = id;
-        } else {
-          id = a.table[row * a.table_stride + blk];
-        }
-        if (id >= 0) slot = (int64_t)id * bs + in;
+#pragma unroll
+      for (int k = 0; k < BT_MANY; ++k) {
+        if (t + k * BT_THREADS + tid >= hi) break;
+        if (entry[k]) *entry[k] = id[k];
+        put_place(a, at[k], id[k] >= 0 ? (int64_t)id[k] * bs + in[k] : -1,
+                  (int32_t)(s_start[i[k]] + (at[k] - s_off[i[k]])), (int32_t)(c0 + i[k]));
       }
-      a.slots[t] = slot;
-      if (a.positions) a.positions[t] = live ? (int32_t)place : -1;
-      if (a.row_of) a.row_of[t] = live ? (int32_t)row : -1;
     }
     if (hi >= end) break;
     __syncthreads();
   }
-  for (int64_t t = max(t0, total) + tid; t < t1; t += BT_THREADS) {
-    a.slots[t] = -1;
-    if (a.positions) a.positions[t] = -1;
-    if (a.row_of) a.row_of[t] = -1;
-  }
-  if (!finish || blockIdx.x != 0) return;
-  __syncthreads();  // out_lengths may be lengths
-  uint32_t unused = 0;
+  for (int64_t t = max(t0, bad ? 0 : last) + tid; t < t1; t += BT_THREADS) put_place(a, t, -1, -1, -1);
+  if ((int)blockIdx.x != finisher) return;
+  __syncthreads();  // out_lengths may be lengths, which every thread has read by now
   for (int64_t r = tid; r < a.rows; r += BT_THREADS) {
-    const RowPlan p = row_plan(a, r, unused);
-    a.out_lengths[r] = bad || p.count == 0 ? p.length : (int32_t)(p.start + (uint32_t)p.count);
+    if (!few) {
+      mine = row_loads<SINGLE>(a, r);
+      row_plan<SINGLE>(a, mine, unused);
+    }
+    a.out_lengths[r] = bad || mine.count == 0 ? mine.length : (int32_t)(mine.start + (uint32_t)mine.count);
   }
   if (tid == 0) {
-    *a.out_n_free = (int32_t)(bad ? n_free : n_free - v[0]);
-    *a.out_n = bad ? fault_code(bad) : v[3];
+    *a.out_n_free = (int32_t)(bad ? n_free : n_free - needed);
+    *a.out_n = bad ? fault_code(bad) : tokens;
   }
 }
 
-// The blocks that row r gives back.
-__device__ inline uint32_t row_release(const ReleaseArgs& a, int64_t r, uint32_t& bad) {
-  const int32_t length = a.lengths[r];
-  if (!a.done[r] || length < 0) return 0;
-  const uint32_t m = div_up32((uint32_t)length, (uint32_t)a.block_size);
-  if (m > a.width) {
-    bad |= BAD_SIZE;
-    return 0;
+// The blocks that the thread's rows of the BT_PART from c0 on give back, and the rows' lengths afterwards.
+__device__ inline void row_releases(const ReleaseArgs& a, int64_t c0, uint32_t (&m)[BT_MANY], int32_t (&length)[BT_MANY],
+                                    uint32_t& bad) {
+  bool done[BT_MANY];
+#pragma unroll
+  for (int k = 0; k < BT_MANY; ++k) {
+    const int64_t r = c0 + BT_MANY * threadIdx.x + k, at = min(r, a.rows - 1);
+    length[k] = a.lengths[at];
+    done[k] = a.done[at] != 0 && r < a.rows;
   }
-  return m;
+#pragma unroll
+  for (int k = 0; k < BT_MANY; ++k) {
+    m[k] = 0;
+    if (!done[k] || length[k] < 0) continue;
+    m[k] = div_up32((uint32_t)length[k], (uint32_t)a.block_size);
+    if (m[k] > a.width) {
+      bad |= BAD_SIZE;
+      m[k] = 0;
+    }
+    length[k] = -1;
+  }
 }
 
-// As k_plan: each workgroup sums up all rows, then copies its part of the
-// blocks that come back.
-__global__ __launch_bounds__(BT_THREADS) void k_release(ReleaseArgs a, bool fill, bool finish) {
-  __shared__ int64_t sums[BT_WAVES * 2];
-  __shared__ uint32_t scan[BT_WAVES];
-  __shared__ uint32_t s_base[BT_THREADS + 1];
+// As k_plan: each workgroup sums up all rows, then copies its part of the blocks that come back.
+__global__ __launch_bounds__(BT_THREADS) void k_release(ReleaseArgs a, bool fill, int finisher) {
+  __shared__ uint32_t s_sums[2][2][BT_WAVES];
+  __shared__ uint32_t s_bad;
+  __shared__ __attribute__((aligned(16))) uint32_t s_base[BT_PART];
   const int tid = threadIdx.x;
-  int64_t v[1] = {0};
-  uint32_t bad = 0;
-  for (int64_t r = tid; r < a.rows; r += BT_THREADS) v[0] += row_release(a, r, bad);
+  const bool few = a.rows <= BT_PART;
+  if (tid == 0) s_bad = 0;
   const int64_t n_free = *a.n_free;
+  int64_t all = 0;
+  uint32_t bad = 0, unused = 0, m[BT_MANY] = {};
+  int32_t length[BT_MANY] = {};
+  for (int64_t c0 = 0; c0 < a.rows; c0 += BT_PART) {
+    row_releases(a, c0, m, length, bad);
+    all += (int64_t)m[0] + m[1] + m[2] + m[3];
+  }
   if (n_free < 0 || n_free > a.free_cap) bad |= BAD_FREE;
-  block_sums(v, bad, sums);
-  if (!(bad & BAD_FREE) && n_free + v[0] > a.free_cap) bad |= BAD_SIZE;
+  __syncthreads();
+  if (bad) atomicOr(&s_bad, bad);
+  all = capped(all);
+  uint32_t v[2] = {low(all), high(all)}, sums[2];
+  block_sums(v, sums, s_sums[1]);
+  bad = s_bad;
+  const int64_t total = joined(sums[0], sums[1]);
+  if (!(bad & BAD_FREE) && n_free + total > a.free_cap) bad |= BAD_SIZE;
   if (fill && !bad) {
-    const int64_t total = v[0], per = div_up(total, gridDim.x);
+    const int64_t per = div_up(total, gridDim.x);
     const int64_t o0 = min((int64_t)blockIdx.x * per, total), o1 = min(o0 + per, total);
     int64_t carry = 0;
-    for (int64_t c0 = 0; c0 < a.rows && carry < o1; c0 += BT_THREADS) {
-      const int64_t r = c0 + tid;
-      uint32_t chunk;
-      const uint32_t base = block_exclusive(r < a.rows ? row_release(a, r, bad) : 0, &chunk, scan);
-      s_base[tid] = base;
-      if (tid == 0) s_base[BT_THREADS] = chunk;
+    int turn = 0;
+    for (int64_t c0 = 0; c0 < a.rows && carry < o1; c0 += BT_PART, ++turn) {
+      uint32_t chunk = (uint32_t)total, base;
+      if (few) {
+        base = (uint32_t)(joined(v[0], v[1]) - all);
+      } else {
+        row_releases(a, c0, m, length, unused);
+        const uint32_t sum = m[0] + m[1] + m[2] + m[3];
+        uint32_t s[1] = {sum}, all_of[1];
+        block_sums(s, all_of, s_sums[turn & 1]);
+        base = s[0] - sum;
+        chunk = all_of[0];
+      }
+#pragma unroll
+      for (int k = 0; k < BT_MANY; ++k) {
+        s_base[BT_MANY * tid + k] = base;
+        base += m[k];
+      }
       __syncthreads();
-      const int64_t lo = max(o0, carry), hi = min(o1, carry + chunk);
-      int i = 0;
-      for (int64_t o = lo + tid; o < hi; o += BT_THREADS) {
-        const uint32_t t = (uint32_t)(o - carry);
-        if (s_base[i + 1] <= t) {
-          int b = BT_THREADS;
-          while (b - i > 1) {
-            const int m = (i + b) >> 1;
-            if (s_base[m] <= t) i = m;
-            else b = m;
-          }
-        }
-        a.free_blocks[n_free + o] = a.table[(c0 + i) * a.table_stride + (t - s_base[i])];
+      const uint32_t lo = (uint32_t)(max(o0, carry) - carry), hi = (uint32_t)min(o1 - carry, (int64_t)chunk);
+      for (uint32_t t = lo; t < hi; t += BT_PART) {
+        uint32_t at[BT_MANY];
+        int i[BT_MANY];
+        int32_t id[BT_MANY];
+#pragma unroll
+        for (int k = 0; k < BT_MANY; ++k) at[k] = min(t + k * BT_THREADS + tid, hi - 1);
+        last_rows<BT_PART>(s_base, at, i);
+#pragma unroll
+        for (int k = 0; k < BT_MANY; ++k) id[k] = a.table[(c0 + i[k]) * a.table_stride + (at[k] - s_base[i[k]])];
+#pragma unroll
+        for (int k = 0; k < BT_MANY; ++k)
+          if (t + k * BT_THREADS + tid < hi) a.free_blocks[n_free + carry + at[k]] = id[k];
       }
       carry += chunk;
       __syncthreads();
     }
   }
-  if (!finish || blockIdx.x != 0) return;
-  __syncthreads();  // out_lengths may be lengths
-  for (int64_t r = tid; r < a.rows; r += BT_THREADS) {
-    const int32_t length = a.lengths[r];
-    a.out_lengths[r] = !bad && a.done[r] && length >= 0 ? -1 : length;
+  if ((int)blockIdx.x != finisher) return;
+  __syncthreads();  // out_lengths may be lengths, which every thread has read by now
+  for (int64_t c0 = 0; c0 < a.rows; c0 += BT_PART) {
+    if (!few) row_releases(a, c0, m, length, unused);
+#pragma unroll
+    for (int k = 0; k < BT_MANY; ++k) {
+      const int64_t r = c0 + BT_MANY * tid + k;
+      if (r < a.rows) a.out_lengths[r] = bad ? a.lengths[r] : length[k];
+    }
   }
   if (tid == 0) {
-    *a.out_n_free = (int32_t)(bad ? n_free : n_free + v[0]);
-    *a.out_n = bad ? fault_code(bad) : v[0];
+    *a.out_n_free = (int32_t)(bad ? n_free : n_free + total);
+    *a.out_n = bad ? fault_code(bad) : total;
   }
 }
 
@@ -887,30 +970,36 @@ void enqueue_shape(const tt_shape_args& a, hipStream_t st) {
 
 }  // namespace
 
+// What is written where it was read has to wait until every workgroup has
+// read it: it gets a launch of its own.  Otherwise one more workgroup, without
+// places, writes lengths and counts beside the others.
 hipError_t launch_plan(const tt_plan_args& a, hipStream_t st) {
-  // at least 1,024 places for a workgroup, and at most 1,024 workgroups: each sums up all rows
-  int64_t per = div_up(div_up(a.places, 1024), BT_THREADS) * BT_THREADS;
-  if (per < 1024) per = 1024;
-  const int64_t grid = a.places > 0 ? div_up(a.places, per) : 1;
-  // lengths must outlive the reads of every workgroup: written by a launch of
-  // its own where several read what one would write over
-  const bool apart = grid > 1 && (a.out_lengths == a.lengths || a.out_n_free == a.n_free);
+  const int64_t per = div_up(div_up(a.places, 1024), BT_PART) * BT_PART;  // at most 1,024 parts: each sums up all rows
+  const int parts = a.places > 0 ? (int)div_up(a.places, per) : 1;
   auto* k = a.offsets ? k_plan<false> : k_plan<true>;
-  hipLaunchKernelGGL(k, dim3((uint32_t)grid), dim3(BT_THREADS), 0, st, a, per, !apart);
-  if (apart) {
-    tt_plan_args f = a;  // no places to fill; the check of offsets against places has to stay
-    hipLaunchKernelGGL(k, dim3(1), dim3(BT_THREADS), 0, st, f, (int64_t)0, true);
+  if (parts == 1) {
+    hipLaunchKernelGGL(k, dim3(1), dim3(BT_THREADS), 0, st, a, per, 0);
+  } else if (a.out_lengths != a.lengths && a.out_n_free != a.n_free) {
+    hipLaunchKernelGGL(k, dim3((uint32_t)parts + 1), dim3(BT_THREADS), 0, st, a, per, parts);
+  } else {
+    hipLaunchKernelGGL(k, dim3((uint32_t)parts), dim3(BT_THREADS), 0, st, a, per, -1);
+    hipLaunchKernelGGL(k, dim3(1), dim3(BT_THREADS), 0, st, a, (int64_t)0, 0);
   }
   return hipGetLastError();
 }
 
 hipError_t launch_release(const ReleaseArgs& a, hipStream_t st) {
-  // 8,192 entries of the table for a workgroup, at most 512 workgroups
-  int64_t grid = a.rows * a.width / 8192 + 1;
-  if (grid > 512) grid = 512;
-  const bool apart = grid > 1 && (a.out_lengths == a.lengths || a.out_n_free == a.n_free);
-  hipLaunchKernelGGL(k_release, dim3((uint32_t)grid), dim3(BT_THREADS), 0, st, a, true, !apart);
-  if (apart) hipLaunchKernelGGL(k_release, dim3(1), dim3(BT_THREADS), 0, st, a, false, true);
+  // the blocks that come back are counted on the device: a part for every 8,192 entries of the table, at most 512
+  int64_t parts = a.rows * a.width / 8192 + 1;
+  if (parts > 512) parts = 512;
+  if (parts == 1) {
+    hipLaunchKernelGGL(k_release, dim3(1), dim3(BT_THREADS), 0, st, a, true, 0);
+  } else if (a.out_lengths != a.lengths && a.out_n_free != a.n_free) {
+    hipLaunchKernelGGL(k_release, dim3((uint32_t)parts), dim3(BT_THREADS), 0, st, a, true, (int)parts - 1);
+  } else {
+    hipLaunchKernelGGL(k_release, dim3((uint32_t)parts), dim3(BT_THREADS), 0, st, a, true, -1);
+    hipLaunchKernelGGL(k_release, dim3(1), dim3(BT_THREADS), 0, st, a, false, 0);
+  }
   return hipGetLastError();
 }
 
