@@ -11,7 +11,6 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import exact_byte_level_amd as tt  # noqa: E402
-from exact_byte_level_amd import serve  # noqa: E402
 from tests import serve_oracle as so  # noqa: E402
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -20,7 +19,15 @@ P = 1 << 20  # an address that no refused call touches
 
 @pytest.fixture(scope="module")
 def lib():
-    return serve._start()
+    """The C calls with their argument types."""
+    L = ctypes.CDLL(tt.LIB_PATH)
+    vp, i64 = ctypes.c_void_p, ctypes.c_int64
+    L.tt_plan_blocks.argtypes = L.tt_shape_logits.argtypes = L.tt_vocab_size.argtypes = L.tt_vocab_strings.argtypes = [vp, vp]
+    L.tt_release_blocks.argtypes = [vp, vp, i64, i64, vp, i64, i64, vp, i64, vp, vp, vp, vp, vp]
+    L.tt_token_bits.argtypes = [vp, i64, vp, i64, i64, vp, i64, ctypes.c_int, vp]
+    L.tt_grammar_bits.argtypes = [vp, vp, i64, vp, i64, i64, vp]
+    L.tt_grammar_advance.argtypes = [vp, vp, vp, i64, vp, vp]
+    return L
 
 
 def test_exports_every_declared_symbol(lib):
@@ -140,6 +147,13 @@ def test_binding_refuses_host_tensors():
         tt.token_bits_into(i32(3), i32(1, 1), 32)
     with pytest.raises(ValueError, match="logits is not on a GPU"):
         tt.shape_logits_into(torch.zeros(1, 8), torch.zeros(1, 8))
+
+
+def test_binding_refuses_what_is_no_tensor():
+    with pytest.raises(ValueError, match="logits: a tensor is needed"):
+        tt.shape_logits_into([1.0], torch.zeros(1, 1))
+    with pytest.raises(ValueError, match="bits: a tensor is needed"):
+        tt.token_bits_into(torch.zeros(1, dtype=torch.int32), None, 32)
 
 
 def test_grammar_checks_its_table():
