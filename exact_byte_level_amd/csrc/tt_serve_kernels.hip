@@ -893,7 +893,10 @@ __global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles) {
   }
   if (biased) {  // the words again, now for the last entry that names each token
 #pragma unroll
-    for (int j = 0; j < 2 * N; ++j) reinterpret_cast<uint4*>(s_word)[2 * N * tid + j] = make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < N; ++j) {  // each thread the ones that it has read: others may not have theirs yet
+      uint4* w = reinterpret_cast<uint4*>(s_word) + 2 * (j * T + tid);
+      w[0] = w[1] = make_uint4(0, 0, 0, 0);
+    }
     __syncthreads();
     for (int i = tid; i < n_bias; i += T) {
       const uint32_t t = (i < T ? first : (uint32_t)a.bias_ids[b0 + i]) - v0;

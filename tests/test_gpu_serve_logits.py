@@ -71,7 +71,9 @@ def host(t):
 @pytest.mark.parametrize("rows, vocab, pad, cap, biases, sets", [
     (1, 1, 0, 1, 1, 1), (2, 7, 1, 3, 2, 1), (1, 31, 0, 40, 3, 2), (3, 32, 5, 9, 1, 3), (5, 4095, 2, 100, 9, 4),
     (2, 4096, 0, 50, 0, 2), (4, 4097, 3, 5000, 30, 3), (3, 20_003, 1, 700, 100, 5), (40, 1000, 0, 64, 4, 8),
-    (2, 100_257, 7, 9000, 300, 2)])
+    (2, 100_257, 7, 9000, 300, 2),
+    # from here on enough tiles for the large ones
+    (1100, 37, 0, 20, 3, 4), (1030, 300, 1, 64, 9, 7), (60, 70_003, 3, 3000, 300, 5), (350, 9000, 0, 500, 40, 5)])
 def test_everything_at_once(src, dst, rows, vocab, pad, cap, biases, sets):
     rng = np.random.default_rng(rows * 31 + vocab)
     wide = torch.from_numpy(rng.normal(0, 4, (rows, vocab + pad)).astype(np.float32)).cuda().to(src)
