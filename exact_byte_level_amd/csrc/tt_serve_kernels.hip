@@ -783,6 +783,12 @@ __device__ inline float pick(uint32_t bits, int k, float a, float b) {
   return d;
 }
 
+// x / d, by its reciprocal: the product and its remainder's share.
+__device__ inline float quotient(float x, float d, float reciprocal) {
+  const float q = x * reciprocal, fixed = fmaf(fmaf(-q, d, x), reciprocal, q);
+  return fabsf(q) < __builtin_inff() ? fixed : q;  // an infinity has no remainder
+}
+
 // Element i of a row, by a 32-bit offset (rows are shorter than 2^32 bytes).
 template <class T>
 __device__ inline T* from(T* row, uint32_t i) {
@@ -912,15 +918,15 @@ __global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles) {
       }
   }
 
-  // x / rho and x / temperature as products with the reciprocal, which is at
-  // most one step of 32 bits off instead of half a one.  Where the result
-  // stays in 32 bits the quotient by rho, which is not the last operation, is put
-  // right by its remainder, as a division does.  Where a reciprocal is not an
-  // ordinary number both are divisions.
+  // Quotients by rho and by the temperature go by the reciprocal: where the
+  // result stays in 32 bits put right by the remainder, which leaves them half a step
+  // off as a division does, else as a mere product, up to one step of 32 bits off, far below
+  // a step of 16.  Where a reciprocal is not an ordinary number both are divisions.
   const float inv_rho = 1.0f / rho, inv_temp = 1.0f / temp;
   const bool plain_rho = !(fabsf(rho) >= 0x1p-100f && fabsf(rho) <= 0x1p100f);
   const bool plain_temp = temp > 0.0f && !(temp >= 0x1p-100f && temp <= 0x1p100f);
-  const float scale = temp > 0.0f && !plain_temp ? inv_temp : 1.0f;
+  const bool scaled = temp > 0.0f && !plain_temp;
+  const float scale = scaled ? inv_temp : 1.0f, divisor = scaled ? temp : 1.0f;
   const float lowest = -__builtin_inff();
   O* dst = static_cast<O*>(a.out) + r * a.out_stride + v0;
 #pragma unroll
@@ -946,10 +952,7 @@ __global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles) {
 #pragma unroll
       for (int k = 0; k < SH_VEC; ++k) {
         if (sizeof(O) == 4) {
-          float q = f[k] * inv_rho;
-          const float fixed = fmaf(fmaf(-q, rho, f[k]), inv_rho, q);
-          q = fabsf(q) < __builtin_inff() ? fixed : q;  // an infinity has no remainder
-          f[k] = pick(was, k, f[k] > 0.0f ? q : f[k] * rho, f[k]);
+          f[k] = pick(was, k, f[k] > 0.0f ? quotient(f[k], rho, inv_rho) : f[k] * rho, f[k]);
         } else {
           f[k] = pick(was, k, f[k] * (f[k] > 0.0f ? inv_rho : rho), f[k]);
         }
@@ -974,7 +977,7 @@ __global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles) {
     }
     typename Pack<O>::type y;
 #pragma unroll
-    for (int k = 0; k < SH_VEC; ++k) y[k] = (O)pick(may, k, f[k] * scale, lowest);
+    for (int k = 0; k < SH_VEC; ++k) y[k] = (O)pick(may, k, sizeof(O) == 4 ? quotient(f[k], divisor, scale) : f[k] * scale, lowest);
     if (i + SH_VEC <= here) {
       *reinterpret_cast<typename Pack<O>::type*>(from(dst, i)) = y;
     } else {
