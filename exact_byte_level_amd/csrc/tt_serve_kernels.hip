@@ -391,16 +391,19 @@ constexpr int64_t TB_LONG = 12288;   // and ids of a text, on average
 
 typedef uint32_t Ids4 __attribute__((ext_vector_type(4), aligned(4)));  // from any id on
 
+// Ids of texts repeat: a bit that is there costs a read, which lanes share, and
+// no atomic, which they would queue for.
+__device__ inline void put_bit(uint32_t id, uint32_t v0, uint32_t v1, uint32_t* set) {
+  if (id < v0 || id >= v1) return;
+  uint32_t* w = &set[(id - v0) >> 5];
+  if (!(*w >> (id & 31) & 1)) atomicOr(w, 1u << (id & 31));
+}
+
 // The ids [lo, hi) that are in [v0, v1), as bits of `set` from id v0 on.  The
 // next ids are loaded before these are looked at; the last loads reach back,
-// since a bit may be set twice.  Ids of texts repeat: a bit that is there costs a
-// read, which lanes share, and no atomic, which they would queue for.
+// since a bit may be set twice.
 __device__ inline void gather_bits(const int32_t* ids, int64_t lo, int64_t hi, uint32_t v0, uint32_t v1, uint32_t* set) {
-  auto put = [&](uint32_t id) {
-    if (id < v0 || id >= v1) return;
-    uint32_t* w = &set[(id - v0) >> 5];
-    if (!(*w >> (id & 31) & 1)) atomicOr(w, 1u << (id & 31));
-  };
+  auto put = [&](uint32_t id) { put_bit(id, v0, v1, set); };
   if (hi - lo < 4) {
     if (lo + threadIdx.x < hi) put((uint32_t)ids[lo + threadIdx.x]);
     return;
@@ -451,19 +454,28 @@ __global__ __launch_bounds__(TB_THREADS) void k_token_bits(const int32_t* ids, i
 // A workgroup gathers what its part has of a text in LDS and joins it to the
 // text's set, cleared before, by atomics (a joint of sets is the same in any
 // order).  Where its part of a text is short, one wavefront sets the bits one by
-// one.  64 texts of two million ids take 10.7 us and the clearing 2: the reads are 8 MB, but
-// a part waits for its bounds, its ids and its LDS atomics in turn, and ids of texts queue there.
+// one.  Ids and bounds are loaded together, and the ids stay in registers for all
+// texts of the part.  64 texts of two million ids (8 MB) take 11 us and the clearing
+// 1 to 4: a part's loads, its LDS atomics and the atomics on memory follow each other, and
+// there is one part for a CU.  Two words to an atomic on memory is no faster.
 __global__ __launch_bounds__(TB_THREADS) void k_token_bits_split(const int32_t* ids, int64_t n, const int64_t* offsets,
                                                                  int64_t rows, int64_t vocab, int32_t* bits,
-                                                                 int64_t stride, int64_t per_block) {
+                                                                 int64_t stride) {
   extern __shared__ uint32_t set[];
   // texts that reach into the part, of the 1,024 at hand, and their ids in it
   __shared__ int s_row[TB_THREADS];
-  __shared__ int64_t s_lo[TB_THREADS], s_hi[TB_THREADS];
+  __shared__ int s_lo[TB_THREADS], s_hi[TB_THREADS];
   __shared__ int s_rows;
   const int tid = threadIdx.x, words = (int)div_up(vocab, 32);
-  const int64_t t0 = (int64_t)blockIdx.x * per_block, t1 = min(t0 + per_block, n);
-  const int64_t least = words > TB_WORDS ? n + 1 : max(words / 4, WAVE);  // ids that are worth a set in LDS
+  const int64_t t0 = (int64_t)blockIdx.x * TB_BATCH, t1 = min(t0 + TB_BATCH, n);
+  const bool in_lds = words <= TB_WORDS;
+  const int least = max(words / 4, WAVE);  // ids that are worth a set in LDS
+  // n is more than a part: the last part's loads reach back
+  const int64_t x_at = min(t0 + 4 * tid, n - 4), y_at = min(t0 + TB_BATCH / 2 + 4 * tid, n - 4);
+  const Ids4 x = *reinterpret_cast<const Ids4*>(ids + x_at), y = *reinterpret_cast<const Ids4*>(ids + y_at);
+  const int x_from = (int)(x_at - t0), y_from = (int)(y_at - t0);  // negative where they reach back
+  if (in_lds)
+    for (int i = tid; i < words; i += TB_THREADS) set[i] = 0;
   for (int64_t base = 0; base < rows; base += TB_THREADS) {
     if (tid == 0) s_rows = 0;
     __syncthreads();
@@ -474,29 +486,34 @@ __global__ __launch_bounds__(TB_THREADS) void k_token_bits_split(const int32_t* 
       if (lo < hi) {
         const int j = atomicAdd(&s_rows, 1);
         s_row[j] = tid;
-        s_lo[j] = lo;
-        s_hi[j] = hi;
+        s_lo[j] = (int)(lo - t0);
+        s_hi[j] = (int)(hi - t0);
       }
     }
     __syncthreads();
     const int count = s_rows;
     for (int j = 0; j < count; ++j) {
-      const int64_t lo = s_lo[j], hi = s_hi[j];
+      const int lo = s_lo[j], hi = s_hi[j];
       uint32_t* out = reinterpret_cast<uint32_t*>(bits) + (base + s_row[j]) * stride;
-      if (hi - lo < least) {
+      if (!in_lds || hi - lo < least) {
         if (j % (TB_THREADS / WAVE) != tid / WAVE) continue;
-        for (int64_t i = lo + tid % WAVE; i < hi; i += WAVE) {
-          const uint32_t id = (uint32_t)ids[i];
+        for (int i = lo + tid % WAVE; i < hi; i += WAVE) {
+          const uint32_t id = (uint32_t)ids[t0 + i];
           if (id < (uint32_t)vocab) atomicOr(&out[id >> 5], 1u << (id & 31));
         }
         continue;
       }
-      for (int i = tid; i < words; i += TB_THREADS) set[i] = 0;
-      __syncthreads();
-      gather_bits(ids, lo, hi, 0, (uint32_t)vocab, set);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (x_from + k >= lo && x_from + k < hi) put_bit(x[k], 0, (uint32_t)vocab, set);
+        if (y_from + k >= lo && y_from + k < hi) put_bit(y[k], 0, (uint32_t)vocab, set);
+      }
       __syncthreads();
       for (int i = tid; i < words; i += TB_THREADS)
-        if (set[i]) atomicOr(&out[i], set[i]);
+        if (const uint32_t w = set[i]) {
+          atomicOr(&out[i], w);
+          set[i] = 0;
+        }
       __syncthreads();
     }
     __syncthreads();
@@ -1054,9 +1071,8 @@ hipError_t launch_token_bits(const int32_t* ids, int64_t n, const int64_t* offse
   if (!add)
     hipLaunchKernelGGL(k_clear_bits, dim3((uint32_t)div_up(words, 256), (uint32_t)min(rows, (int64_t)32768)), dim3(256),
                        0, st, bits, rows, words, stride);
-  const int64_t per = max((int64_t)TB_BATCH, div_up(n, 512));
-  hipLaunchKernelGGL(k_token_bits_split, dim3((uint32_t)div_up(n, per)), dim3(TB_THREADS), lds, st, ids, n, offsets, rows,
-                     vocab, bits, stride, per);
+  hipLaunchKernelGGL(k_token_bits_split, dim3((uint32_t)div_up(n, TB_BATCH)), dim3(TB_THREADS), lds, st, ids, n, offsets,
+                     rows, vocab, bits, stride);
   return hipGetLastError();
 }
 
