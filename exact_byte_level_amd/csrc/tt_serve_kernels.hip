@@ -588,8 +588,9 @@ __global__ __launch_bounds__(GR_THREADS) void k_grammar_bits(tt_grammar g, const
 constexpr int GM_THREADS = 1024;
 constexpr int GM_CHUNKS = 2;                       // tokens of a thread
 constexpr int GM_TOKENS = GM_THREADS * GM_CHUNKS;  // of a workgroup
+constexpr int GM_WORDS = GM_TOKENS / 32;
 constexpr int GM_KEEP = 16;                        // bytes of a token that are kept as classes
-constexpr int GM_LDS = 112 * 1024;  // of the automaton, at most; beyond, it is read from L2
+constexpr int64_t GM_LDS = 156 * 1024;              // at most, beside 1.3 KB that are always there
 
 typedef uint32_t Bytes16 __attribute__((ext_vector_type(4)));
 typedef uint32_t Bytes16Any __attribute__((ext_vector_type(4), aligned(1)));  // at any address
@@ -617,19 +618,20 @@ __device__ inline uint32_t walk(const int16_t* next, uint32_t n, uint32_t nc, co
 template <bool IN_LDS>
 __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const int32_t* states, int64_t rows,
                                                              int64_t vocab, int32_t* bits, int64_t stride, int tiles,
-                                                             int64_t per_block) {
-  extern __shared__ __attribute__((aligned(16))) uint64_t s_self[];  // [n] classes that lead from a state to itself
-  __shared__ uint32_t s_bits[WAVE][GM_TOKENS / 32];  // sets of the 64 states at hand; first, the tokens' order
+                                                             int64_t per_block, int batch) {
+  // [batch][GM_WORDS] the sets at hand (first, the tokens' order); [n] classes that lead from a state to itself; the automaton
+  extern __shared__ __attribute__((aligned(16))) uint32_t s_bits[];
   __shared__ uint8_t cls[256];
   __shared__ uint32_t s_first[257];  // tokens by the class of their first byte
   const int tid = threadIdx.x, lane = tid % WAVE;
   const uint32_t n = (uint32_t)g.n_states, nc = (uint32_t)g.n_classes;
   const bool sets = nc <= 64;
+  uint64_t* s_self = reinterpret_cast<uint64_t*>(s_bits + batch * GM_WORDS);
   int16_t* s_next = reinterpret_cast<int16_t*>(s_self + (sets ? (n + 1) / 2 * 2 : 0));
   const int16_t* next = IN_LDS ? s_next : g.next;
   // the tokens in order of their first class; those that are not walked are left out
   const int64_t v0 = (int64_t)(blockIdx.x % tiles) * GM_TOKENS;
-  uint16_t* order = reinterpret_cast<uint16_t*>(&s_bits[0][0]);
+  uint16_t* order = reinterpret_cast<uint16_t*>(s_bits);
   int first[GM_CHUNKS], nth[GM_CHUNKS];
 #pragma unroll
   for (int j = 0; j < GM_CHUNKS; ++j) {
@@ -711,16 +713,25 @@ __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const
   }
 
   const int64_t r0 = blockIdx.x / tiles * per_block, r1 = min(r0 + per_block, rows);
-  const int64_t word0 = v0 / 32, words = min(div_up(vocab, 32) - word0, (int64_t)(GM_TOKENS / 32));
+  const int64_t word0 = v0 / 32, words = min(div_up(vocab, 32) - word0, (int64_t)GM_WORDS);
   const int end = g.end_id >= v0 && g.end_id < min(v0 + GM_TOKENS, vocab) ? (int)(g.end_id - v0) : -1;
-  for (int64_t r = r0; r < r1; r += WAVE) {
-    const int count = (int)min((int64_t)WAVE, r1 - r);
-    __syncthreads();  // the order is read, or the sets before are written
-    for (int i = tid; i < WAVE * GM_TOKENS / 32; i += GM_THREADS) (&s_bits[0][0])[i] = 0;
-    __syncthreads();
-    const int32_t q_lane = lane < count ? states[r + lane] : TT_STATE_DEAD;
+  for (int64_t r = r0; r < r1; r += batch) {
+   const int batch_rows = (int)min((int64_t)batch, r1 - r);
+   __syncthreads();  // the order is read, or the sets before are written
+   for (int i = tid; i < batch_rows * GM_WORDS; i += GM_THREADS) s_bits[i] = 0;
+   __syncthreads();
+   for (int r64 = 0; r64 < batch_rows; r64 += WAVE) {
+    const int count = min(WAVE, batch_rows - r64);
+    uint32_t* sets_of = s_bits + r64 * GM_WORDS;
+    const int32_t q_lane = lane < count ? states[r + r64 + lane] : TT_STATE_DEAD;
     const bool good = (uint32_t)q_lane < n;
-    const uint64_t free = __ballot(q_lane == TT_STATE_FREE);
+    uint64_t free = __ballot(q_lane == TT_STATE_FREE);
+    for (; free && tid < WAVE; free &= free - 1) {
+      static_assert(GM_WORDS == WAVE, "a lane for each word");
+      const int64_t rest = vocab - (word0 + lane) * 32;
+      sets_of[__builtin_ctzll(free) * GM_WORDS + lane] = rest >= 32 ? 0xFFFFFFFFu : rest > 0 ? (1u << rest) - 1u : 0u;
+    }
+    if (end >= 0 && tid < count && good && g.accept[q_lane]) atomicOr(&sets_of[tid * GM_WORDS + (end >> 5)], 1u << (end & 31));
 #pragma unroll
     for (int j = 0; j < GM_CHUNKS; ++j) {
       // the states that some token's first byte leaves alive
@@ -741,21 +752,15 @@ __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const
         q = walk<1>(next, n, nc, t[j], q, go);
         for (int k = GM_KEEP; go && k < t[j].len && q < n; ++k)
           q = (uint32_t)(int32_t)next[q * nc + cls[g.strings[t[j].at + k]]];
-        if (q < n) atomicOr(&s_bits[i][t[j].place >> 5], 1u << (t[j].place & 31));
+        if (q < n) atomicOr(&sets_of[i * GM_WORDS + (t[j].place >> 5)], 1u << (t[j].place & 31));
       }
     }
-    if (end >= 0 && tid < count && good && g.accept[q_lane]) atomicOr(&s_bits[tid][end >> 5], 1u << (end & 31));
-    __syncthreads();
-    for (int i = tid; i < count * (GM_TOKENS / 32); i += GM_THREADS) {
-      const int row = i / (GM_TOKENS / 32), w = i % (GM_TOKENS / 32);
-      if (w >= words) continue;
-      uint32_t out = s_bits[row][w];
-      if (free >> row & 1) {
-        const int64_t rest = vocab - (word0 + w) * 32;
-        out = rest >= 32 ? 0xFFFFFFFFu : (1u << rest) - 1u;
-      }
-      bits[(r + row) * stride + word0 + w] = (int32_t)out;
-    }
+   }
+   __syncthreads();
+   for (int i = tid; i < batch_rows * GM_WORDS; i += GM_THREADS) {
+     const int row = i / GM_WORDS, w = i % GM_WORDS;
+     if (w < words) bits[(r + row) * stride + word0 + w] = (int32_t)s_bits[i];
+   }
   }
 }
 
@@ -1079,18 +1084,21 @@ hipError_t launch_token_bits(const int32_t* ids, int64_t n, const int64_t* offse
 hipError_t launch_grammar_bits(const tt_grammar& g, const int32_t* states, int64_t rows, int32_t* bits,
                                int64_t stride, int64_t vocab, hipStream_t st) {
   if (rows >= WAVE) {
-    // a workgroup for every CU, each with 64 states at least
+    // a workgroup for every CU, each with 64 states at least; as many sets at a time as LDS holds beside the
+    // automaton, which is read from L2 where not even 64 fit beside it
     const int64_t tiles = div_up(vocab, GM_TOKENS);
     const int64_t parts = min(div_up(rows, WAVE), max((int64_t)1, (int64_t)256 / tiles)), per = div_up(rows, parts);
     const int64_t table = 2 * g.n_states * g.n_classes, self = g.n_classes <= 64 ? (g.n_states + 1) / 2 * 16 : 0;
-    const dim3 grid((uint32_t)(tiles * div_up(rows, per))), block(GM_THREADS);
-    if (table + self <= GM_LDS)
-      hipLaunchKernelGGL(k_grammar_many<true>, grid, block, (size_t)(table + self), st, g, states, rows, vocab, bits,
-                         stride, (int)tiles, per);
-    else if (self <= GM_LDS)
-      hipLaunchKernelGGL(k_grammar_many<false>, grid, block, (size_t)self, st, g, states, rows, vocab, bits, stride,
-                         (int)tiles, per);
-    if (self <= GM_LDS) return hipGetLastError();
+    const bool in_lds = table + self + WAVE * GM_WORDS * 4 <= GM_LDS;
+    const int64_t fixed = self + (in_lds ? table : 0), room = (GM_LDS - fixed) / (WAVE * GM_WORDS * 4) * WAVE;
+    const int64_t batch = min(room, div_up(per, WAVE) * WAVE);
+    if (batch > 0) {
+      auto* k = in_lds ? k_grammar_many<true> : k_grammar_many<false>;
+      hipLaunchKernelGGL(k, dim3((uint32_t)(tiles * div_up(rows, per))), dim3(GM_THREADS),
+                         (size_t)(fixed + batch * GM_WORDS * 4), st, g, states, rows, vocab, bits, stride, (int)tiles, per,
+                         (int)batch);
+      return hipGetLastError();
+    }
   }
   const int64_t tiles = div_up(vocab, GR_THREADS);
   hipLaunchKernelGGL(k_grammar_bits, dim3((uint32_t)(rows * tiles)), dim3(GR_THREADS), 0, st, g, states, vocab, bits,
