@@ -589,6 +589,7 @@ constexpr int GM_THREADS = 1024;
 constexpr int GM_CHUNKS = 2;                       // tokens of a thread
 constexpr int GM_TOKENS = GM_THREADS * GM_CHUNKS;  // of a workgroup
 constexpr int GM_WORDS = GM_TOKENS / 32;
+constexpr int GM_KEYS = 512;                       // by which a workgroup's tokens are ordered
 constexpr int GM_KEEP = 16;                        // bytes of a token that are kept as classes
 constexpr int64_t GM_LDS = 156 * 1024;              // at most, beside 1.3 KB that are always there
 
@@ -602,6 +603,16 @@ struct KeptToken {
   int at, len;              // its bytes; len 0: none or not to be walked
   int place;                // in the workgroup's tokens
 };
+
+// Classes that lead from a state to itself, and to any state.
+struct StateSets {
+  uint64_t self, live;
+};
+
+__device__ inline uint64_t wave_or(uint64_t v) {
+  for (int d = WAVE / 2; d > 0; d >>= 1) v |= __shfl_xor((unsigned long long)v, d);
+  return v;
+}
 
 // The state after the bytes K .. GM_KEEP - 1 of each lane's token.
 template <int K>
@@ -619,20 +630,20 @@ template <bool IN_LDS>
 __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const int32_t* states, int64_t rows,
                                                              int64_t vocab, int32_t* bits, int64_t stride, int tiles,
                                                              int64_t per_block, int batch) {
-  // [batch][GM_WORDS] the sets at hand (first, the tokens' order); [n] classes that lead from a state to itself; the automaton
+  // [batch][GM_WORDS] the sets at hand (first, the tokens' order); [n] the states' sets; the automaton
   extern __shared__ __attribute__((aligned(16))) uint32_t s_bits[];
   __shared__ uint8_t cls[256];
-  __shared__ uint32_t s_first[257];  // tokens by the class of their first byte
+  __shared__ uint32_t s_first[GM_KEYS + 1];  // tokens by their first class and three bits of the second
   const int tid = threadIdx.x, lane = tid % WAVE;
   const uint32_t n = (uint32_t)g.n_states, nc = (uint32_t)g.n_classes;
   const bool sets = nc <= 64;
-  uint64_t* s_self = reinterpret_cast<uint64_t*>(s_bits + batch * GM_WORDS);
-  int16_t* s_next = reinterpret_cast<int16_t*>(s_self + (sets ? (n + 1) / 2 * 2 : 0));
+  StateSets* s_sets = reinterpret_cast<StateSets*>(s_bits + batch * GM_WORDS);
+  int16_t* s_next = reinterpret_cast<int16_t*>(s_sets + (sets ? n : 0));
   const int16_t* next = IN_LDS ? s_next : g.next;
   // the tokens in order of their first class; those that are not walked are left out
   const int64_t v0 = (int64_t)(blockIdx.x % tiles) * GM_TOKENS;
   uint16_t* order = reinterpret_cast<uint16_t*>(s_bits);
-  int first[GM_CHUNKS], nth[GM_CHUNKS];
+  int first[GM_CHUNKS], then[GM_CHUNKS], nth[GM_CHUNKS];
 #pragma unroll
   for (int j = 0; j < GM_CHUNKS; ++j) {
     const int64_t v = v0 + j * GM_THREADS + tid;
@@ -640,9 +651,10 @@ __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const
     int len = 0;
     if (v < g.n_tokens && v < vocab && v != g.end_id) token_span(g, v, at, len);
     first[j] = len > 0 ? g.strings[at] : -1;
+    then[j] = len > 1 ? g.strings[at + 1] : -1;
   }
   for (int i = tid; i < 256; i += GM_THREADS) cls[i] = (uint8_t)min((int)g.classes[i], (int)nc - 1);
-  if (tid < 257) s_first[tid] = 0;
+  if (tid <= GM_KEYS) s_first[tid] = 0;
   if (IN_LDS) {
     const uint32_t whole = n * nc / 8;
 #pragma unroll 4
@@ -654,35 +666,39 @@ __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const
 #pragma unroll
   for (int j = 0; j < GM_CHUNKS; ++j)
     if (first[j] >= 0) {
-      first[j] = cls[first[j]];
+      first[j] = sets ? cls[first[j]] * 8 + (then[j] >= 0 ? cls[then[j]] & 7 : 0) : cls[first[j]];
       nth[j] = (int)atomicAdd(&s_first[first[j] + 1], 1u);
     }
   if (sets)
     for (uint32_t q = tid; q < n; q += GM_THREADS) {
-      uint64_t m = 0;
-      for (uint32_t k = 0; k < nc; ++k) m |= (uint64_t)((uint32_t)(int32_t)next[q * nc + k] == q) << k;
-      s_self[q] = m;
+      StateSets m{0, 0};
+      for (uint32_t k = 0; k < nc; ++k) {
+        const uint32_t to = (uint32_t)(int32_t)next[q * nc + k];
+        m.self |= (uint64_t)(to == q) << k;
+        m.live |= (uint64_t)(to < n) << k;
+      }
+      s_sets[q] = m;
     }
   __syncthreads();
-  if (tid < WAVE) {  // inclusive sums of 256 counts by one wavefront, four to a lane
-    uint32_t c[4], sum = 0;
+  if (tid < WAVE) {  // inclusive sums of the counts by one wavefront, eight to a lane
+    constexpr int EACH = GM_KEYS / WAVE;
+    uint32_t c[EACH], sum = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) c[k] = sum += s_first[1 + 4 * lane + k];
-    uint32_t inc = sum;
-    for (int d = 1; d < WAVE; d <<= 1) {
-      const uint32_t o = (uint32_t)__shfl_up((int)inc, d);
-      if (lane >= d) inc += o;
-    }
+    for (int k = 0; k < EACH; ++k) c[k] = sum += s_first[1 + EACH * lane + k];
+    const uint32_t before = wave_sums(sum) - sum;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) s_first[1 + 4 * lane + k] = inc - sum + c[k];
+    for (int k = 0; k < EACH; ++k) s_first[1 + EACH * lane + k] = before + c[k];
   }
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < GM_CHUNKS; ++j)
     if (first[j] >= 0) order[s_first[first[j]] + nth[j]] = (uint16_t)(j * GM_THREADS + tid);
   __syncthreads();
-  const int walked = (int)s_first[256];
+  const int walked = (int)s_first[GM_KEYS];
   KeptToken t[GM_CHUNKS];
+  bool alike[GM_CHUNKS], single[GM_CHUNKS];
+  int lead[GM_CHUNKS];
+  uint64_t second[GM_CHUNKS], later[GM_CHUNKS];
 #pragma unroll
   for (int j = 0; j < GM_CHUNKS; ++j) {
     // a wavefront's chunks are 16 apart, so that all wavefronts share the long runs of one class
@@ -710,6 +726,14 @@ __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const
       if (k && k < t[j].len) t[j].later |= 1ull << (c & 63);
     }
     for (int k = GM_KEEP; k < t[j].len; ++k) t[j].later |= 1ull << (cls[g.strings[t[j].at + k]] & 63);
+    // what the 64 tokens have in common: their first class, if it is one, and the sets of their other ones
+    const uint64_t some = __ballot(t[j].len > 0);
+    lead[j] = some ? __builtin_ctzll(some) : 0;
+    const uint32_t c0 = (uint32_t)__builtin_amdgcn_readlane((int)(t[j].c[0] & 255), lead[j]);
+    alike[j] = sets && some && __ballot(t[j].len > 0 && (t[j].c[0] & 255) != c0) == 0;
+    single[j] = __any(t[j].len == 1);
+    second[j] = wave_or(t[j].len > 1 ? 1ull << (t[j].c[0] >> 8 & 63) : 0);
+    later[j] = wave_or(t[j].later);
   }
 
   const int64_t r0 = blockIdx.x / tiles * per_block, r1 = min(r0 + per_block, rows);
@@ -725,6 +749,7 @@ __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const
     uint32_t* sets_of = s_bits + r64 * GM_WORDS;
     const int32_t q_lane = lane < count ? states[r + r64 + lane] : TT_STATE_DEAD;
     const bool good = (uint32_t)q_lane < n;
+    const uint64_t possible = sets && good ? s_sets[q_lane].live : 0;
     uint64_t free = __ballot(q_lane == TT_STATE_FREE);
     for (; free && tid < WAVE; free &= free - 1) {
       static_assert(GM_WORDS == WAVE, "a lane for each word");
@@ -734,21 +759,38 @@ __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const
     if (end >= 0 && tid < count && good && g.accept[q_lane]) atomicOr(&sets_of[tid * GM_WORDS + (end >> 5)], 1u << (end & 31));
 #pragma unroll
     for (int j = 0; j < GM_CHUNKS; ++j) {
-      // the states that some token's first byte leaves alive
-      uint64_t live = 0, left = __ballot(t[j].len > 0);
-      while (left) {
-        const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)(t[j].c[0] & 255), __builtin_ctzll(left));
-        live |= __ballot(good && (uint32_t)(int32_t)next[(good ? (uint32_t)q_lane : 0) * nc + c] < n);
-        left &= ~__ballot((t[j].c[0] & 255) == c);
+      // the states that each token's first byte leaves alive
+      uint64_t mine = 0, all = 0;
+      if (alike[j]) {  // and of them those that all tokens stay in, and those that some token's second byte leaves alive
+        const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)(t[j].c[0] & 255), lead[j]);
+        const uint32_t q = good ? (uint32_t)(int32_t)next[(uint32_t)q_lane * nc + c] : n;
+        const StateSets m = s_sets[q < n ? q : 0];
+        const bool whole = q < n && (later[j] & ~m.self) == 0;
+        all = __ballot(whole);
+        const uint64_t some = __ballot(q < n && !whole && (single[j] || (m.live & second[j])));
+        if (t[j].len > 0) mine = some;
+      } else {
+        for (uint64_t left = __ballot(t[j].len > 0); left;) {
+          const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)(t[j].c[0] & 255), __builtin_ctzll(left));
+          const bool same = t[j].len > 0 && (t[j].c[0] & 255) == c;
+          bool live = possible >> (c & 63) & 1;
+          if (!sets) live = good && (uint32_t)(int32_t)next[(uint32_t)q_lane * nc + c] < n;
+          const uint64_t states_of = __ballot(live);
+          if (same) mine = states_of;
+          left &= ~__ballot(same);
+        }
       }
-      while (live) {
-        const int i = __builtin_ctzll(live);
-        live &= live - 1;
-        const uint32_t q0 = (uint32_t)__builtin_amdgcn_readlane(q_lane, i);
+      for (; all; all &= all - 1)
+        if (t[j].len > 0) atomicOr(&sets_of[__builtin_ctzll(all) * GM_WORDS + (t[j].place >> 5)], 1u << (t[j].place & 31));
+      while (__any(mine != 0)) {  // each lane walks from its own next state
+        const bool on = mine != 0;
+        const int i = on ? __builtin_ctzll(mine) : 0;
+        mine &= mine - 1;
+        const uint32_t q0 = (uint32_t)__shfl(q_lane, i);
         uint32_t q = n;
-        if (t[j].len > 0) q = (uint32_t)(int32_t)next[q0 * nc + (t[j].c[0] & 255)];
+        if (on) q = (uint32_t)(int32_t)next[q0 * nc + (t[j].c[0] & 255)];
         bool go = q < n && t[j].len > 1;
-        if (sets && go && (t[j].later & ~s_self[q]) == 0) go = false;  // every further byte stays in it
+        if (sets && go && (t[j].later & ~s_sets[q].self) == 0) go = false;  // every further byte stays in it
         q = walk<1>(next, n, nc, t[j], q, go);
         for (int k = GM_KEEP; go && k < t[j].len && q < n; ++k)
           q = (uint32_t)(int32_t)next[q * nc + cls[g.strings[t[j].at + k]]];
@@ -1088,7 +1130,7 @@ hipError_t launch_grammar_bits(const tt_grammar& g, const int32_t* states, int64
     // automaton, which is read from L2 where not even 64 fit beside it
     const int64_t tiles = div_up(vocab, GM_TOKENS);
     const int64_t parts = min(div_up(rows, WAVE), max((int64_t)1, (int64_t)256 / tiles)), per = div_up(rows, parts);
-    const int64_t table = 2 * g.n_states * g.n_classes, self = g.n_classes <= 64 ? (g.n_states + 1) / 2 * 16 : 0;
+    const int64_t table = 2 * g.n_states * g.n_classes, self = g.n_classes <= 64 ? 16 * g.n_states : 0;
     const bool in_lds = table + self + WAVE * GM_WORDS * 4 <= GM_LDS;
     const int64_t fixed = self + (in_lds ? table : 0), room = (GM_LDS - fixed) / (WAVE * GM_WORDS * 4) * WAVE;
     const int64_t batch = min(room, div_up(per, WAVE) * WAVE);
