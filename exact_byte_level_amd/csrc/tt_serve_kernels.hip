@@ -573,18 +573,21 @@ __global__ __launch_bounds__(GR_THREADS) void k_grammar_bits(tt_grammar g, const
 }
 
 // The sets of many states at a time.  A workgroup takes 2,048 tokens, puts them
-// in order of the class of their first byte, and keeps the byte classes of two
-// tokens in each thread's registers, so that the 64 tokens of a wavefront mostly
-// start alike.  Then, 64 states at a time, one lane tries the first byte
-// for each state: only the states that live on are walked with the 64 tokens, and
-// in most states of a grammar few first bytes are possible.  A token whose
-// further bytes all lead from a state back to it (the inside of a text) is
-// done after one look at two sets of classes.
-// 1,024 states and 100,257 tokens take 62 us (k_grammar_bits 340): about 10 us
-// to load and order the tokens, then walks, each a chain of three or four reads of
-// LDS that four wavefronts to a SIMD do not hide, and waits for the wavefront with
-// the most of them.  With 4,096 tokens a workgroup it is 58 us, but 31 us instead of
-// 22 for 64 states, from which on this kernel is no slower than the other.
+// in order of the classes of their first two bytes, and keeps the byte classes of
+// two tokens in each thread's registers, so that the 64 tokens of a wavefront mostly
+// begin alike.  Then, 64 states at a time, a lane looks for each state at what the
+// tokens begin with: in most states of a grammar few bytes are possible, and those
+// that none of the 64 tokens begins with are done.  So are the states from which all
+// further bytes of all 64 lead back to it (the inside of a text), by two sets of classes.
+// What is left is walked, each lane from its own next state.
+//
+// 1,024 states and 100,257 tokens take 51-55 us (k_grammar_bits 340).  About 10 us are the
+// loading and ordering of the tokens; then wavefronts with many walks (runs of
+// spaces, mixed beginnings), each a chain of reads of LDS, keep the others of
+// their workgroup waiting, which is what bounds it.  Walking two or four states together
+// in a lane is slower (63 and 69 us where one took 58), and so is skipping bytes that lead
+// back to a state by their classes (84 us where stepping takes 51).  From 64 states on this
+// kernel is no slower than the other.
 constexpr int GM_THREADS = 1024;
 constexpr int GM_CHUNKS = 2;                       // tokens of a thread
 constexpr int GM_TOKENS = GM_THREADS * GM_CHUNKS;  // of a workgroup
