@@ -8,6 +8,7 @@ constexpr int64_t MAX_ROWS = (int64_t)1 << 24;
 constexpr int64_t MAX_VOCAB = (int64_t)1 << 24;
 constexpr int64_t MAX_INT32 = 0x7FFFFFFF;
 constexpr int64_t MAX_BLOCK = (int64_t)1 << 20;
+constexpr int64_t MAX_LIST = (int64_t)1 << 30;  // entries of a list that is counted in 32 bits
 constexpr int64_t MAX_GRID = (int64_t)1 << 30;  // workgroups of a launch
 
 int done(hipError_t e) { return e == hipSuccess ? TT_OK : TT_EHIP; }
@@ -113,7 +114,7 @@ int tt_shape_logits(const tt_shape_args* args, hipStream_t stream) {
   if (a.generated && (a.generated_cap < 0 || a.generated_stride < 0)) return TT_EINVAL;
   if (a.n_bias < 0 || (a.bias_offsets && a.n_bias > 0 && (!a.bias_ids || !a.bias_values))) return TT_EINVAL;
   if (a.allowed && (a.allowed_count < 0 || a.allowed_stride < 0)) return TT_EINVAL;
-  if (a.generated_cap > MAX_INT32 || a.n_bias > MAX_INT32) return TT_ETOOBIG;
+  if (a.generated_cap > MAX_LIST || a.n_bias > MAX_LIST) return TT_ETOOBIG;
   if (a.rows * words > MAX_GRID) return TT_ETOOBIG;
   return done(tt::launch_shape(a, stream));
 }

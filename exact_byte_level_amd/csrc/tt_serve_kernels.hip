@@ -873,8 +873,8 @@ __device__ inline T* from(T* row, uint32_t i) {
 // 256 x 262,144 float32 take 99 us, 5.6 TB/s of what has to be read and written
 // (a library copy of the logits alone 100 us): bound by memory.  16-bit logits come
 // near the vector instructions, 25 for a token: 256 x 262,144 bfloat16 to float32 84 us,
-// 4.9 TB/s.  61 x 100,257 float16 take 13 us, where all tiles are resident at
-// once and the list, the biases and the barriers between them add 5 us to the copy's 8.
+// 4.9 TB/s.  61 x 100,257 float16 take 12 us, where all tiles are resident at
+// once and the list, the biases and the barriers between them add 4 us to the copy's 8.
 template <class I, class O, int T, int N>
 __global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles) {
   constexpr int TOKENS = T * SH_VEC * N;  // of a tile

@@ -160,7 +160,7 @@ typedef struct tt_shape_args {
   const int32_t* seen;         /* token sets [rows] of the prompts; NULL: none */
   int64_t seen_stride;
   const int32_t* generated;    /* [rows][generated_cap] tokens generated so far; NULL: none */
-  int64_t generated_stride, generated_cap;
+  int64_t generated_stride, generated_cap;  /* cap 0 .. 2^30 */
   const int32_t* n_generated;  /* [rows], taken into 0 .. generated_cap; NULL: generated_cap */
   const float* repetition;     /* [rows] rho; NULL: 1 */
   const float* frequency;      /* [rows] phi; NULL: 0 */
@@ -168,7 +168,7 @@ typedef struct tt_shape_args {
   const int64_t* bias_offsets; /* [rows + 1] biases of row r are entries bias_offsets[r] .. bias_offsets[r+1]; NULL: none */
   const int32_t* bias_ids;     /* [n_bias] */
   const float* bias_values;    /* [n_bias] */
-  int64_t n_bias;
+  int64_t n_bias;              /* 0 .. 2^30 */
   const int32_t* allowed;      /* token sets [allowed_count]; NULL: every token is allowed */
   int64_t allowed_stride, allowed_count;
   const int32_t* allowed_rows; /* [rows] which set each row goes by, or TT_STATE_FREE; NULL: set r */

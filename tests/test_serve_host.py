@@ -122,7 +122,7 @@ SHAPE = dict(logits=P, logits_stride=100, out=2 * P, out_stride=100, rows=3, voc
     (dict(generated_cap=-1), tt.TT_EINVAL), (dict(n_bias=-1), tt.TT_EINVAL), (dict(bias_ids=0), tt.TT_EINVAL),
     (dict(bias_values=0), tt.TT_EINVAL), (dict(allowed_count=-1), tt.TT_EINVAL), (dict(seen_stride=-1), tt.TT_EINVAL),
     (dict(vocab=(1 << 24) + 1), tt.TT_ETOOBIG), (dict(rows=(1 << 24) + 1), tt.TT_ETOOBIG),
-    (dict(n_bias=1 << 31), tt.TT_ETOOBIG), (dict(rows=0), tt.TT_OK), (dict(vocab=0), tt.TT_OK)])
+    (dict(n_bias=(1 << 30) + 1), tt.TT_ETOOBIG), (dict(generated_cap=(1 << 30) + 1), tt.TT_ETOOBIG), (dict(rows=0), tt.TT_OK), (dict(vocab=0), tt.TT_OK)])
 def test_shape_refuses(lib, change, code):
     args = dict(SHAPE, **change)
     assert list(args) == list(SHAPE)
