@@ -594,7 +594,7 @@ constexpr int GM_TOKENS = GM_THREADS * GM_CHUNKS;  // of a workgroup
 constexpr int GM_WORDS = GM_TOKENS / 32;
 constexpr int GM_KEYS = 512;                       // by which a workgroup's tokens are ordered
 constexpr int GM_KEEP = 16;                        // bytes of a token that are kept as classes
-constexpr int64_t GM_LDS = 156 * 1024;              // at most, beside 1.3 KB that are always there
+constexpr int64_t GM_LDS = 156 * 1024;              // at most, beside 2.3 KB that are always there
 
 typedef uint32_t Bytes16 __attribute__((ext_vector_type(4)));
 typedef uint32_t Bytes16Any __attribute__((ext_vector_type(4), aligned(1)));  // at any address
@@ -643,7 +643,7 @@ __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const
   StateSets* s_sets = reinterpret_cast<StateSets*>(s_bits + batch * GM_WORDS);
   int16_t* s_next = reinterpret_cast<int16_t*>(s_sets + (sets ? n : 0));
   const int16_t* next = IN_LDS ? s_next : g.next;
-  // the tokens in order of their first class; those that are not walked are left out
+  // the tokens in order; those that are not walked are left out
   const int64_t v0 = (int64_t)(blockIdx.x % tiles) * GM_TOKENS;
   uint16_t* order = reinterpret_cast<uint16_t*>(s_bits);
   int first[GM_CHUNKS], then[GM_CHUNKS], nth[GM_CHUNKS];
@@ -704,7 +704,7 @@ __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const
   uint64_t second[GM_CHUNKS], later[GM_CHUNKS];
 #pragma unroll
   for (int j = 0; j < GM_CHUNKS; ++j) {
-    // a wavefront's chunks are 16 apart, so that all wavefronts share the long runs of one class
+    // a wavefront's chunks are 16 apart, so that the long runs of one class are shared out
     const int i = (j * (GM_THREADS / WAVE) + tid / WAVE) * WAVE + lane;
     t[j] = KeptToken{};
     if (i < walked) {
@@ -743,69 +743,73 @@ __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const
   const int64_t word0 = v0 / 32, words = min(div_up(vocab, 32) - word0, (int64_t)GM_WORDS);
   const int end = g.end_id >= v0 && g.end_id < min(v0 + GM_TOKENS, vocab) ? (int)(g.end_id - v0) : -1;
   for (int64_t r = r0; r < r1; r += batch) {
-   const int batch_rows = (int)min((int64_t)batch, r1 - r);
-   __syncthreads();  // the order is read, or the sets before are written
-   for (int i = tid; i < batch_rows * GM_WORDS; i += GM_THREADS) s_bits[i] = 0;
-   __syncthreads();
-   for (int r64 = 0; r64 < batch_rows; r64 += WAVE) {
-    const int count = min(WAVE, batch_rows - r64);
-    uint32_t* sets_of = s_bits + r64 * GM_WORDS;
-    const int32_t q_lane = lane < count ? states[r + r64 + lane] : TT_STATE_DEAD;
-    const bool good = (uint32_t)q_lane < n;
-    const uint64_t possible = sets && good ? s_sets[q_lane].live : 0;
-    uint64_t free = __ballot(q_lane == TT_STATE_FREE);
-    for (; free && tid < WAVE; free &= free - 1) {
-      static_assert(GM_WORDS == WAVE, "a lane for each word");
-      const int64_t rest = vocab - (word0 + lane) * 32;
-      sets_of[__builtin_ctzll(free) * GM_WORDS + lane] = rest >= 32 ? 0xFFFFFFFFu : rest > 0 ? (1u << rest) - 1u : 0u;
-    }
-    if (end >= 0 && tid < count && good && g.accept[q_lane]) atomicOr(&sets_of[tid * GM_WORDS + (end >> 5)], 1u << (end & 31));
+    const int batch_rows = (int)min((int64_t)batch, r1 - r);
+    __syncthreads();  // the order is read, or the sets before are written
+    for (int i = tid; i < batch_rows * GM_WORDS; i += GM_THREADS) s_bits[i] = 0;
+    __syncthreads();
+    for (int r64 = 0; r64 < batch_rows; r64 += WAVE) {
+      const int count = min(WAVE, batch_rows - r64);
+      uint32_t* sets_of = s_bits + r64 * GM_WORDS;
+      const int32_t q_lane = lane < count ? states[r + r64 + lane] : TT_STATE_DEAD;
+      const bool good = (uint32_t)q_lane < n;
+      const uint64_t possible = sets && good ? s_sets[q_lane].live : 0;
+      uint64_t free = __ballot(q_lane == TT_STATE_FREE);
+      for (; free && tid < WAVE; free &= free - 1) {
+        static_assert(GM_WORDS == WAVE, "a lane for each word");
+        const int64_t rest = vocab - (word0 + lane) * 32;
+        sets_of[__builtin_ctzll(free) * GM_WORDS + lane] = rest >= 32 ? 0xFFFFFFFFu : rest > 0 ? (1u << rest) - 1u : 0u;
+      }
+      if (end >= 0 && tid < count && good && g.accept[q_lane])
+        atomicOr(&sets_of[tid * GM_WORDS + (end >> 5)], 1u << (end & 31));
 #pragma unroll
-    for (int j = 0; j < GM_CHUNKS; ++j) {
-      // the states that each token's first byte leaves alive
-      uint64_t mine = 0, all = 0;
-      if (alike[j]) {  // and of them those that all tokens stay in, and those that some token's second byte leaves alive
-        const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)(t[j].c[0] & 255), lead[j]);
-        const uint32_t q = good ? (uint32_t)(int32_t)next[(uint32_t)q_lane * nc + c] : n;
-        const StateSets m = s_sets[q < n ? q : 0];
-        const bool whole = q < n && (later[j] & ~m.self) == 0;
-        all = __ballot(whole);
-        const uint64_t some = __ballot(q < n && !whole && (single[j] || (m.live & second[j])));
-        if (t[j].len > 0) mine = some;
-      } else {
-        for (uint64_t left = __ballot(t[j].len > 0); left;) {
-          const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)(t[j].c[0] & 255), __builtin_ctzll(left));
-          const bool same = t[j].len > 0 && (t[j].c[0] & 255) == c;
-          bool live = possible >> (c & 63) & 1;
-          if (!sets) live = good && (uint32_t)(int32_t)next[(uint32_t)q_lane * nc + c] < n;
-          const uint64_t states_of = __ballot(live);
-          if (same) mine = states_of;
-          left &= ~__ballot(same);
+      for (int j = 0; j < GM_CHUNKS; ++j) {
+        // the states that each token's first byte leaves alive
+        uint64_t mine = 0, all = 0;
+        if (alike[j]) {
+          // of them, those that all tokens stay in, and those that some token's second byte leaves alive
+          const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)(t[j].c[0] & 255), lead[j]);
+          const uint32_t q = good ? (uint32_t)(int32_t)next[(uint32_t)q_lane * nc + c] : n;
+          const StateSets m = s_sets[q < n ? q : 0];
+          const bool whole = q < n && (later[j] & ~m.self) == 0;
+          all = __ballot(whole);
+          const uint64_t some = __ballot(q < n && !whole && (single[j] || (m.live & second[j])));
+          if (t[j].len > 0) mine = some;
+        } else {
+          for (uint64_t left = __ballot(t[j].len > 0); left;) {
+            const uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)(t[j].c[0] & 255), __builtin_ctzll(left));
+            const bool same = t[j].len > 0 && (t[j].c[0] & 255) == c;
+            bool live = possible >> (c & 63) & 1;
+            if (!sets) live = good && (uint32_t)(int32_t)next[(uint32_t)q_lane * nc + c] < n;
+            const uint64_t states_of = __ballot(live);
+            if (same) mine = states_of;
+            left &= ~__ballot(same);
+          }
+        }
+        const int word = t[j].place >> 5;
+        const uint32_t bit = 1u << (t[j].place & 31);
+        for (; all; all &= all - 1)
+          if (t[j].len > 0) atomicOr(&sets_of[__builtin_ctzll(all) * GM_WORDS + word], bit);
+        while (__any(mine != 0)) {  // each lane walks from its own next state
+          const bool on = mine != 0;
+          const int i = on ? __builtin_ctzll(mine) : 0;
+          mine &= mine - 1;
+          const uint32_t q0 = (uint32_t)__shfl(q_lane, i);
+          uint32_t q = n;
+          if (on) q = (uint32_t)(int32_t)next[q0 * nc + (t[j].c[0] & 255)];
+          bool go = q < n && t[j].len > 1;
+          if (sets && go && (t[j].later & ~s_sets[q].self) == 0) go = false;  // every further byte stays in it
+          q = walk<1>(next, n, nc, t[j], q, go);
+          for (int k = GM_KEEP; go && k < t[j].len && q < n; ++k)
+            q = (uint32_t)(int32_t)next[q * nc + cls[g.strings[t[j].at + k]]];
+          if (q < n) atomicOr(&sets_of[i * GM_WORDS + word], bit);
         }
       }
-      for (; all; all &= all - 1)
-        if (t[j].len > 0) atomicOr(&sets_of[__builtin_ctzll(all) * GM_WORDS + (t[j].place >> 5)], 1u << (t[j].place & 31));
-      while (__any(mine != 0)) {  // each lane walks from its own next state
-        const bool on = mine != 0;
-        const int i = on ? __builtin_ctzll(mine) : 0;
-        mine &= mine - 1;
-        const uint32_t q0 = (uint32_t)__shfl(q_lane, i);
-        uint32_t q = n;
-        if (on) q = (uint32_t)(int32_t)next[q0 * nc + (t[j].c[0] & 255)];
-        bool go = q < n && t[j].len > 1;
-        if (sets && go && (t[j].later & ~s_sets[q].self) == 0) go = false;  // every further byte stays in it
-        q = walk<1>(next, n, nc, t[j], q, go);
-        for (int k = GM_KEEP; go && k < t[j].len && q < n; ++k)
-          q = (uint32_t)(int32_t)next[q * nc + cls[g.strings[t[j].at + k]]];
-        if (q < n) atomicOr(&sets_of[i * GM_WORDS + (t[j].place >> 5)], 1u << (t[j].place & 31));
-      }
     }
-   }
-   __syncthreads();
-   for (int i = tid; i < batch_rows * GM_WORDS; i += GM_THREADS) {
-     const int row = i / GM_WORDS, w = i % GM_WORDS;
-     if (w < words) bits[(r + row) * stride + word0 + w] = (int32_t)s_bits[i];
-   }
+    __syncthreads();
+    for (int i = tid; i < batch_rows * GM_WORDS; i += GM_THREADS) {
+      const int row = i / GM_WORDS, w = i % GM_WORDS;
+      if (w < words) bits[(r + row) * stride + word0 + w] = (int32_t)s_bits[i];
+    }
   }
 }
 
@@ -1044,7 +1048,10 @@ __global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles) {
     }
     typename Pack<O>::type y;
 #pragma unroll
-    for (int k = 0; k < SH_VEC; ++k) y[k] = (O)pick(may, k, sizeof(O) == 4 ? quotient(f[k], divisor, scale) : f[k] * scale, lowest);
+    for (int k = 0; k < SH_VEC; ++k) {
+      const float z = sizeof(O) == 4 ? quotient(f[k], divisor, scale) : f[k] * scale;
+      y[k] = (O)pick(may, k, z, lowest);
+    }
     if (i + SH_VEC <= here) {
       *reinterpret_cast<typename Pack<O>::type*>(from(dst, i)) = y;
     } else {

@@ -162,6 +162,24 @@ def test_grammar_bits_and_advance(states, classes, density, tokens, longest, voc
         assert states_d.tolist() == after
 
 
+@pytest.mark.parametrize("states, classes, rows", [(300, 40, 5000), (700, 60, 3000), (40, 100, 2000)])
+def test_grammar_bits_of_many_rows(states, classes, rows):
+    """More sets than LDS holds at a time, some rows free or dead: each row is its state's of the call for all states."""
+    rng = np.random.default_rng(states)
+    nxt, accept = random_grammar(rng, states, classes, 0.8)
+    strings, data, offsets = random_strings(rng, 60_000, 9)
+    g, t = tt.Grammar(nxt, accept, end_id=60_000), tt.TokenStrings(data, offsets)
+    every = tt.grammar_bits(g, t, vocab=60_003)
+    some = rng.integers(0, states, 3)
+    assert np.array_equal(every.cpu().numpy()[some], so.grammar_bits(nxt, accept, 60_000, strings, some, 60_003))
+    q = rng.integers(-2, states, rows).astype(np.int32)
+    got = tt.grammar_bits(g, t, dev(q), 60_003).cpu().numpy()
+    want = every.cpu().numpy()[np.maximum(q, 0)]
+    want[q == -1] = 0
+    want[q == -2] = so.pack(np.ones((1, 60_003), bool))
+    assert np.array_equal(got, want)
+
+
 def test_grammar_over_the_tokenizer():
     """The loaded tokenizer's own strings; the sets of every state; a token is in a state's set exactly if the step
     over it does not end in the dead state."""
