@@ -715,7 +715,7 @@ __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const
     }
     Bytes16 b = 0;
     if (t[j].len > 0) {
-      if (t[j].at + GM_KEEP <= g.n_bytes) {
+      if ((int64_t)t[j].at + GM_KEEP <= g.n_bytes) {  // strings may be 2^31 - 1 bytes long
         b = *reinterpret_cast<const Bytes16Any*>(g.strings + t[j].at);
       } else {  // at the end of the strings
         for (int k = 0; k < min(t[j].len, GM_KEEP); ++k) b[k / 4] |= (uint32_t)g.strings[t[j].at + k] << (8 * (k % 4));
