@@ -586,8 +586,7 @@ __global__ __launch_bounds__(GR_THREADS) void k_grammar_bits(tt_grammar g, const
 // spaces, mixed beginnings), each a chain of reads of LDS, keep the others of
 // their workgroup waiting, which is what bounds it.  Walking two or four states together
 // in a lane is slower (63 and 69 us where one took 58), and so is skipping bytes that lead
-// back to a state by their classes (84 us where stepping takes 51).  From 64 states on this
-// kernel is no slower than the other.
+// back to a state by their classes (84 us where stepping takes 51).
 constexpr int GM_THREADS = 1024;
 constexpr int GM_CHUNKS = 2;                       // tokens of a thread
 constexpr int GM_TOKENS = GM_THREADS * GM_CHUNKS;  // of a workgroup
@@ -632,14 +631,13 @@ __device__ inline uint32_t walk(const int16_t* next, uint32_t n, uint32_t nc, co
 template <bool IN_LDS>
 __global__ __launch_bounds__(GM_THREADS) void k_grammar_many(tt_grammar g, const int32_t* states, int64_t rows,
                                                              int64_t vocab, int32_t* bits, int64_t stride, int tiles,
-                                                             int64_t per_block, int batch) {
-  // [batch][GM_WORDS] the sets at hand (first, the tokens' order); [n] the states' sets; the automaton
+                                                             int64_t per_block, int batch, bool sets) {
+  // [batch][GM_WORDS] the sets at hand (first, the tokens' order); [n] the states' sets, if `sets`; the automaton
   extern __shared__ __attribute__((aligned(16))) uint32_t s_bits[];
   __shared__ uint8_t cls[256];
   __shared__ uint32_t s_first[GM_KEYS + 1];  // tokens by their first class and three bits of the second
   const int tid = threadIdx.x, lane = tid % WAVE;
   const uint32_t n = (uint32_t)g.n_states, nc = (uint32_t)g.n_classes;
-  const bool sets = nc <= 64;
   StateSets* s_sets = reinterpret_cast<StateSets*>(s_bits + batch * GM_WORDS);
   int16_t* s_next = reinterpret_cast<int16_t*>(s_sets + (sets ? n : 0));
   const int16_t* next = IN_LDS ? s_next : g.next;
@@ -1135,22 +1133,26 @@ hipError_t launch_token_bits(const int32_t* ids, int64_t n, const int64_t* offse
 
 hipError_t launch_grammar_bits(const tt_grammar& g, const int32_t* states, int64_t rows, int32_t* bits,
                                int64_t stride, int64_t vocab, hipStream_t st) {
-  if (rows >= WAVE) {
-    // a workgroup for every CU, each with 64 states at least; as many sets at a time as LDS holds beside the
-    // automaton, which is read from L2 where not even 64 fit beside it
+  // The sets of many states have LDS hold the classes' sets of all states, where there are at most 64 classes and 8,960 states, and
+  // the automaton where it fits beside them, which is read from L2 otherwise.  With the classes' sets 64 rows are no slower
+  // than by k_grammar_bits; without them a wavefront's tokens are tried one class at a time, which pays from about 128 rows
+  // on: 10,000 states of 35 classes take 36 us for 64 rows (k_grammar_bits 27), 37 us for 300 (100) and 0.81 ms for all
+  // (3.2); 2,000 states of 151 classes 101 us for 128 rows (77) and 0.58 ms for all (1.2).
+  const int64_t least = WAVE * GM_WORDS * 4, table = 2 * g.n_states * g.n_classes;
+  const bool sets = g.n_classes <= 64 && 16 * g.n_states + least <= GM_LDS;
+  if (rows >= (sets ? WAVE : 2 * WAVE)) {
+    // a workgroup for every CU, each with 64 states at least; as many sets at a time as LDS holds beside the rest
     const int64_t tiles = div_up(vocab, GM_TOKENS);
     const int64_t parts = min(div_up(rows, WAVE), max((int64_t)1, (int64_t)256 / tiles)), per = div_up(rows, parts);
-    const int64_t table = 2 * g.n_states * g.n_classes, self = g.n_classes <= 64 ? 16 * g.n_states : 0;
-    const bool in_lds = table + self + WAVE * GM_WORDS * 4 <= GM_LDS;
-    const int64_t fixed = self + (in_lds ? table : 0), room = (GM_LDS - fixed) / (WAVE * GM_WORDS * 4) * WAVE;
+    const int64_t self = sets ? 16 * g.n_states : 0;
+    const bool in_lds = table + self + least <= GM_LDS;
+    const int64_t fixed = self + (in_lds ? table : 0), room = (GM_LDS - fixed) / least * WAVE;
     const int64_t batch = min(room, div_up(per, WAVE) * WAVE);
-    if (batch > 0) {
-      auto* k = in_lds ? k_grammar_many<true> : k_grammar_many<false>;
-      hipLaunchKernelGGL(k, dim3((uint32_t)(tiles * div_up(rows, per))), dim3(GM_THREADS),
-                         (size_t)(fixed + batch * GM_WORDS * 4), st, g, states, rows, vocab, bits, stride, (int)tiles, per,
-                         (int)batch);
-      return hipGetLastError();
-    }
+    auto* k = in_lds ? k_grammar_many<true> : k_grammar_many<false>;
+    hipLaunchKernelGGL(k, dim3((uint32_t)(tiles * div_up(rows, per))), dim3(GM_THREADS),
+                       (size_t)(fixed + batch * GM_WORDS * 4), st, g, states, rows, vocab, bits, stride, (int)tiles, per,
+                       (int)batch, sets);
+    return hipGetLastError();
   }
   const int64_t tiles = div_up(vocab, GR_THREADS);
   hipLaunchKernelGGL(k_grammar_bits, dim3((uint32_t)(rows * tiles)), dim3(GR_THREADS), 0, st, g, states, vocab, bits,
