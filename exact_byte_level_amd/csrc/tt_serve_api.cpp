@@ -9,7 +9,7 @@ constexpr int64_t MAX_VOCAB = (int64_t)1 << 24;
 constexpr int64_t MAX_INT32 = 0x7FFFFFFF;
 constexpr int64_t MAX_BLOCK = (int64_t)1 << 20;
 constexpr int64_t MAX_LIST = (int64_t)1 << 30;  // entries of a list that is counted in 32 bits
-constexpr int64_t MAX_GRID = (int64_t)1 << 30;  // workgroups of a launch
+constexpr int64_t MAX_WORDS = (int64_t)1 << 30;  // words of all sets of a call, or that its logits' sets would have
 
 int done(hipError_t e) { return e == hipSuccess ? TT_OK : TT_EHIP; }
 
@@ -71,7 +71,7 @@ int tt_token_bits(const int32_t* ids, int64_t n, const int64_t* offsets, int64_t
   if (vocab > MAX_VOCAB || rows > MAX_ROWS) return TT_ETOOBIG;
   if (rows == 0 || vocab == 0) return TT_OK;
   if (!bits || (rows > 1 && bits_stride < words)) return TT_EINVAL;
-  if (rows * words > MAX_GRID) return TT_ETOOBIG;
+  if (rows * words > MAX_WORDS) return TT_ETOOBIG;
   return done(tt::launch_token_bits(ids, n, offsets, rows, vocab, bits, bits_stride, add != 0, stream));
 }
 
@@ -84,7 +84,7 @@ int tt_grammar_bits(const tt_grammar* grammar, const int32_t* states, int64_t ro
   if (rows == 0 || vocab == 0) return TT_OK;
   const int64_t words = (vocab + 31) / 32;
   if (!bits || (rows > 1 && bits_stride < words)) return TT_EINVAL;
-  if (rows * words > MAX_GRID) return TT_ETOOBIG;
+  if (rows * words > MAX_WORDS) return TT_ETOOBIG;
   return done(tt::launch_grammar_bits(*grammar, states, rows, bits, bits_stride, vocab, stream));
 }
 
@@ -115,7 +115,7 @@ int tt_shape_logits(const tt_shape_args* args, hipStream_t stream) {
   if (a.n_bias < 0 || (a.bias_offsets && a.n_bias > 0 && (!a.bias_ids || !a.bias_values))) return TT_EINVAL;
   if (a.allowed && (a.allowed_count < 0 || a.allowed_stride < 0)) return TT_EINVAL;
   if (a.generated_cap > MAX_LIST || a.n_bias > MAX_LIST) return TT_ETOOBIG;
-  if (a.rows * words > MAX_GRID) return TT_ETOOBIG;
+  if (a.rows * words > MAX_WORDS) return TT_ETOOBIG;
   return done(tt::launch_shape(a, stream));
 }
 

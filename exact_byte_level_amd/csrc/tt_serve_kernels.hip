@@ -2,12 +2,14 @@
 // shaping of logits (declared in include/tt_serve.h).
 #include "tt_serve_kernels.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace tt {
 namespace {
 
 constexpr int WAVE = 64;
+constexpr int64_t MAX_ITEMS = 0xFFFFFFFF;  // threads that a launch may have in a dimension of its grid
 
 __host__ __device__ inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 __host__ __device__ inline uint32_t div_up32(uint32_t a, uint32_t b) { return a / b + (a % b != 0); }
@@ -458,16 +460,17 @@ __global__ __launch_bounds__(TB_THREADS) void k_token_bits(const int32_t* ids, i
 // texts of the part.  64 texts of two million ids (8 MB) take 11 us and the clearing
 // 1 to 4: a part's loads, its LDS atomics and the atomics on memory follow each other, and
 // there is one part for a CU.  Two words to an atomic on memory is no faster.
+// `first`: the id that the launch's first part begins with.
 __global__ __launch_bounds__(TB_THREADS) void k_token_bits_split(const int32_t* ids, int64_t n, const int64_t* offsets,
                                                                  int64_t rows, int64_t vocab, int32_t* bits,
-                                                                 int64_t stride) {
+                                                                 int64_t stride, int64_t first) {
   extern __shared__ uint32_t set[];
   // texts that reach into the part, of the 1,024 at hand, and their ids in it
   __shared__ int s_row[TB_THREADS];
   __shared__ int s_lo[TB_THREADS], s_hi[TB_THREADS];
   __shared__ int s_rows;
   const int tid = threadIdx.x, words = (int)div_up(vocab, 32);
-  const int64_t t0 = (int64_t)blockIdx.x * TB_BATCH, t1 = min(t0 + TB_BATCH, n);
+  const int64_t t0 = first + (int64_t)blockIdx.x * TB_BATCH, t1 = min(t0 + TB_BATCH, n);
   const bool in_lds = words <= TB_WORDS;
   const int least = max(words / 4, WAVE);  // ids that are worth a set in LDS
   // n is more than a part: the last part's loads reach back
@@ -1078,6 +1081,8 @@ void enqueue_shape(const tt_shape_args& a, hipStream_t st) {
 
 }  // namespace
 
+// In the launchers min and max are std's: HIP's own take ints on the host.
+
 // What is written where it was read has to wait until every workgroup has
 // read it: it gets a launch of its own.  Otherwise one more workgroup, without
 // places, writes lengths and counts beside the others.
@@ -1119,15 +1124,19 @@ hipError_t launch_token_bits(const int32_t* ids, int64_t n, const int64_t* offse
   // 11 us), 250 texts of two million 8.5 us (12 us).  Fewer and longer ones are dealt out: 64 texts of two
   // million ids take 12.6 us (one workgroup each 21 us), one text of two million 12 us (216 us).
   if (n < TB_SPLIT || n < TB_LONG * rows) {
-    hipLaunchKernelGGL(k_token_bits, dim3((uint32_t)(rows * tiles)), dim3(TB_THREADS), lds, st, ids, n, offsets, vocab,
-                       bits, stride, (int)tiles, add);
+    const int64_t most = MAX_ITEMS / TB_THREADS / tiles;  // texts of a launch
+    for (int64_t r = 0; r < rows; r += most)
+      hipLaunchKernelGGL(k_token_bits, dim3((uint32_t)(std::min(most, rows - r) * tiles)), dim3(TB_THREADS), lds, st, ids, n,
+                         offsets ? offsets + r : nullptr, vocab, bits + r * stride, stride, (int)tiles, add);
     return hipGetLastError();
   }
   if (!add)
-    hipLaunchKernelGGL(k_clear_bits, dim3((uint32_t)div_up(words, 256), (uint32_t)min(rows, (int64_t)32768)), dim3(256),
+    hipLaunchKernelGGL(k_clear_bits, dim3((uint32_t)div_up(words, 256), (uint32_t)std::min(rows, (int64_t)32768)), dim3(256),
                        0, st, bits, rows, words, stride);
-  hipLaunchKernelGGL(k_token_bits_split, dim3((uint32_t)div_up(n, TB_BATCH)), dim3(TB_THREADS), lds, st, ids, n, offsets,
-                     rows, vocab, bits, stride);
+  const int64_t most = MAX_ITEMS / TB_THREADS * TB_BATCH;  // ids of a launch
+  for (int64_t t = 0; t < n; t += most)
+    hipLaunchKernelGGL(k_token_bits_split, dim3((uint32_t)div_up(std::min(most, n - t), TB_BATCH)), dim3(TB_THREADS), lds, st, ids,
+                       n, offsets, rows, vocab, bits, stride, t);
   return hipGetLastError();
 }
 
@@ -1143,11 +1152,11 @@ hipError_t launch_grammar_bits(const tt_grammar& g, const int32_t* states, int64
   if (rows >= (sets ? WAVE : 2 * WAVE)) {
     // a workgroup for every CU, each with 64 states at least; as many sets at a time as LDS holds beside the rest
     const int64_t tiles = div_up(vocab, GM_TOKENS);
-    const int64_t parts = min(div_up(rows, WAVE), max((int64_t)1, (int64_t)256 / tiles)), per = div_up(rows, parts);
+    const int64_t parts = std::min(div_up(rows, WAVE), std::max((int64_t)1, (int64_t)256 / tiles)), per = div_up(rows, parts);
     const int64_t self = sets ? 16 * g.n_states : 0;
     const bool in_lds = table + self + least <= GM_LDS;
     const int64_t fixed = self + (in_lds ? table : 0), room = (GM_LDS - fixed) / least * WAVE;
-    const int64_t batch = min(room, div_up(per, WAVE) * WAVE);
+    const int64_t batch = std::min(room, div_up(per, WAVE) * WAVE);
     auto* k = in_lds ? k_grammar_many<true> : k_grammar_many<false>;
     hipLaunchKernelGGL(k, dim3((uint32_t)(tiles * div_up(rows, per))), dim3(GM_THREADS),
                        (size_t)(fixed + batch * GM_WORDS * 4), st, g, states, rows, vocab, bits, stride, (int)tiles, per,

@@ -89,3 +89,39 @@ def test_every_state_of_a_large_automaton_over_a_large_vocabulary():
     assert torch.equal(every[dev(some).long()], tt.grammar_bits(g, t, dev(some), 262_144))
     two = some[[0, -1]]
     assert np.array_equal(every[dev(two).long()].cpu().numpy(), so.grammar_bits(nxt, accept, 262_143, strings, two, 262_144))
+
+
+@pytest.mark.parametrize("add", [False, True])
+def test_token_bits_of_four_million_texts(add):
+    """More texts than workgroups of 1,024 threads fit one launch."""
+    rows, vocab = 2**22 + 5, 40
+    g = torch.Generator("cuda").manual_seed(3)
+    new = torch.randint(0, 4, (rows,), device="cuda", generator=g)
+    offsets = torch.zeros(rows + 1, dtype=torch.int64, device="cuda")
+    offsets[1:] = torch.cumsum(new, 0)
+    n = int(offsets[-1])
+    ids = torch.randint(-1, vocab + 2, (n,), device="cuda", generator=g)
+    member = torch.zeros((rows, 64), dtype=torch.bool, device="cuda")
+    fine = (ids >= 0) & (ids < vocab)
+    member[torch.repeat_interleave(torch.arange(rows, device="cuda"), new)[fine], ids[fine]] = True
+    place = torch.ones(32, dtype=torch.int64, device="cuda") << torch.arange(32, device="cuda")
+    want = torch.stack([(member[:, k:k + 32] * place).sum(1).to(torch.int32) for k in (0, 32)], 1)
+    del member
+    bits = torch.full((rows, 2), 0x50, dtype=torch.int32, device="cuda")
+    tt.token_bits_into(ids.int(), bits, vocab, offsets=offsets, add=add)
+    assert torch.equal(bits, want | 0x50 if add else want)
+
+
+def test_token_bits_of_a_text_of_more_than_2_to_35_ids():
+    """A text whose parts are more than one launch holds: ids at its ends and around the place where the second begins."""
+    n = 2**35 + 9000
+    if torch.cuda.mem_get_info()[0] < 4 * n + 2**34:
+        pytest.skip("needs 145 GB of free memory")
+    ids = torch.empty(n, dtype=torch.int32, device="cuda")
+    ids.fill_(-1)
+    second = (2**32 - 1) // 1024 * 8192
+    marks = [0, 8191, 8192, 2**33, second - 1, second, second + 8191, second + 8192, n - 5, n - 1]
+    for k, at in enumerate(marks):
+        ids[at] = 37 * k
+    got = tt.token_bits(ids, 1000).cpu().numpy()
+    assert np.flatnonzero(so.unpack(got, 1000)[0]).tolist() == [37 * k for k in range(len(marks))]
