@@ -881,11 +881,11 @@ __device__ inline T* from(T* row, uint32_t i) {
 // 4.9 TB/s.  61 x 100,257 float16 take 12 us, where all tiles are resident at
 // once and the list, the biases and the barriers between them add 4 us to the copy's 8.
 template <class I, class O, int T, int N>
-__global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles) {
+__global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles, int64_t first_row) {
   constexpr int TOKENS = T * SH_VEC * N;  // of a tile
   __shared__ __attribute__((aligned(16))) uint32_t s_word[TOKENS];
   __shared__ int s_hit[2];  // some entry names a token of the tile; some generated token is in it
-  const int64_t r = blockIdx.x / tiles;
+  const int64_t r = first_row + blockIdx.x / tiles;
   const int tid = threadIdx.x;
   const uint32_t vocab = (uint32_t)a.vocab, v0 = blockIdx.x % tiles * (uint32_t)TOKENS;
   const uint32_t here = min((uint32_t)TOKENS, vocab - v0);
@@ -1066,7 +1066,10 @@ __global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles) {
 template <class I, class O, int T, int N>
 void enqueue_tiles(const tt_shape_args& a, hipStream_t st) {
   const int64_t tiles = div_up(a.vocab, T * SH_VEC * N);
-  hipLaunchKernelGGL((k_shape<I, O, T, N>), dim3((uint32_t)(a.rows * tiles)), dim3(T), 0, st, a, (int)tiles);
+  const int64_t most = MAX_ITEMS / T / tiles;  // rows of a launch
+  for (int64_t r = 0; r < a.rows; r += most)
+    hipLaunchKernelGGL((k_shape<I, O, T, N>), dim3((uint32_t)(std::min(most, a.rows - r) * tiles)), dim3(T), 0, st, a,
+                       (int)tiles, r);
 }
 
 // Tiles of 4,096 tokens once they fill the card, since every tile reads the

@@ -125,3 +125,18 @@ def test_token_bits_of_a_text_of_more_than_2_to_35_ids():
         ids[at] = 37 * k
     got = tt.token_bits(ids, 1000).cpu().numpy()
     assert np.flatnonzero(so.unpack(got, 1000)[0]).tolist() == [37 * k for k in range(len(marks))]
+
+
+def test_logits_of_sixteen_million_rows():
+    """As many rows as are allowed, one workgroup more than a launch holds; in place, row r by set r."""
+    rows = 2**24
+    g = torch.Generator("cuda").manual_seed(4)
+    x = torch.randn((rows, 3), device="cuda", generator=g)
+    allowed = torch.randint(0, 8, (rows, 1), device="cuda", generator=g).int()
+    seen = torch.randint(0, 8, (rows, 1), device="cuda", generator=g).int()
+    half = torch.full((rows,), 0.5, device="cuda")
+    place = torch.arange(3, device="cuda", dtype=torch.int32)
+    want = torch.where((seen >> place) & 1 == 1, torch.where(x > 0, x * 2, x / 2), x) * 2  # by powers of two: exact
+    want[(allowed >> place) & 1 == 0] = -float("inf")
+    tt.shape_logits_into(x, x, seen=seen, repetition=half, allowed=allowed, temperature=half)
+    assert torch.equal(x, want)

@@ -76,7 +76,7 @@ CASES = [
     bits(9_000, 64, 9_000, 262_144), bits(100, 3, MOST, 64), bits(32_767, 64, MOST, 1), bits(32_767, 256, 63, MOST), bits(32_767, 64, 64, MOST),
     token_bits(10, (1 << 22) - 1, 32), token_bits(10, 1 << 22, 32), token_bits(10, MOST, 64), token_bits(1 << 31, 60, MOST),
     token_bits((1 << 35) - 1, 1, 1000, offsets=False), token_bits((1 << 35) + 8193, 1, 1000, offsets=False), token_bits(1 << 36, 1000, 1 << 20),
-    shape(MOST - 1, 1), shape(64, MOST, (1, 0)), shape(1, MOST),
+    shape(MOST - 1, 1), shape(MOST, 1), shape(MOST, 2048, (2, 2)), shape(64, MOST, (1, 0)), shape(1, MOST),
     plan(MOST, (1 << 31) - 1, True, True), plan(MOST, MOST, False, False), plan(1, 1, False, True),
     ["tt_release_blocks", [P, P, MOST, 1, P, 0x7FFFFFFF, 0x7FFFFFFF, P, 1 << 30, P, P, P, P, 0]],
     ["tt_grammar_advance", [grammar(5, 5, 5), P, P, MOST, P, 0]],
