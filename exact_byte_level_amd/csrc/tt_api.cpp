@@ -283,8 +283,8 @@ int session_full(tt_session* s, int64_t n, hipStream_t st) {
   return session_read_info(s, st);
 }
 
-// Sizes of the loaded tokenizer's token strings and, if asked for, the
-// strings, put together from the operands of every merge.
+// Sizes of the loaded tokenizer's token strings or, if the sizes are still
+// those given, the strings, put together from the operands of every merge.
 int vocab_strings(int64_t* n_tokens, int64_t* n_bytes, uint8_t* bytes, int32_t* offsets) {
   const int rc = check_stream_state();
   if (rc != TT_OK) return rc;
@@ -303,9 +303,12 @@ int vocab_strings(int64_t* n_tokens, int64_t* n_bytes, uint8_t* bytes, int32_t* 
       at[t + 1] = at[t] + len;
       if (at[t + 1] > 0x7FFFFFFF) return TT_ETOOBIG;
     }
-    *n_tokens = (int64_t)(256 + M);
-    *n_bytes = at[256 + M];
-    if (!bytes) return TT_OK;
+    if (!bytes) {
+      *n_tokens = (int64_t)(256 + M);
+      *n_bytes = at[256 + M];
+      return TT_OK;
+    }
+    if (*n_tokens != (int64_t)(256 + M) || *n_bytes != at[256 + M]) return TT_ESTALE;
     for (size_t t = 0; t < 256; ++t) bytes[t] = (uint8_t)t;
     for (size_t t = 256; t < 256 + M; ++t) {
       const size_t x = (uint32_t)kids[t - 256], y = kids[t - 256] >> 32;
@@ -939,10 +942,9 @@ int tt_vocab_size(int64_t* n_tokens, int64_t* n_bytes) {
   return vocab_strings(n_tokens, n_bytes, nullptr, nullptr);
 }
 
-int tt_vocab_strings(uint8_t* bytes, int32_t* offsets) {
+int tt_vocab_strings(uint8_t* bytes, int32_t* offsets, int64_t n_tokens, int64_t n_bytes) {
   std::lock_guard<std::mutex> lock(g_mu);
-  if (!bytes || !offsets) return TT_EINVAL;
-  int64_t n_tokens = 0, n_bytes = 0;
+  if (!bytes || !offsets || n_tokens < 0 || n_bytes < 0) return TT_EINVAL;
   return vocab_strings(&n_tokens, &n_bytes, bytes, offsets);
 }
 
@@ -964,7 +966,7 @@ const char* tt_strerror(int code) {
     case TT_ENOTLOADED: return "no tokenizer loaded";
     case TT_EOFFSETS: return "invalid batch offsets";
     case TT_ETOOBIG: return "size beyond library limits";
-    case TT_ESTALE: return "tokenizer replaced since the session began";
+    case TT_ESTALE: return "tokenizer replaced since the session began or its sizes were read";
     case TT_EUNSUPPORTED: return "input case not decided by the o200k-style GPU rules";
     case TT_ENOBLOCKS: return "not enough free blocks";
     default: return "unknown error";

@@ -21,7 +21,7 @@ import struct
 
 import numpy as np
 
-from . import TTError, TT_OK, _check, lib as _base_lib
+from . import TTError, TT_ESTALE, TT_OK, _check, lib as _base_lib
 
 STATE_DEAD, STATE_FREE = -1, -2
 
@@ -44,7 +44,8 @@ def _start():
     bind.connect(*(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
         "tt_plan_blocks", "tt_release_blocks", "tt_token_bits", "tt_grammar_bits", "tt_grammar_advance",
         "tt_shape_logits")))
-    L.tt_vocab_size.argtypes = L.tt_vocab_strings.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    L.tt_vocab_size.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    L.tt_vocab_strings.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64]
     _torch = torch
     _bind = bind
     return bind
@@ -194,9 +195,12 @@ class TokenStrings:
             _start()
         L = _base_lib()
         n, size = ctypes.c_int64(), ctypes.c_int64()
-        _check(L.tt_vocab_size(ctypes.byref(n), ctypes.byref(size)), "tt_vocab_size")
-        strings, offsets = np.empty(size.value, np.uint8), np.empty(n.value + 1, np.int32)
-        _check(L.tt_vocab_strings(strings.ctypes.data, offsets.ctypes.data), "tt_vocab_strings")
+        rc = TT_ESTALE
+        while rc == TT_ESTALE:  # another thread has loaded another tokenizer in between
+            _check(L.tt_vocab_size(ctypes.byref(n), ctypes.byref(size)), "tt_vocab_size")
+            strings, offsets = np.empty(size.value, np.uint8), np.empty(n.value + 1, np.int32)
+            rc = L.tt_vocab_strings(strings.ctypes.data, offsets.ctypes.data, n, size)
+        _check(rc, "tt_vocab_strings")
         return cls(strings, offsets, device)
 
 

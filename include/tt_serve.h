@@ -196,9 +196,10 @@ int tt_shape_logits(const tt_shape_args* args, hipStream_t stream);
  * length of their strings.  Reads the device, so it waits for it. */
 int tt_vocab_size(int64_t* n_tokens, int64_t* n_bytes);
 
-/* tt_vocab_strings -- the strings, to host buffers: bytes[n_bytes], offsets[n_tokens + 1].
- * Returns TT_OK, TT_EINVAL, TT_ENOTLOADED, TT_ENOMEM, TT_ETOOBIG (strings beyond 2^31 - 1 bytes) or TT_EHIP. */
-int tt_vocab_strings(uint8_t* bytes, int32_t* offsets);
+/* tt_vocab_strings -- the strings, to host buffers: bytes[n_bytes], offsets[n_tokens + 1], with the sizes that
+ * tt_vocab_size gave.  TT_ESTALE, and nothing written, if the tokenizer that is loaded by now has others.
+ * Returns TT_OK, TT_EINVAL, TT_ENOTLOADED, TT_ESTALE, TT_ENOMEM, TT_ETOOBIG (strings beyond 2^31 - 1 bytes) or TT_EHIP. */
+int tt_vocab_strings(uint8_t* bytes, int32_t* offsets, int64_t n_tokens, int64_t n_bytes);
 
 #ifdef __cplusplus
 }
