@@ -855,10 +855,41 @@ __device__ inline float pick(uint32_t bits, int k, float a, float b) {
   return d;
 }
 
-// x / d, by its reciprocal: the product and its remainder's share.
-__device__ inline float quotient(float x, float d, float reciprocal) {
-  const float q = x * reciprocal, fixed = fmaf(fmaf(-q, d, x), reciprocal, q);
-  return fabsf(q) < __builtin_inff() ? fixed : q;  // an infinity has no remainder
+// Whether quotients by d may go by its reciprocal.
+__device__ inline bool has_reciprocal(float d) { return fabsf(d) >= 0x1p-20f && fabsf(d) <= 0x1p100f; }
+
+// Quotients of eight values, as exact as divisions: the product with the reciprocal, put right by its remainder's share, where that
+// is exact (a multiple of 2^-47 of the value) and no finite value has an infinite product.  Values outside the bounds, a
+// zero among them, whose sign would be lost, are divided; infinities, which have no remainder, are only passed over.
+__device__ inline void quotients(const float (&x)[SH_VEC], float d, float reciprocal, bool by_reciprocal, float (&y)[SH_VEC]) {
+  constexpr float LEAST = 0x1p-100f, MOST = 0x1p100f;
+  float lo = fabsf(x[0]), hi = lo;
+#pragma unroll
+  for (int k = 1; k < SH_VEC; ++k) {
+    lo = fminf(lo, fabsf(x[k]));
+    hi = fmaxf(hi, fabsf(x[k]));
+  }
+  if (by_reciprocal && lo >= LEAST && hi <= MOST) {
+#pragma unroll
+    for (int k = 0; k < SH_VEC; ++k) {
+      const float q = x[k] * reciprocal;
+      y[k] = fmaf(fmaf(-q, d, x[k]), reciprocal, q);
+    }
+    return;
+  }
+  hi = 0.0f;
+#pragma unroll
+  for (int k = 0; k < SH_VEC; ++k) hi = fmaxf(hi, fabsf(fmaf(x[k], 0.0f, x[k])));  // NaN, which max passes over, for an infinity
+  if (by_reciprocal && lo >= LEAST && hi <= MOST) {
+#pragma unroll
+    for (int k = 0; k < SH_VEC; ++k) {
+      const float q = x[k] * reciprocal, fixed = fmaf(fmaf(-q, d, x[k]), reciprocal, q);
+      y[k] = fabsf(q) < __builtin_inff() ? fixed : q;
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < SH_VEC; ++k) y[k] = x[k] / d;
 }
 
 // Element i of a row, by a 32-bit offset (rows are shorter than 2^32 bytes).
@@ -990,15 +1021,12 @@ __global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles, int6
       }
   }
 
-  // Quotients by rho and by the temperature go by the reciprocal: where the
-  // result stays in 32 bits put right by the remainder, which leaves them half a step
-  // off as a division does, else as a mere product, up to one step of 32 bits off, far below
-  // a step of 16.  Where a reciprocal is not an ordinary number both are divisions.
+  // Quotients by rho and by the temperature go by the reciprocal.  Where the result stays in 32 bits they are put right by the
+  // remainder, and vectors with a value that this does not serve are divided; where it has 16 they are mere products, each off
+  // by up to 2^-23 of the value at hand (a division 2^-24), before the one rounding to 16.
   const float inv_rho = 1.0f / rho, inv_temp = 1.0f / temp;
-  const bool plain_rho = !(fabsf(rho) >= 0x1p-100f && fabsf(rho) <= 0x1p100f);
-  const bool plain_temp = temp > 0.0f && !(temp >= 0x1p-100f && temp <= 0x1p100f);
-  const bool scaled = temp > 0.0f && !plain_temp;
-  const float scale = scaled ? inv_temp : 1.0f, divisor = scaled ? temp : 1.0f;
+  const bool plain_rho = !has_reciprocal(rho), plain_temp = temp > 0.0f && !has_reciprocal(temp);
+  const float scale = temp > 0.0f && !plain_temp ? inv_temp : 1.0f;
   const float lowest = -__builtin_inff();
   O* dst = static_cast<O*>(a.out) + r * a.out_stride + v0;
 #pragma unroll
@@ -1020,17 +1048,17 @@ __global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles, int6
 #pragma unroll
       for (int k = 0; k < SH_VEC; ++k) was |= (c[k] != 0) << k;
     }
-    if (was && !plain_rho) {
+    if (sizeof(O) == 4 && was) {
+      float y[SH_VEC];
+      quotients(f, rho, inv_rho, !plain_rho, y);
 #pragma unroll
-      for (int k = 0; k < SH_VEC; ++k) {
-        if (sizeof(O) == 4) {
-          f[k] = pick(was, k, f[k] > 0.0f ? quotient(f[k], rho, inv_rho) : f[k] * rho, f[k]);
-        } else {
-          f[k] = pick(was, k, f[k] * (f[k] > 0.0f ? inv_rho : rho), f[k]);
-        }
-      }
+      for (int k = 0; k < SH_VEC; ++k) f[k] = pick(was, k, f[k] > 0.0f ? y[k] : f[k] * rho, f[k]);
     }
-    if (was && plain_rho) {
+    if (sizeof(O) == 2 && was && !plain_rho) {
+#pragma unroll
+      for (int k = 0; k < SH_VEC; ++k) f[k] = pick(was, k, f[k] * (f[k] > 0.0f ? inv_rho : rho), f[k]);
+    }
+    if (sizeof(O) == 2 && was && plain_rho) {
 #pragma unroll
       for (int k = 0; k < SH_VEC; ++k) f[k] = pick(was, k, f[k] > 0.0f ? f[k] / rho : f[k] * rho, f[k]);
     }
@@ -1043,16 +1071,19 @@ __global__ __launch_bounds__(T, 6) void k_shape(tt_shape_args a, int tiles, int6
 #pragma unroll
       for (int k = 0; k < SH_VEC; ++k) f[k] += add[j][k];
     }
-    if (plain_temp) {
+    if (sizeof(O) == 4 && temp > 0.0f) {
+      float y[SH_VEC];
+      quotients(f, temp, inv_temp, !plain_temp, y);
+#pragma unroll
+      for (int k = 0; k < SH_VEC; ++k) f[k] = y[k];
+    }
+    if (sizeof(O) == 2 && plain_temp) {
 #pragma unroll
       for (int k = 0; k < SH_VEC; ++k) f[k] /= temp;
     }
     typename Pack<O>::type y;
 #pragma unroll
-    for (int k = 0; k < SH_VEC; ++k) {
-      const float z = sizeof(O) == 4 ? quotient(f[k], divisor, scale) : f[k] * scale;
-      y[k] = (O)pick(may, k, z, lowest);
-    }
+    for (int k = 0; k < SH_VEC; ++k) y[k] = (O)pick(may, k, sizeof(O) == 4 ? f[k] : f[k] * scale, lowest);
     if (i + SH_VEC <= here) {
       *reinterpret_cast<typename Pack<O>::type*>(from(dst, i)) = y;
     } else {
