@@ -9,6 +9,7 @@
 
 #include <cstdarg>
 #include <cstring>
+#include <initializer_list>
 
 #include "tt_serve.h"
 
@@ -120,6 +121,14 @@ struct Call {
     return v;
   }
 
+  // Returns rc after a call that wrote into these tensors (or None): autograd, which may have kept one of them for a
+  // gradient, goes by their versions.
+  int wrote(int rc, std::initializer_list<PyObject*> tensors) {
+    for (PyObject* o : tensors)
+      if (o != Py_None && !THPVariable_Unpack(o).is_inference()) THPVariable_Unpack(o).unsafeGetTensorImpl()->bump_version();
+    return rc;
+  }
+
   // The stream given (its address), or the device's current one.
   hipStream_t stream(PyObject* o) {
     if (!ok) return nullptr;
@@ -170,7 +179,8 @@ PyObject* plan(PyObject*, PyObject* const* v, Py_ssize_t n) {
     a.out_n_free = v[11] == Py_None ? const_cast<int32_t*>(a.n_free)
                                     : (int32_t*)c.vec(v[11], "out_n_free", ScalarType::Int, 1);
     const hipStream_t st = c.stream(v[12]);
-    return c.ok ? tt.plan_blocks(&a, st) : 0;
+    if (!c.ok) return 0;
+    return c.wrote(tt.plan_blocks(&a, st), {v[1], v[5], v[6], v[8], v[9], v[v[10] == Py_None ? 0 : 10], v[v[11] == Py_None ? 3 : 11]});
   });
 }
 
@@ -192,9 +202,10 @@ PyObject* release(PyObject*, PyObject* const* v, Py_ssize_t n) {
     auto* out_lengths = v[7] == Py_None ? lengths : (int32_t*)c.vec(v[7], "out_lengths", ScalarType::Int, rows);
     auto* out_n_free = v[8] == Py_None ? n_free : (int32_t*)c.vec(v[8], "out_n_free", ScalarType::Int, 1);
     const hipStream_t st = c.stream(v[9]);
-    return c.ok ? tt.release_blocks(lengths, done, rows, block_size, table, stride, width, free_blocks, cap, n_free,
-                                    out_lengths, out_n_free, out_n, st)
-                : 0;
+    if (!c.ok) return 0;
+    return c.wrote(tt.release_blocks(lengths, done, rows, block_size, table, stride, width, free_blocks, cap, n_free,
+                                     out_lengths, out_n_free, out_n, st),
+                   {v[3], v[6], v[v[7] == Py_None ? 0 : 7], v[v[8] == Py_None ? 4 : 8]});
   });
 }
 
@@ -209,7 +220,7 @@ PyObject* token_bits(PyObject*, PyObject* const* v, Py_ssize_t n) {
     auto* bits = (int32_t*)c.mat(v[1], "bits", ScalarType::Int, &stride, bounds - 1, (vocab + 31) / 32);
     const int add = PyObject_IsTrue(v[4]);
     const hipStream_t st = c.stream(v[5]);
-    return c.ok ? tt.token_bits(ids, count, offsets, bounds - 1, vocab, bits, stride, add, st) : 0;
+    return c.ok ? c.wrote(tt.token_bits(ids, count, offsets, bounds - 1, vocab, bits, stride, add, st), {v[1]}) : 0;
   });
 }
 
@@ -237,7 +248,7 @@ PyObject* grammar_bits(PyObject*, PyObject* const* v, Py_ssize_t n) {
     auto* states = (const int32_t*)c.vec(v[2], "states", ScalarType::Int, -1, &rows);
     auto* bits = (int32_t*)c.mat(v[3], "bits", ScalarType::Int, &stride, rows, (vocab + 31) / 32);
     const hipStream_t st = c.stream(v[5]);
-    return c.ok ? tt.grammar_bits(&g, states, rows, bits, stride, vocab, st) : 0;
+    return c.ok ? c.wrote(tt.grammar_bits(&g, states, rows, bits, stride, vocab, st), {v[3]}) : 0;
   });
 }
 
@@ -251,7 +262,7 @@ PyObject* grammar_advance(PyObject*, PyObject* const* v, Py_ssize_t n) {
     auto* chosen = (const int32_t*)c.vec(v[3], "chosen", ScalarType::Int, rows);
     auto* out = v[4] == Py_None ? states : (int32_t*)c.vec(v[4], "out_states", ScalarType::Int, rows);
     const hipStream_t st = c.stream(v[5]);
-    return c.ok ? tt.grammar_advance(&g, states, chosen, rows, out, st) : 0;
+    return c.ok ? c.wrote(tt.grammar_advance(&g, states, chosen, rows, out, st), {v[v[4] == Py_None ? 2 : 4]}) : 0;
   });
 }
 
@@ -297,7 +308,7 @@ PyObject* shape(PyObject*, PyObject* const* v, Py_ssize_t n) {
     a.allowed_rows = (const int32_t*)c.vec(v[12], "allowed_rows", ScalarType::Int, a.rows);
     a.temperature = (const float*)c.vec(v[13], "temperature", ScalarType::Float, a.rows);
     const hipStream_t st = c.stream(v[14]);
-    return c.ok ? tt.shape_logits(&a, st) : 0;
+    return c.ok ? c.wrote(tt.shape_logits(&a, st), {v[1]}) : 0;
   });
 }
 

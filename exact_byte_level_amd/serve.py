@@ -7,6 +7,9 @@ current stream (or ``stream``), so they can be captured into a HIP graph; the
 others make their results and, where the device may report a data error, wait
 for it.  Arguments of a wrong type, shape or device raise ValueError.
 
+Nothing is differentiated: results carry no gradient, whatever the logits carry.  What is written in place counts as
+modified, so that a gradient which needs the value from before raises.
+
     ids, offsets = tt.encode_batch(prompts, starts)           # offsets: int64 [B + 1]
     cache = tt.BlockTable(rows=B, width=256, blocks=4096, block_size=16)
     slots, positions, rows = cache.plan(offsets.cuda())
