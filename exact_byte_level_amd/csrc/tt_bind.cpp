@@ -121,6 +121,12 @@ struct Call {
     return v;
   }
 
+  bool truth(PyObject* o) {
+    const int v = ok ? PyObject_IsTrue(o) : 0;
+    if (v < 0) ok = false;
+    return v > 0;
+  }
+
   // Returns rc after a call that wrote into these tensors (or None): autograd, which may have kept one of them for a
   // gradient, goes by their versions.
   int wrote(int rc, std::initializer_list<PyObject*> tensors) {
@@ -218,7 +224,7 @@ PyObject* token_bits(PyObject*, PyObject* const* v, Py_ssize_t n) {
     auto* ids = (const int32_t*)c.vec(v[0], "ids", ScalarType::Int, -1, &count);
     auto* offsets = (const int64_t*)c.vec(v[3], "offsets", ScalarType::Long, -1, &bounds);
     auto* bits = (int32_t*)c.mat(v[1], "bits", ScalarType::Int, &stride, bounds - 1, (vocab + 31) / 32);
-    const int add = PyObject_IsTrue(v[4]);
+    const bool add = c.truth(v[4]);
     const hipStream_t st = c.stream(v[5]);
     return c.ok ? c.wrote(tt.token_bits(ids, count, offsets, bounds - 1, vocab, bits, stride, add, st), {v[1]}) : 0;
   });

@@ -140,3 +140,11 @@ def test_logits_of_sixteen_million_rows():
     want[(allowed >> place) & 1 == 0] = -float("inf")
     tt.shape_logits_into(x, x, seen=seen, repetition=half, allowed=allowed, temperature=half)
     assert torch.equal(x, want)
+
+
+def test_token_bits_of_an_add_that_is_no_truth_value():
+    """Its error is raised, and nothing is written."""
+    bits = torch.full((1, 2), 5, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="ambiguous"):
+        tt.token_bits_into(torch.arange(4, dtype=torch.int32, device="cuda"), bits, 64, add=np.array([1, 2]))
+    assert bits.tolist() == [[5, 5]]
