@@ -171,7 +171,19 @@ def token_bits(ids, vocab, offsets=None, stream=None):
     return bits
 
 
-class TokenStrings:
+class _OnDevice:
+    """Tensors whose addresses the calls take from ``_fields``, packed once.  They stay alive with the object, also where an
+    attribute is set to another tensor (which the calls do not see); a copy points to its own."""
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_fields"}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self._point(*self._tensors)
+
+
+class TokenStrings(_OnDevice):
     """The byte strings of a vocabulary on the GPU: token v is ``strings[offsets[v]:offsets[v + 1]]`` (uint8
     and whole numbers, on the host).  A token without bytes is one that no grammar allows."""
 
@@ -187,9 +199,13 @@ class TokenStrings:
         self.n_tokens = len(offsets) - 1
         self.strings = _torch.from_numpy(strings.copy()).to(device)
         self.offsets = _torch.from_numpy(offsets.astype(np.int32)).to(device)
-        self._device = self.strings.get_device()
-        # the last fields of tt_grammar; the tensors above stay the ones they point to
-        self._fields = struct.pack("=4q", self.strings.data_ptr(), len(strings), self.offsets.data_ptr(), self.n_tokens)
+        self._point(self.strings, self.offsets)
+
+    def _point(self, strings, offsets):
+        self._tensors = strings, offsets
+        self._device = strings.get_device()
+        # the last fields of tt_grammar
+        self._fields = struct.pack("=4q", strings.data_ptr(), strings.numel(), offsets.data_ptr(), self.n_tokens)
 
     @classmethod
     def of_tokenizer(cls, device="cuda"):
@@ -207,7 +223,7 @@ class TokenStrings:
         return cls(strings, offsets, device)
 
 
-class Grammar:
+class Grammar(_OnDevice):
     """An automaton over bytes on the GPU: ``next`` [S, 256] gives the state after each byte, -1 where there is none;
     ``accept`` [S] the states in which an answer may end.  ``end_id`` is the token that ends it (-1: none).
     Bytes that no state tells apart are put into one class, which makes the table small enough for LDS."""
@@ -232,10 +248,14 @@ class Grammar:
         self.classes = _torch.from_numpy(classes).to(device)
         self.next = _torch.from_numpy(np.ascontiguousarray(by_byte[first].T)).to(device)
         self.accept = _torch.from_numpy((accept != 0).astype(np.uint8)).to(device)
-        self._device = self.next.get_device()
-        # the first fields of tt_grammar; the tensors above stay the ones they point to
-        self._fields = struct.pack("=6q", self.classes.data_ptr(), self.next.data_ptr(), self.accept.data_ptr(),
-                                   self.n_states, self.n_classes, self.end_id)
+        self._point(self.classes, self.next, self.accept)
+
+    def _point(self, classes, next, accept):
+        self._tensors = classes, next, accept
+        self._device = next.get_device()
+        # the first fields of tt_grammar
+        self._fields = struct.pack("=6q", classes.data_ptr(), next.data_ptr(), accept.data_ptr(), self.n_states,
+                                   self.n_classes, self.end_id)
 
 
 def _shared_device(grammar, tokens):
