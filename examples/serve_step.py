@@ -43,11 +43,12 @@ def answer(prompts, steps=48, seed=0):
 
     # prompts -> ids, sets of their tokens, blocks of the cache
     bounds = torch.tensor(np.cumsum([0] + [len(p) for p in prompts]), device="cuda")
-    text = torch.frombuffer(bytearray(b"".join(prompts)), dtype=torch.uint8).cuda()
+    text = torch.from_numpy(np.frombuffer(b"".join(prompts), np.uint8).copy()).cuda()
     ids, offsets = tt.encode_batch(text, bounds)
+    width = -(-(int(offsets.diff().max()) + steps) // 16)    # room for the longest prompt and its answer
     offsets = offsets.cuda()
     seen = tt.token_bits(ids, vocab, offsets=offsets)
-    cache = tt.BlockTable(rows, width=64, blocks=64 * rows, block_size=16)
+    cache = tt.BlockTable(rows, width=width, blocks=width * rows, block_size=16)
     slots, positions, row_of = cache.plan(offsets)           # where the model puts the prompts' keys and values
 
     model = torch.randn(vocab, vocab, device="cuda", generator=torch.Generator("cuda").manual_seed(seed)).bfloat16()
@@ -55,7 +56,8 @@ def answer(prompts, steps=48, seed=0):
     n_made = torch.zeros(rows, dtype=torch.int32, device="cuda")
     states = torch.zeros(rows, dtype=torch.int32, device="cuda")
     live = torch.ones(rows, dtype=torch.bool, device="cuda")
-    last = ids[offsets[1:] - 1].long()
+    # the prompts' last tokens; an empty one begins after an end token
+    last = torch.cat([ids, ids.new_full((1,), end)])[torch.where(offsets[1:] > offsets[:-1], offsets[1:] - 1, len(ids))].long()
     fixed = {k: torch.full((rows,), v, device="cuda") for k, v in
              dict(repetition=1.2, frequency=0.3, presence=0.1, temperature=0.8).items()}
     # closing gets likelier than random logits make it
