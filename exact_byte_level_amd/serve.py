@@ -24,7 +24,7 @@ import struct
 
 import numpy as np
 
-from . import TTError, TT_ESTALE, TT_OK, _check, lib as _base_lib
+from . import TTError, TT_ESTALE, TT_ETOOBIG, TT_OK, _check, lib as _base_lib
 
 STATE_DEAD, STATE_FREE = -1, -2
 
@@ -129,8 +129,13 @@ class BlockTable:
     def plan(self, offsets=None, stream=None):
         """(slots, positions, rows) of the new tokens; raises if the device reports an error."""
         with _on(stream):
-            places = self.lengths.numel() if offsets is None else int(offsets[-1].item())
-            dev = self.lengths.device
+            places, dev = self.lengths.numel(), self.lengths.device
+            if offsets is not None:
+                if offsets.shape != (places + 1,):
+                    raise ValueError("offsets: [%d] is needed, got %s" % (places + 1, list(offsets.shape)))
+                places = int(offsets[-1].item())
+                if places > 0x7FFFFFFF:
+                    raise TTError(TT_ETOOBIG, "tt_plan_blocks")
             slots = _torch.empty(max(places, 0), dtype=_torch.int64, device=dev)
             positions, rows = (_torch.empty(max(places, 0), dtype=_torch.int32, device=dev) for _ in range(2))
             out_n = _torch.empty(1, dtype=_torch.int64, device=dev)
@@ -165,7 +170,7 @@ def token_bits(ids, vocab, offsets=None, stream=None):
     if _bind is None:
         _start()
     with _on(stream):
-        bits = _torch.empty((1 if offsets is None else offsets.numel() - 1, _words(vocab)), dtype=_torch.int32,
+        bits = _torch.empty((1 if offsets is None else max(offsets.numel() - 1, 0), _words(vocab)), dtype=_torch.int32,
                             device=ids.device)
         token_bits_into(ids, bits, vocab, offsets=offsets, stream=stream)
     return bits

@@ -148,3 +148,21 @@ def test_token_bits_of_an_add_that_is_no_truth_value():
     with pytest.raises(ValueError, match="ambiguous"):
         tt.token_bits_into(torch.arange(4, dtype=torch.int32, device="cuda"), bits, 64, add=np.array([1, 2]))
     assert bits.tolist() == [[5, 5]]
+
+
+def test_refusals_of_offsets():
+    """Before anything of their size is made."""
+    cache = tt.BlockTable(2, 4, 8, 16)
+    for n in (2**31, 2**40, 2**62):
+        with pytest.raises(tt.TTError) as e:
+            cache.plan(torch.tensor([0, 1, n], device="cuda"))
+        assert e.value.code == tt.TT_ETOOBIG
+    for shape in ((0,), (2,), (4,), (1, 3)):
+        with pytest.raises(ValueError, match="offsets"):
+            cache.plan(torch.zeros(shape, dtype=torch.int64, device="cuda"))
+    with pytest.raises(ValueError, match="offsets"):
+        cache.plan(torch.zeros(3, dtype=torch.int64))
+    assert cache.lengths.tolist() == [-1, -1] and int(cache.n_free) == 8
+    with pytest.raises(tt.TTError) as e:
+        tt.token_bits(torch.zeros(3, dtype=torch.int32, device="cuda"), 40, offsets=torch.zeros(0, dtype=torch.int64, device="cuda"))
+    assert e.value.code == tt.TT_EINVAL
