@@ -195,8 +195,12 @@ class TokenStrings(_OnDevice):
     def __init__(self, strings, offsets, device="cuda"):
         if _bind is None:
             _start()
-        strings = np.ascontiguousarray(np.asarray(strings, dtype=np.uint8).reshape(-1))
-        offsets = np.asarray(offsets).reshape(-1)
+        strings, offsets = np.asarray(strings).reshape(-1), np.asarray(offsets).reshape(-1)
+        if strings.dtype != np.uint8 and len(strings) and not (strings.dtype.kind in "iu" and 0 <= strings.min() and strings.max() <= 255):
+            raise ValueError("strings: bytes, as whole numbers from 0 to 255, are needed")
+        if offsets.dtype.kind not in "iu" and np.any(offsets != np.floor(offsets)):
+            raise ValueError("offsets: whole numbers are needed")
+        strings = np.ascontiguousarray(strings.astype(np.uint8, copy=False))
         if not len(offsets) or offsets[0] < 0 or offsets[-1] > len(strings) or np.any(offsets[1:] < offsets[:-1]):
             raise ValueError("offsets: one more than there are tokens, in order and inside the strings")
         if len(strings) > 0x7FFFFFFF or len(offsets) > (1 << 24) + 1:

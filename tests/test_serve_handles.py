@@ -43,3 +43,22 @@ def test_a_copy_points_to_its_own_tensors(which, again):
     rest = [i for i in range(len(fields)) if i not in places]
     before = struct.unpack("=%dq" % len(fields), handle._fields)
     assert [fields[i] for i in rest] == [before[i] for i in rest]
+
+
+@pytest.mark.parametrize("strings", [[0, 256], [-1, 3], np.array([1.5, 2.0]), np.array([300, 5])])
+def test_strings_that_are_no_bytes_are_refused(strings):
+    with pytest.raises(ValueError, match="strings"):
+        tt.TokenStrings(strings, [0, 1, 2], device="cpu")
+
+
+@pytest.mark.parametrize("offsets", [[0, 0.5, 2], [0, np.nan, 2], [0, 1, np.inf]])
+def test_offsets_that_are_no_whole_numbers_are_refused(offsets):
+    with pytest.raises(ValueError, match="offsets"):
+        tt.TokenStrings(np.arange(2), offsets, device="cpu")
+
+
+def test_strings_of_any_type_that_holds_bytes():
+    for strings in (np.arange(256), np.arange(256, dtype=np.uint8), list(range(256)), np.arange(256, dtype=np.int16)):
+        assert tt.TokenStrings(strings, [0, 200, 256], device="cpu").strings.tolist() == list(range(256))
+    assert tt.TokenStrings([], [0, 0], device="cpu").n_tokens == 1
+    assert tt.TokenStrings(np.arange(3), np.array([0.0, 2.0, 3.0]), device="cpu").offsets.tolist() == [0, 2, 3]
