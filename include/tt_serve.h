@@ -13,9 +13,11 @@
  *    return values are 0 or a negative TT_E* code for argument and launch
  *    errors, data errors are written on the device into the count the caller
  *    reads.  Except for tt_vocab_* no call needs a loaded tokenizer, and calls
- *    on different streams do not disturb each other.
+ *    on different streams do not disturb each other.  tt_vocab_* are
+ *    host-synchronous and may run beside a call that loads another tokenizer.
  *  - A token set is a row of 32-bit words: token id v is bit v & 31 of word
- *    v >> 5, and a vocabulary of V ids takes (V + 31) / 32 words.
+ *    v >> 5, and a vocabulary of V ids takes (V + 31) / 32 words.  A call
+ *    takes at most 2^24 rows, and rows times words of at most 2^30.
  *  - Rows of matrices may be any number of elements apart (the *_stride
  *    arguments; in tt_shape_logits rows that are only read may share their
  *    memory: stride 0), and no alignment beyond that of the element is needed.
@@ -90,7 +92,7 @@ int tt_plan_blocks(const tt_plan_args* args, hipStream_t stream);
 /* tt_release_blocks -- take back the blocks of the requests that ended.
  *
  * Rows r with done[r] != 0 that are in use give back their blocks, row by
- * row in the order of the table, to free_blocks from entry n_free on;
+ * row in the order of the table (whatever it holds, negative entries too), to free_blocks from entry n_free on;
  * out_lengths[r] = -1.  The other rows keep their lengths; the table itself is
  * not touched.  out_n receives the number of blocks, or, with nothing changed,
  * TT_ETOOBIG (a row beyond its width, or more blocks than free_cap has room for) or
