@@ -196,8 +196,10 @@ class TokenStrings(_OnDevice):
         if _bind is None:
             _start()
         strings, offsets = np.asarray(strings).reshape(-1), np.asarray(offsets).reshape(-1)
-        if strings.dtype != np.uint8 and len(strings) and not (strings.dtype.kind in "iu" and 0 <= strings.min() and strings.max() <= 255):
-            raise ValueError("strings: bytes, as whole numbers from 0 to 255, are needed")
+        if strings.dtype != np.uint8 and len(strings):
+            whole = strings.dtype.kind in "biuf" and np.all(strings == np.floor(strings))
+            if not whole or strings.min() < 0 or strings.max() > 255:
+                raise ValueError("strings: bytes, as whole numbers from 0 to 255, are needed")
         if offsets.dtype.kind not in "iu" and np.any(offsets != np.floor(offsets)):
             raise ValueError("offsets: whole numbers are needed")
         strings = np.ascontiguousarray(strings.astype(np.uint8, copy=False))

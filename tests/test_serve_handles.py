@@ -45,7 +45,7 @@ def test_a_copy_points_to_its_own_tensors(which, again):
     assert [fields[i] for i in rest] == [before[i] for i in rest]
 
 
-@pytest.mark.parametrize("strings", [[0, 256], [-1, 3], np.array([1.5, 2.0]), np.array([300, 5])])
+@pytest.mark.parametrize("strings", [[0, 256], [-1, 3], np.array([1.5, 2.0]), np.array([300, 5]), [np.nan, 1], [b"ab"], b"ab"])
 def test_strings_that_are_no_bytes_are_refused(strings):
     with pytest.raises(ValueError, match="strings"):
         tt.TokenStrings(strings, [0, 1, 2], device="cpu")
@@ -58,7 +58,7 @@ def test_offsets_that_are_no_whole_numbers_are_refused(offsets):
 
 
 def test_strings_of_any_type_that_holds_bytes():
-    for strings in (np.arange(256), np.arange(256, dtype=np.uint8), list(range(256)), np.arange(256, dtype=np.int16)):
+    for strings in (np.arange(256), np.arange(256, dtype=np.uint8), list(range(256)), np.arange(256, dtype=np.int16), np.arange(256.0)):
         assert tt.TokenStrings(strings, [0, 200, 256], device="cpu").strings.tolist() == list(range(256))
     assert tt.TokenStrings([], [0, 0], device="cpu").n_tokens == 1
     assert tt.TokenStrings(np.arange(3), np.array([0.0, 2.0, 3.0]), device="cpu").offsets.tolist() == [0, 2, 3]
