@@ -326,3 +326,5 @@ def free():
 from .serve import (STATE_DEAD, STATE_FREE, BlockTable, Grammar, TokenStrings, grammar_advance_into,  # noqa: E402
                     grammar_bits, grammar_bits_into, plan_blocks_into, release_blocks_into, shape_logits,
                     shape_logits_into, token_bits, token_bits_into)
+from .step import (KeyValueCache, attend_cache, attend_cache_into, attend_workspace, sample_tokens,  # noqa: E402
+                   sample_tokens_into, sample_workspace, write_cache_into)

@@ -35,7 +35,9 @@ def build(verbose=False):
     _compile(["hipcc"] + HIPCC_FLAGS + [
         "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-I", GEN,
         os.path.join(CSRC, "tt_kernels.hip"), os.path.join(CSRC, "tt_api.cpp"),
-        os.path.join(CSRC, "tt_serve_kernels.hip"), os.path.join(CSRC, "tt_serve_api.cpp")], LIB, verbose)
+        os.path.join(CSRC, "tt_serve_kernels.hip"), os.path.join(CSRC, "tt_serve_api.cpp"),
+        os.path.join(CSRC, "tt_cache_kernels.hip"), os.path.join(CSRC, "tt_sample_kernels.hip"),
+        os.path.join(CSRC, "tt_step_api.cpp")], LIB, verbose)
     _compile(_bind_command(), BIND, verbose)
     return LIB
 

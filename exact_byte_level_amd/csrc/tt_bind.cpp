@@ -1,5 +1,5 @@
 // tt_bind.cpp -- Python binding of the serving calls: takes tensors, checks
-// them and calls the C ABI (include/tt_serve.h).
+// them and calls the C ABI (include/tt_serve.h, include/tt_step.h).
 //
 // A serving step of one request is a few microseconds on the GPU; reading the
 // dozen tensors of a call from Python costs about 10 us, here one.
@@ -11,7 +11,7 @@
 #include <cstring>
 #include <initializer_list>
 
-#include "tt_serve.h"
+#include "tt_step.h"
 
 namespace {
 
@@ -27,6 +27,15 @@ struct {
   decltype(&tt_shape_logits) shape_logits;
 } tt;
 
+// And those of tt_step.h, set by connect_step().
+struct {
+  decltype(&tt_write_cache) write_cache;
+  decltype(&tt_attend_cache) attend_cache;
+  decltype(&tt_attend_workspace) attend_workspace;
+  decltype(&tt_sample_tokens) sample_tokens;
+  decltype(&tt_sample_workspace) sample_workspace;
+} step;
+
 PyObject* raw_stream = nullptr;  // torch's look-up of a device's current stream
 
 const char* type_name(ScalarType t) {
@@ -38,6 +47,7 @@ const char* type_name(ScalarType t) {
     case ScalarType::BFloat16: return "bfloat16";
     case ScalarType::Bool: return "bool";
     case ScalarType::Byte: return "uint8";
+    case ScalarType::Float8_e4m3fn: return "float8_e4m3fn";
     default: return c10::toString(t);
   }
 }
@@ -112,6 +122,44 @@ struct Call {
     if (count) *count = n;
     if (width) *width = m;
     return t->data_ptr();
+  }
+
+  // Address and strides of a tensor of several dimensions, the entries of the last one behind the other; an extent that is
+  // not negative is needed, the others are written.
+  void* wide(PyObject* o, const char* name, ScalarType type, std::initializer_list<int64_t*> extents, std::initializer_list<int64_t*> strides) {
+    const at::Tensor* t = tensor(o, name);
+    if (!fits(t, name, type, (int)extents.size())) return nullptr;
+    int k = 0;
+    for (int64_t* extent : extents) {
+      const int64_t n = t->size(k);
+      if (*extent >= 0 && n != *extent) fail("%s has %lld entries in dimension %d, not %lld", name, (long long)n, k, (long long)*extent);
+      *extent = n;
+      ++k;
+    }
+    if (t->numel() > 0 && t->size(k - 1) > 1 && t->stride(k - 1) != 1) fail("%s has gaps within its last dimension", name);
+    k = 0;
+    for (int64_t* stride : strides) *stride = t->stride(k++);
+    return t->data_ptr();
+  }
+
+  // A workspace, at least `bytes` long; None if there are none.
+  void* space(PyObject* o, int64_t bytes, int64_t* length) {
+    if (!ok || bytes <= 0) return nullptr;
+    if (o == Py_None) {
+      fail("workspace: %lld bytes are needed", (long long)bytes);
+      return nullptr;
+    }
+    void* at = vec(o, "workspace", ScalarType::Byte, -1, length);
+    if (ok && *length < bytes) fail("workspace has %lld bytes, %lld are needed", (long long)*length, (long long)bytes);
+    if (ok && reinterpret_cast<uintptr_t>(at) % 16) fail("workspace does not start at a multiple of 16 bytes");
+    return at;
+  }
+
+  double real(PyObject* o) {
+    if (!ok) return 0;
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1 && PyErr_Occurred()) ok = false;
+    return v;
   }
 
   int64_t number(PyObject* o) {
@@ -318,24 +366,133 @@ PyObject* shape(PyObject*, PyObject* const* v, Py_ssize_t n) {
   });
 }
 
-// Addresses of the six calls, in the order above.
-PyObject* connect(PyObject*, PyObject* const* v, Py_ssize_t n) {
-  if (n != (Py_ssize_t)(sizeof(tt) / sizeof(void*))) {
+int64_t cache_type(ScalarType t) { return t == ScalarType::Float8_e4m3fn ? TT_E4M3 : t == ScalarType::Float ? -1 : logits_type(t); }
+
+// Keys and values [blocks, block_size, heads, dim] of one type and shape, and their scales.
+void cache_of(Call& c, PyObject* keys, PyObject* values, PyObject* key_scale, PyObject* value_scale, tt_paged_cache& p) {
+  const at::Tensor* k = c.tensor(keys, "key_cache");
+  if (!k) return;
+  p.type = cache_type(k->scalar_type());
+  if (p.type < 0) c.fail("key_cache: float16, bfloat16 or float8_e4m3fn is needed, got %s", type_name(k->scalar_type()));
+  p.blocks = p.block_size = p.heads = p.dim = -1;
+  p.keys = c.wide(keys, "key_cache", k->scalar_type(), {&p.blocks, &p.block_size, &p.heads, &p.dim},
+                  {&p.key_block_stride, &p.key_place_stride, &p.key_head_stride});
+  p.values = c.wide(values, "value_cache", k->scalar_type(), {&p.blocks, &p.block_size, &p.heads, &p.dim},
+                    {&p.value_block_stride, &p.value_place_stride, &p.value_head_stride});
+  p.key_scale = (const float*)c.vec(key_scale, "key_scale", ScalarType::Float, p.heads);
+  p.value_scale = (const float*)c.vec(value_scale, "value_scale", ScalarType::Float, p.heads);
+  if (c.ok && (p.block_size < 1 || p.heads < 1 || p.dim < 8 || p.dim % 8 || p.dim > 256))
+    c.fail("key_cache: places and heads, and heads of 8 to 256 elements in steps of 8, are needed, got [%lld, %lld, %lld, %lld]",
+           (long long)p.blocks, (long long)p.block_size, (long long)p.heads, (long long)p.dim);
+}
+
+// keys, values, slots, key_cache, value_cache, key_scale, value_scale, stream
+PyObject* write_cache(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded(n, 8, [&](Call& c) -> int {
+    tt_write_args a{};
+    c.device(v[0], "keys");
+    const at::Tensor* x = c.tensor(v[0], "keys");
+    if (!x) return 0;
+    cache_of(c, v[3], v[4], v[5], v[6], a.cache);
+    a.in_type = logits_type(x->scalar_type());
+    if (a.in_type < 0 || (a.in_type != TT_F32 && a.cache.type != TT_E4M3 && a.cache.type != a.in_type))
+      c.fail("keys %s to a cache of another type: float32, float16 or bfloat16 to itself, to float8_e4m3fn or from float32 to 16 bits is needed",
+             type_name(x->scalar_type()));
+    a.tokens = -1;
+    a.keys = c.wide(v[0], "keys", x->scalar_type(), {&a.tokens, &a.cache.heads, &a.cache.dim}, {&a.key_stride, &a.key_head_stride});
+    a.values = c.wide(v[1], "values", x->scalar_type(), {&a.tokens, &a.cache.heads, &a.cache.dim}, {&a.value_stride, &a.value_head_stride});
+    if (v[2] == Py_None) c.fail("slots: a tensor is needed");
+    a.slots = (const int64_t*)c.vec(v[2], "slots", ScalarType::Long, a.tokens);
+    const hipStream_t st = c.stream(v[7]);
+    return c.ok ? c.wrote(step.write_cache(&a, st), {v[3], v[4]}) : 0;
+  });
+}
+
+// query, key_cache, value_cache, table, lengths, out, rows, scale, window, softcap, key_scale, value_scale, lse, workspace, stream
+PyObject* attend_cache(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded(n, 15, [&](Call& c) -> int {
+    tt_attend_args a{};
+    c.device(v[0], "query");
+    const at::Tensor* x = c.tensor(v[0], "query");
+    if (!x) return 0;
+    a.type = logits_type(x->scalar_type());
+    cache_of(c, v[1], v[2], v[10], v[11], a.cache);
+    if (a.type <= TT_F32 || (a.cache.type != TT_E4M3 && a.cache.type != a.type))
+      c.fail("query: float16 or bfloat16, as the cache or over float8_e4m3fn, is needed, got %s", type_name(x->scalar_type()));
+    a.queries = a.heads = -1;
+    a.query = c.wide(v[0], "query", x->scalar_type(), {&a.queries, &a.heads, &a.cache.dim}, {&a.query_stride, &a.query_head_stride});
+    a.out = c.wide(v[5], "out", x->scalar_type(), {&a.queries, &a.heads, &a.cache.dim}, {&a.out_stride, &a.out_head_stride});
+    if (c.ok && (a.heads < a.cache.heads || a.heads % a.cache.heads))
+      c.fail("query: a multiple of the cache's %lld heads is needed, got %lld", (long long)a.cache.heads, (long long)a.heads);
+    if (v[3] == Py_None || v[4] == Py_None) c.fail("table and lengths are needed");
+    a.table = (const int32_t*)c.mat(v[3], "table", ScalarType::Int, &a.table_stride, v[6] == Py_None ? a.queries : -1, 0, &a.table_rows, &a.width);
+    a.lengths = (const int32_t*)c.vec(v[4], "lengths", ScalarType::Int, a.queries);
+    a.rows = (const int32_t*)c.vec(v[6], "rows", ScalarType::Int, a.queries);
+    a.scale = c.real(v[7]);
+    a.window = c.number(v[8]);
+    a.softcap = c.real(v[9]);
+    if (c.ok && (a.window < 0 || !(a.softcap >= 0 && a.softcap <= 1e30)))
+      c.fail("a window of 0 or more and a softcap from 0 to 1e30 are needed");
+    a.lse = (float*)c.mat(v[12], "lse", ScalarType::Float, &a.lse_stride, a.queries, a.heads);
+    if (!c.ok) return 0;
+    const int64_t bytes = step.attend_workspace(a.queries, a.heads, a.cache.heads, a.cache.dim);
+    if (bytes < 0) return (int)bytes;
+    a.workspace = c.space(v[13], bytes, &a.workspace_bytes);
+    const hipStream_t st = c.stream(v[14]);
+    return c.ok ? c.wrote(step.attend_cache(&a, st), {v[5], v[12]}) : 0;
+  });
+}
+
+// logits, uniform, tokens, temperature, top_k, top_p, min_p, logprobs, workspace, stream
+PyObject* sample_tokens(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  return guarded(n, 10, [&](Call& c) -> int {
+    tt_sample_args a{};
+    c.device(v[0], "logits");
+    const at::Tensor* x = c.tensor(v[0], "logits");
+    if (!x) return 0;
+    a.type = logits_type(x->scalar_type());
+    if (a.type < 0) c.fail("logits: float32, float16 or bfloat16 is needed, got %s", type_name(x->scalar_type()));
+    a.logits = c.mat(v[0], "logits", x->scalar_type(), &a.logits_stride, -1, 0, &a.rows, &a.vocab);
+    if (v[1] == Py_None || v[2] == Py_None) c.fail("uniform and tokens are needed");
+    a.uniform = (const float*)c.vec(v[1], "uniform", ScalarType::Float, a.rows);
+    a.tokens = (int32_t*)c.vec(v[2], "tokens", ScalarType::Int, a.rows);
+    a.temperature = (const float*)c.vec(v[3], "temperature", ScalarType::Float, a.rows);
+    a.top_k = (const int32_t*)c.vec(v[4], "top_k", ScalarType::Int, a.rows);
+    a.top_p = (const float*)c.vec(v[5], "top_p", ScalarType::Float, a.rows);
+    a.min_p = (const float*)c.vec(v[6], "min_p", ScalarType::Float, a.rows);
+    a.logprobs = (float*)c.vec(v[7], "logprobs", ScalarType::Float, a.rows);
+    if (!c.ok) return 0;
+    const int64_t bytes = step.sample_workspace(a.rows, a.vocab);
+    if (bytes < 0) return (int)bytes;
+    a.workspace = c.space(v[8], bytes, &a.workspace_bytes);
+    const hipStream_t st = c.stream(v[9]);
+    return c.ok ? c.wrote(step.sample_tokens(&a, st), {v[2], v[7]}) : 0;
+  });
+}
+
+template <class F>
+PyObject* connected(F& calls, PyObject* const* v, Py_ssize_t n) {
+  if (n != (Py_ssize_t)(sizeof(calls) / sizeof(void*))) {
     PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
     return nullptr;
   }
-  void* at[sizeof(tt) / sizeof(void*)];
+  void* at[sizeof(calls) / sizeof(void*)];
   for (Py_ssize_t i = 0; i < n; ++i) {
     at[i] = PyLong_AsVoidPtr(v[i]);
     if (PyErr_Occurred()) return nullptr;
   }
-  std::memcpy(&tt, at, sizeof(tt));
+  std::memcpy(&calls, at, sizeof(calls));
   Py_RETURN_NONE;
 }
 
+// Addresses of the six calls, and of the five of tt_step.h, in the order above.
+PyObject* connect(PyObject*, PyObject* const* v, Py_ssize_t n) { return connected(tt, v, n); }
+PyObject* connect_step(PyObject*, PyObject* const* v, Py_ssize_t n) { return connected(step, v, n); }
+
 #define CALL(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CALL(connect),         CALL(plan),  CALL(release), CALL(token_bits), CALL(grammar_bits),
-                         CALL(grammar_advance), CALL(shape), {nullptr, nullptr, 0, nullptr}};
+                         CALL(grammar_advance), CALL(shape), CALL(connect_step),  CALL(write_cache), CALL(attend_cache), CALL(sample_tokens),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,685 @@
+// tt_cache_kernels.hip -- keys and values of a paged cache: written, and
+// attended to (declared in include/tt_step.h).
+#include "tt_step_kernels.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace tt {
+namespace {
+
+constexpr int WAVE = 64;
+constexpr int64_t MAX_ITEMS = 0xFFFFFFFF;  // threads that a launch may have in a dimension of its grid
+
+__host__ __device__ inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// N words at any address.
+template <int N>
+struct Words {
+  typedef uint32_t type __attribute__((ext_vector_type(N), aligned(1)));
+};
+template <>
+struct Words<1> {
+  typedef uint32_t type __attribute__((aligned(1)));
+};
+
+// Division of numbers below 2^31 by one from 1 to 2^20: with s = ceil(log2 d) the factor is above 2^(31+s) / d by at
+// most 1, which adds less than a / 2^31 of a d-th to a / d.
+struct Division {
+  uint32_t divisor, factor, shift;
+};
+Division division(int64_t d) {
+  uint32_t s = 0;
+  while (((int64_t)1 << s) < d) ++s;
+  return {(uint32_t)d, (uint32_t)(((uint64_t)1 << (31 + s)) / (uint64_t)d + 1), 31 + s};
+}
+__device__ inline uint32_t quotient(uint32_t a, Division d) { return (uint32_t)(((uint64_t)a * d.factor) >> d.shift); }
+
+// ------------------------------------------------------------------- writing
+
+constexpr int WR_THREADS = 256;
+
+template <class T>
+struct Eight {
+  typedef T type __attribute__((ext_vector_type(8), aligned(alignof(T))));
+};
+
+// Eight elements, divided by their scale, in the cache's type.
+template <class I, class O>
+__device__ inline void put_eight(typename Eight<I>::type x, const float* scale, int64_t head, O* to) {
+  if constexpr (std::is_same<O, uint8_t>::value) {
+    const float s = scale ? scale[head] : 1.0f;
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float q = (float)x[k] / s;
+      f[k] = q > 448.0f ? 448.0f : q < -448.0f ? -448.0f : q;  // NaN stays
+    }
+    typename Words<2>::type w;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int low = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * k], f[4 * k + 1], 0, false);
+      w[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[4 * k + 2], f[4 * k + 3], low, true);
+    }
+    *reinterpret_cast<typename Words<2>::type*>(to) = w;
+  } else {
+    typename Eight<O>::type y;
+    if (scale) {
+      const float s = scale[head];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = (O)((float)x[k] / s);
+    } else if constexpr (std::is_same<I, O>::value) {
+      y = x;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] = (O)x[k];
+    }
+    *reinterpret_cast<typename Eight<O>::type*>(to) = y;
+  }
+}
+
+// Each thread moves eight keys and the eight values beside them.
+template <class I, class O>
+__global__ __launch_bounds__(WR_THREADS) void k_write(tt_write_args a, uint32_t per_head, uint32_t per_token, int64_t first,
+                                                      int64_t total) {
+  const int64_t at = first + (int64_t)blockIdx.x * WR_THREADS + threadIdx.x;
+  if (at >= total) return;
+  const int64_t token = at / per_token;
+  const uint32_t rest = (uint32_t)(at - token * per_token), head = rest / per_head, d = (rest - head * per_head) * 8;
+  const int64_t slot = a.slots[token];
+  typedef typename Eight<I>::type In;
+  const In k = *reinterpret_cast<const In*>(static_cast<const I*>(a.keys) + token * a.key_stride + head * a.key_head_stride + d);
+  const In v = *reinterpret_cast<const In*>(static_cast<const I*>(a.values) + token * a.value_stride + head * a.value_head_stride + d);
+  if (slot < 0) return;
+  const tt_paged_cache& c = a.cache;
+  const int64_t block = slot <= 0xFFFFFFFF ? (uint32_t)slot / (uint32_t)c.block_size : slot / c.block_size;
+  const int64_t place = slot - block * c.block_size;
+  if (block >= c.blocks) return;
+  put_eight<I, O>(k, c.key_scale, head,
+                  static_cast<O*>(c.keys) + block * c.key_block_stride + place * c.key_place_stride + head * c.key_head_stride + d);
+  put_eight<I, O>(v, c.value_scale, head,
+                  static_cast<O*>(c.values) + block * c.value_block_stride + place * c.value_place_stride + head * c.value_head_stride + d);
+}
+
+// ----------------------------------------------------------------- attention
+//
+// Products go by 16x16x32 matrix instructions, whose lane l holds row (of the first operand) or column (of the second)
+// l % 16 and of the 32 that are summed over those of group g = l / 16, eight of them; of the result it holds column l % 16
+// and rows 4 g .. 4 g + 3.  What is summed over may come in any order that both operands share.
+//
+//   scores:  keys [16 tokens x 32 d] times queries [32 d x 16 heads]: lane (c, g) loads 16 bytes of token c's key, and gets
+//            the scores of head c with tokens 4 g + r.
+//   output:  values [16 d x 32 tokens] times weights [32 tokens x 16 heads], over the tokens that the lane's scores are
+//            of, 4 g + r of two tiles of 16: the weights need no exchange.  Lane (c, g) loads the same d of its eight
+//            tokens, D / 16 of them from c * D / 16 on, and product j takes every j-th: one byte permutation per pair.
+//
+// Keys and values so go from memory to registers without LDS, each read once.
+
+constexpr int AT_THREADS = 256;
+constexpr int AT_WAVES = AT_THREADS / WAVE;
+constexpr int AT_TILE = 32;                  // tokens of a wavefront at a time
+constexpr int AT_UNIT = AT_TILE * AT_WAVES;  // tokens of a workgroup at a time
+constexpr int AT_HEADS = 16;                 // query heads of a workgroup
+constexpr int AT_QUERIES = 1024;             // most queries of a call whose tokens are dealt out
+constexpr int AT_GROUPS = 512;               // workgroups that they are dealt out to
+
+// How a call is cut up.
+struct AttendShape {
+  int group, parts, rows;  // query heads of a head of keys; workgroups that they take; heads of a workgroup
+  int64_t lanes;           // heads of keys times parts
+  int workers;             // workgroups that the tokens of each lane are dealt out to; 0: one for each query
+};
+
+AttendShape attend_shape(int64_t queries, int64_t heads, int64_t cache_heads) {
+  AttendShape s;
+  s.group = (int)(heads / cache_heads);
+  s.parts = (int)div_up(s.group, AT_HEADS);
+  s.rows = std::min(s.group, AT_HEADS);
+  s.lanes = cache_heads * s.parts;
+  const bool deal = queries <= AT_QUERIES && queries * s.lanes < 8 * AT_GROUPS;
+  s.workers = deal ? (int)std::max((int64_t)1, AT_GROUPS / s.lanes) : 0;
+  return s;
+}
+
+int padded(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+// A workspace: two pieces of output for every worker of every lane, their maxima and sums, and for each
+// query and lane the first piece (-1: there is only one, which was put out at once) and the last worker.
+struct AttendSpace {
+  float* piece;
+  float* statistic;
+  int32_t* first;
+  int32_t* last;
+  int64_t bytes;
+};
+AttendSpace attend_space(const AttendShape& s, int64_t queries, int64_t dim, void* at) {
+  AttendSpace w{};
+  if (!s.workers) return w;
+  const int64_t pieces = 2 * s.workers * s.lanes * s.rows;
+  w.piece = static_cast<float*>(at);
+  w.statistic = w.piece + pieces * padded(dim);
+  w.first = reinterpret_cast<int32_t*>(w.statistic + 2 * pieces);
+  w.last = w.first + queries * s.lanes;
+  w.bytes = pieces * (padded(dim) + 2) * 4 + 2 * queries * s.lanes * 4;
+  return w;
+}
+
+// Which tokens of which row a query sees.
+struct Seen {
+  int64_t row;
+  uint32_t from, upto;
+};
+__device__ inline Seen seen(const tt_attend_args& a, int64_t i) {
+  Seen s;
+  s.row = a.rows ? a.rows[i] : i;
+  const int64_t most = a.width * a.cache.block_size;
+  int64_t n = min((int64_t)a.lengths[i], most);
+  if (n < 0 || s.row < 0 || s.row >= a.table_rows) n = 0;
+  s.upto = (uint32_t)n;
+  s.from = a.window > 0 && n > a.window ? (uint32_t)(n - a.window) : 0;
+  return s;
+}
+
+template <class T>
+__device__ inline f32x4 product(u32x4 x, u32x4 y, f32x4 z) {
+  if constexpr (std::is_same<T, _Float16>::value)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, x), __builtin_bit_cast(f16x8, y), z, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), z, 0, 0, 0);
+}
+
+// Two e4m3 (bytes 0 and 1, or 2 and 3) in 16 bits each, which hold them exactly.
+template <class T, bool HIGH>
+__device__ inline uint32_t widened(uint32_t w) {
+  if constexpr (std::is_same<T, _Float16>::value)
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HIGH));
+  else
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HIGH));
+}
+
+template <class T>
+__device__ inline uint32_t two(float x, float y) {
+  typedef T pair __attribute__((ext_vector_type(2)));
+  const pair p = {(T)x, (T)y};
+  return __builtin_bit_cast(uint32_t, p);
+}
+template <class T>
+__device__ inline float one_of(uint32_t w, int k) {
+  typedef T pair __attribute__((ext_vector_type(2)));
+  return (float)__builtin_bit_cast(pair, w)[k];
+}
+
+__device__ inline float over_groups(float x, bool sum) {
+  const float y = __shfl_xor(x, 16), z = sum ? x + y : fmaxf(x, y), u = __shfl_xor(z, 32);
+  return sum ? z + u : fmaxf(z, u);
+}
+
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
+
+// One workgroup: a lane's heads, for some tokens of a query after the other.
+template <class T, bool EIGHT, int D, bool WHOLE>
+struct Attend {
+  static constexpr int SIZE = EIGHT ? 1 : 2;
+  static constexpr int STEPS = D / 32;             // products of a score
+  static constexpr int PER = 16 / SIZE;            // elements of a load of keys
+  static constexpr int LOADS = D / (4 * PER);      // of a token's key, by its four lanes
+  static constexpr int MINE = D / 16;              // values of a token that a lane loads
+  static constexpr int VWORDS = MINE * SIZE / 4;
+  static constexpr int ROW = D + 4;                // of the output in LDS, so that 16 heads lie in other banks
+
+  struct Shared {
+    float out[AT_WAVES][AT_HEADS][ROW];
+    float top[AT_WAVES][AT_HEADS], sum[AT_WAVES][AT_HEADS], total[AT_HEADS];
+    int64_t key_at[AT_WAVES][AT_TILE], value_at[AT_WAVES][AT_TILE];
+  };
+
+  const tt_attend_args& a;
+  const AttendShape& shape;
+  const AttendSpace& space;
+  Division by_block;
+  Shared& s;
+  int lane, wave, c, g;
+  int64_t head;   // of keys
+  int part, here;  // query heads: which of the lane's, how many of them
+
+  // Tokens upto `end` of query i; slot: where the piece goes, negative: it is the whole output.
+  __device__ void run(int64_t i, const Seen& q, uint32_t from, uint32_t end, int64_t slot) {
+    const tt_paged_cache& cache = a.cache;
+    const uint32_t dim = (uint32_t)cache.dim;
+    u32x4 query[STEPS];
+    const T* row = static_cast<const T*>(a.query) + i * a.query_stride + (head * shape.group + part * AT_HEADS + c) * a.query_head_stride;
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+      const uint32_t d = EIGHT ? k / 2 * 64 + g * 16 + k % 2 * 8 : k * 32 + g * 8;
+      query[k] = 0;
+      if (c < here && (WHOLE || d < dim)) query[k] = *reinterpret_cast<const typename Words<4>::type*>(row + d);
+    }
+    float before = (float)a.scale * (cache.key_scale ? cache.key_scale[head] : 1.0f), after = 0;
+    const bool capped = (float)a.softcap > 0;
+    if (capped) {  // tanh(y) = 1 - 2 / (1 + 2^(2 y log2 e))
+      before = before / (float)a.softcap * (2 * LOG2E);
+      after = (float)a.softcap * LOG2E;
+    } else {
+      before *= LOG2E;
+    }
+
+    const int32_t* table = a.table + q.row * a.table_stride;
+    const char* keys = static_cast<const char*>(cache.keys) + head * cache.key_head_stride * SIZE;
+    const char* values = static_cast<const char*>(cache.values) + head * cache.value_head_stride * SIZE;
+    uint32_t base = from + wave * AT_TILE;
+
+    // A tile's blocks, its addresses in LDS, then its keys and values.
+    auto entry_of = [&](uint32_t at) {
+      const uint32_t t = at + lane;
+      return lane < AT_TILE && t < end ? table[quotient(t, by_block)] : -1;
+    };
+    auto addresses = [&](int32_t entry, uint32_t at) -> uint32_t {
+      const uint32_t t = at + lane;
+      const bool there = entry >= 0 && entry < cache.blocks;
+      const int64_t block = there ? entry : 0, place = there ? t - quotient(t, by_block) * by_block.divisor : 0;
+      if (lane < AT_TILE) {
+        s.key_at[wave][lane] = (block * cache.key_block_stride + place * cache.key_place_stride) * SIZE;
+        s.value_at[wave][lane] = (block * cache.value_block_stride + place * cache.value_place_stride) * SIZE;
+      }
+      return (uint32_t)__ballot(there);
+    };
+    u32x4 key[2][LOADS];
+    auto load_keys = [&] {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const char* at = keys + s.key_at[wave][t * 16 + c];
+#pragma unroll
+        for (int k = 0; k < LOADS; ++k) {
+          const uint32_t d = k * 4 * PER + g * PER;
+          if (WHOLE) {
+            key[t][k] = *reinterpret_cast<const typename Words<4>::type*>(at + d * SIZE);
+          } else if (!EIGHT) {  // past the head: its first elements again, against zeros of the query
+            key[t][k] = *reinterpret_cast<const typename Words<4>::type*>(at + (d < dim ? d : 0) * SIZE);
+            if (d >= dim) key[t][k] = 0;
+          } else {
+            const auto low = *reinterpret_cast<const typename Words<2>::type*>(at + (d < dim ? d : 0));
+            const auto high = *reinterpret_cast<const typename Words<2>::type*>(at + (d + 8 < dim ? d + 8 : 0));
+            key[t][k][0] = d < dim ? low[0] : 0, key[t][k][1] = d < dim ? low[1] : 0;
+            key[t][k][2] = d + 8 < dim ? high[0] : 0, key[t][k][3] = d + 8 < dim ? high[1] : 0;
+          }
+        }
+      }
+    };
+    uint32_t value[8][VWORDS];
+    auto load_values = [&] {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const char* at = values + s.value_at[wave][k / 4 * 16 + g * 4 + k % 4];
+        constexpr int N = VWORDS < 4 ? VWORDS : 4;
+#pragma unroll
+        for (int w = 0; w < VWORDS; w += N) {
+          // past the head: its first elements again, for outputs that are not stored
+          uint32_t d = c * MINE + w * 4 / SIZE;
+          if constexpr (!WHOLE && N * 4 / SIZE > 8) {  // 16 elements, of which the head may have 8
+            const auto low = *reinterpret_cast<const typename Words<2>::type*>(at + (d < dim ? d : 0));
+            const auto high = *reinterpret_cast<const typename Words<2>::type*>(at + (d + 8 < dim ? d + 8 : 0));
+            value[k][w] = low[0], value[k][w + 1] = low[1], value[k][w + 2] = high[0], value[k][w + 3] = high[1];
+          } else {
+            if (!WHOLE && d >= dim) d = 0;
+            const auto x = *reinterpret_cast<const typename Words<N>::type*>(at + d * SIZE);
+            if constexpr (N == 1) {
+              value[k][w] = x;
+            } else {
+#pragma unroll
+              for (int n = 0; n < N; ++n) value[k][w + n] = x[n];
+            }
+          }
+        }
+      }
+    };
+
+    f32x4 out[MINE];
+#pragma unroll
+    for (int j = 0; j < MINE; ++j) out[j] = 0;
+    float top = -__builtin_inff(), sum = 0;
+
+    int32_t entry = entry_of(base);
+    uint32_t there = addresses(entry, base);
+    entry = entry_of(base + AT_UNIT);
+    if (there) {
+      load_keys();
+      load_values();
+    }
+    while (base < end) {
+      const uint32_t there_next = addresses(entry, base + AT_UNIT);
+      entry = entry_of(base + 2 * AT_UNIT);
+      float x[8];
+      if (there) {
+        f32x4 score[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          score[t] = 0;
+#pragma unroll
+          for (int k = 0; k < STEPS; ++k) {
+            u32x4 w;
+            if constexpr (EIGHT) {
+              const uint32_t lo = key[t][k / 2][k % 2 * 2], hi = key[t][k / 2][k % 2 * 2 + 1];
+              w = u32x4{widened<T, false>(lo), widened<T, true>(lo), widened<T, false>(hi), widened<T, true>(hi)};
+            } else {
+              w = key[t][k];
+            }
+            score[t] = product<T>(w, query[k], score[t]);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          x[k] = score[k / 4][k % 4] * before;
+          if (capped) x[k] = (1.0f - 2.0f / (1.0f + __builtin_amdgcn_exp2f(x[k]))) * after;
+        }
+        if (there != 0xFFFFFFFFu) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (!(there >> (k / 4 * 16 + g * 4 + k % 4) & 1)) {
+              x[k] = -__builtin_inff();
+#pragma unroll
+              for (int w = 0; w < VWORDS; ++w) value[k][w] = 0;  // a weight of zero does not take out NaN
+            }
+        }
+      }
+      if (there_next) load_keys();
+      if (there) {
+        // weights go by a maximum that may be 8 too low: they stay below 2^8, and most tiles leave it as it is
+        float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+        if (__any(most > top + 8.0f)) {
+          most = fmaxf(over_groups(most, false), top);
+          const float by = most == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top - most);
+          top = most;
+          sum *= by;
+#pragma unroll
+          for (int j = 0; j < MINE; ++j) out[j] *= by;
+        }
+        const float less = top == -__builtin_inff() ? 0.0f : top;
+        // weights in two terms of 16 bits each, together good for 16 bits of mantissa and more: rounded to one they would
+        // cost as much as the output's own rounding
+        u32x4 weight, rest;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          x[k] = __builtin_amdgcn_exp2f(x[k] - less);
+          sum += x[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          weight[k] = two<T>(x[2 * k], x[2 * k + 1]);
+          rest[k] = two<T>(x[2 * k] - one_of<T>(weight[k], 0), x[2 * k + 1] - one_of<T>(weight[k], 1));
+        }
+#pragma unroll
+        for (int j = 0; j < MINE; j += 2) {
+          uint32_t pair[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if constexpr (EIGHT) pair[k] = j % 4 ? widened<T, true>(value[k][j / 4]) : widened<T, false>(value[k][j / 4]);
+            else pair[k] = value[k][j / 2];
+          }
+          u32x4 even, odd;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            even[k] = __builtin_amdgcn_perm(pair[2 * k + 1], pair[2 * k], 0x05040100);
+            odd[k] = __builtin_amdgcn_perm(pair[2 * k + 1], pair[2 * k], 0x07060302);
+          }
+          out[j] = product<T>(even, weight, out[j]);
+          out[j] = product<T>(even, rest, out[j]);
+          out[j + 1] = product<T>(odd, weight, out[j + 1]);
+          out[j + 1] = product<T>(odd, rest, out[j + 1]);
+        }
+      }
+      if (there_next) load_values();
+      there = there_next;
+      base += AT_UNIT;
+    }
+
+    // the wavefronts' parts together
+    sum = over_groups(sum, true);
+    if (g == 0) s.top[wave][c] = top, s.sum[wave][c] = sum;
+    __syncthreads();
+    float all = s.top[0][c], total = 0;
+#pragma unroll
+    for (int w = 1; w < AT_WAVES; ++w) all = fmaxf(all, s.top[w][c]);
+    const float less = all == -__builtin_inff() ? 0.0f : all;
+#pragma unroll
+    for (int w = 0; w < AT_WAVES; ++w) total += s.sum[w][c] * __builtin_amdgcn_exp2f(s.top[w][c] - less);
+    const float by = __builtin_amdgcn_exp2f(top - less);
+    if (c < here) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < MINE; j += 4)
+          *reinterpret_cast<f32x4*>(&s.out[wave][c][(g * 4 + r) * MINE + j]) =
+              f32x4{out[j][r], out[j + 1][r], out[j + 2][r], out[j + 3][r]} * by;
+    }
+    const int64_t unit = head * shape.parts + part;
+    if (wave == 0 && g == 0 && c < here) {
+      if (slot < 0) {
+        if (a.lse) a.lse[i * a.lse_stride + head * shape.group + part * AT_HEADS + c] = total == 0 ? -__builtin_inff() : (all + __log2f(total)) * LN2;
+      } else {
+        float* to = space.statistic + ((slot * shape.lanes + unit) * shape.rows + c) * 2;
+        to[0] = all, to[1] = total;
+      }
+      s.total[c] = total;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < here * (D / 8); e += AT_THREADS) {
+      const int row = e / (D / 8), d = e % (D / 8) * 8;
+      f32x4 y[2] = {0, 0};
+#pragma unroll
+      for (int w = 0; w < AT_WAVES; ++w)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) y[k] += *reinterpret_cast<const f32x4*>(&s.out[w][row][d + 4 * k]);
+      if (slot < 0) {
+        if (!WHOLE && d >= (int)dim) continue;
+        const float of = s.total[row], scale = (cache.value_scale ? cache.value_scale[head] : 1.0f) / of;
+        typename Eight<T>::type z;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) z[k] = (T)(of == 0 ? 0.0f : y[k / 4][k % 4] * scale);
+        *reinterpret_cast<typename Eight<T>::type*>(static_cast<T*>(a.out) + i * a.out_stride +
+                                                    (head * shape.group + part * AT_HEADS + row) * a.out_head_stride + d) = z;
+      } else {
+        float* to = space.piece + ((slot * shape.lanes + unit) * shape.rows + row) * D + d;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) *reinterpret_cast<f32x4*>(to + 4 * k) = y[k];
+      }
+    }
+    __syncthreads();  // before the next query's parts
+  }
+};
+
+// Units that a query's tokens take; one that sees nothing has one too, to put out its zeros.
+__device__ inline int64_t units_of(const Seen& q) { return max((q.upto - q.from + AT_UNIT - 1) / AT_UNIT, 1u); }
+
+// The first units of the queries, one behind the other, and the number of all.
+__device__ inline void starts_of(const tt_attend_args& a, int64_t* start, int64_t* sums) {
+  const int n = (int)a.queries, tid = threadIdx.x, per = (n + AT_THREADS - 1) / AT_THREADS;
+  int64_t mine = 0;
+  for (int i = tid * per; i < min(n, (tid + 1) * per); ++i) mine += units_of(seen(a, i));
+  int64_t upto = mine;  // inclusive sums over the wavefront
+#pragma unroll
+  for (int d = 1; d < WAVE; d *= 2) {
+    const int64_t other = __shfl_up(upto, d);
+    if (tid % WAVE >= d) upto += other;
+  }
+  if (tid % WAVE == WAVE - 1) sums[tid / WAVE] = upto;
+  __syncthreads();
+  int64_t at = upto - mine;
+  for (int w = 0; w < tid / WAVE; ++w) at += sums[w];
+  for (int i = tid * per; i < min(n, (tid + 1) * per); ++i) {
+    start[i] = at;
+    at += units_of(seen(a, i));
+  }
+  if (tid == AT_THREADS - 1) start[n] = at;
+  __syncthreads();
+}
+
+// Workgroups of the same lane share out the units of all queries evenly, so that short and long requests do not wait for
+// each other; where the cut goes through a query its pieces are joined by k_join.
+template <class T, bool EIGHT, int D, bool WHOLE>
+__global__ __launch_bounds__(AT_THREADS, D == 256 ? 1 : 2) void k_attend(tt_attend_args a, AttendShape shape, AttendSpace space,
+                                                                     Division by_block, int64_t first) {
+  typedef Attend<T, EIGHT, D, WHOLE> Work;
+  __shared__ typename Work::Shared s;
+  __shared__ int64_t s_start[AT_QUERIES + 1], s_sums[AT_WAVES];
+  const int64_t id = first + blockIdx.x, unit = id % shape.lanes;
+  const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+  const int part = (int)(unit % shape.parts);
+  Work work{a, shape, space, by_block, s, lane, wave, lane % 16, lane / 16, unit / shape.parts, part,
+            min(AT_HEADS, shape.group - part * AT_HEADS)};
+  if (!shape.workers) {
+    const int64_t i = id / shape.lanes;
+    const Seen q = seen(a, i);
+    work.run(i, q, q.from, q.upto, -1);
+    return;
+  }
+  starts_of(a, s_start, s_sums);
+  const int n = (int)a.queries, worker = (int)(id / shape.lanes);
+  const int64_t all = s_start[n], sharers = min((int64_t)shape.workers, all);  // each has a unit at least, so a query's pieces have workers in a row
+  if (worker >= sharers) return;
+  const int64_t upto = all * (worker + 1) / sharers;
+  int64_t at = all * worker / sharers;
+  int lo = 0, hi = n;  // the query that unit `at` is of
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (s_start[mid] <= at) lo = mid;
+    else hi = mid;
+  }
+  for (int nth = 0; at < upto; ++nth, ++lo) {
+    const int64_t begin = s_start[lo], end = s_start[lo + 1], stop = min(end, upto);
+    const int slot = 2 * worker + (nth > 0);
+    const bool whole = at == begin && stop == end;
+    if (threadIdx.x == 0) {
+      if (at == begin) space.first[lo * shape.lanes + unit] = whole ? -1 : slot;
+      if (stop == end) space.last[lo * shape.lanes + unit] = worker;
+    }
+    const Seen q = seen(a, lo);
+    work.run(lo, q, q.from + (uint32_t)(at - begin) * AT_UNIT, stop == end ? q.upto : q.from + (uint32_t)(stop - begin) * AT_UNIT,
+             whole ? -1 : slot);
+    at = stop;
+  }
+}
+
+// The pieces of a query head together: those of its first worker, and the first one of each worker up to its last.
+template <class T>
+__global__ __launch_bounds__(AT_THREADS) void k_join(tt_attend_args a, AttendShape shape, AttendSpace space, int wide) {
+  __shared__ float s_by[AT_GROUPS], s_max[AT_WAVES], s_sum[AT_WAVES];
+  __shared__ f32x4 s_out[AT_THREADS];
+  const int64_t i = blockIdx.x / a.heads;
+  const int h = (int)(blockIdx.x % a.heads), kv = h / shape.group, nth = h % shape.group;
+  const int64_t unit = (int64_t)kv * shape.parts + nth / AT_HEADS, row = nth % AT_HEADS;
+  const int first = space.first[i * shape.lanes + unit];
+  if (first < 0) return;
+  const int before = first / 2, pieces = space.last[i * shape.lanes + unit] - before + 1;
+  auto place = [&](int k) { return ((k ? 2 * (before + k) : first) * shape.lanes + unit) * shape.rows + row; };
+  const int tid = threadIdx.x;
+  float top = -__builtin_inff();
+  for (int k = tid; k < pieces; k += AT_THREADS) top = fmaxf(top, space.statistic[place(k) * 2]);
+#pragma unroll
+  for (int d = 1; d < WAVE; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+  if (tid % WAVE == 0) s_max[tid / WAVE] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < AT_WAVES; ++w) top = fmaxf(top, s_max[w]);
+  const float less = top == -__builtin_inff() ? 0.0f : top;
+  float sum = 0;
+  for (int k = tid; k < pieces; k += AT_THREADS) {
+    const float by = __builtin_amdgcn_exp2f(space.statistic[place(k) * 2] - less);
+    s_by[k] = by;
+    sum += by * space.statistic[place(k) * 2 + 1];
+  }
+#pragma unroll
+  for (int d = 1; d < WAVE; d *= 2) sum += __shfl_xor(sum, d);
+  if (tid % WAVE == 0) s_sum[tid / WAVE] = sum;
+  __syncthreads();
+  sum = 0;
+#pragma unroll
+  for (int w = 0; w < AT_WAVES; ++w) sum += s_sum[w];
+  const int across = wide / 4, side = AT_THREADS / across, d = tid % across * 4;
+  f32x4 y = 0;
+  for (int k = tid / across; k < pieces; k += side) y += *reinterpret_cast<const f32x4*>(space.piece + place(k) * wide + d) * s_by[k];
+  s_out[tid] = y;
+  __syncthreads();
+  if (tid == 0 && a.lse) a.lse[i * a.lse_stride + h] = sum == 0 ? -__builtin_inff() : (top + __log2f(sum)) * LN2;
+  if (tid >= across || d >= a.cache.dim) return;
+  for (int k = 1; k < side; ++k) y += s_out[k * across + tid];
+  const float scale = (a.cache.value_scale ? a.cache.value_scale[kv] : 1.0f) / sum;
+  T* to = static_cast<T*>(a.out) + i * a.out_stride + h * a.out_head_stride + d;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) to[k] = (T)(sum == 0 ? 0.0f : y[k] * scale);
+}
+
+template <class T, bool EIGHT, int D, bool WHOLE>
+void enqueue_attend(const tt_attend_args& a, const AttendShape& shape, const AttendSpace& space, hipStream_t st) {
+  const Division by_block = division(a.cache.block_size);
+  const int64_t groups = shape.lanes * (shape.workers ? shape.workers : a.queries), most = MAX_ITEMS / AT_THREADS;
+  for (int64_t at = 0; at < groups; at += most)
+    hipLaunchKernelGGL((k_attend<T, EIGHT, D, WHOLE>), dim3((uint32_t)std::min(most, groups - at)), dim3(AT_THREADS), 0, st, a,
+                       shape, space, by_block, at);
+}
+
+template <class T, bool EIGHT>
+void enqueue_attend(const tt_attend_args& a, const AttendShape& shape, const AttendSpace& space, hipStream_t st) {
+  switch (a.cache.dim) {
+    case 64: return enqueue_attend<T, EIGHT, 64, true>(a, shape, space, st);
+    case 128: return enqueue_attend<T, EIGHT, 128, true>(a, shape, space, st);
+    case 256: return enqueue_attend<T, EIGHT, 256, true>(a, shape, space, st);
+  }
+  if (a.cache.dim < 64) return enqueue_attend<T, EIGHT, 64, false>(a, shape, space, st);
+  if (a.cache.dim < 128) return enqueue_attend<T, EIGHT, 128, false>(a, shape, space, st);
+  return enqueue_attend<T, EIGHT, 256, false>(a, shape, space, st);
+}
+
+template <class I, class O>
+void enqueue_write(const tt_write_args& a, hipStream_t st) {
+  const uint32_t per_head = (uint32_t)(a.cache.dim / 8), per_token = (uint32_t)a.cache.heads * per_head;
+  const int64_t total = a.tokens * per_token, most = MAX_ITEMS / WR_THREADS * WR_THREADS;
+  for (int64_t at = 0; at < total; at += most)
+    hipLaunchKernelGGL((k_write<I, O>), dim3((uint32_t)div_up(std::min(most, total - at), WR_THREADS)), dim3(WR_THREADS), 0, st, a,
+                       per_head, per_token, at, total);
+}
+
+template <class I>
+void enqueue_write(const tt_write_args& a, hipStream_t st) {
+  if (a.cache.type == TT_E4M3) enqueue_write<I, uint8_t>(a, st);
+  else if (a.cache.type == TT_F16) enqueue_write<I, _Float16>(a, st);
+  else enqueue_write<I, __bf16>(a, st);
+}
+
+}  // namespace
+
+hipError_t launch_write(const tt_write_args& a, hipStream_t st) {
+  if (a.in_type == TT_F32) enqueue_write<float>(a, st);
+  else if (a.in_type == TT_F16 && a.cache.type == TT_E4M3) enqueue_write<_Float16, uint8_t>(a, st);
+  else if (a.in_type == TT_F16) enqueue_write<_Float16, _Float16>(a, st);
+  else if (a.cache.type == TT_E4M3) enqueue_write<__bf16, uint8_t>(a, st);
+  else enqueue_write<__bf16, __bf16>(a, st);
+  return hipGetLastError();
+}
+
+int64_t attend_workspace(int64_t queries, int64_t heads, int64_t cache_heads, int64_t dim) {
+  return attend_space(attend_shape(queries, heads, cache_heads), queries, dim, nullptr).bytes;
+}
+
+hipError_t launch_attend(const tt_attend_args& a, hipStream_t st) {
+  const AttendShape shape = attend_shape(a.queries, a.heads, a.cache.heads);
+  const AttendSpace space = attend_space(shape, a.queries, a.cache.dim, a.workspace);
+  const bool eight = a.cache.type == TT_E4M3, half = a.type == TT_F16;
+  if (half && eight) enqueue_attend<_Float16, true>(a, shape, space, st);
+  else if (half) enqueue_attend<_Float16, false>(a, shape, space, st);
+  else if (eight) enqueue_attend<__bf16, true>(a, shape, space, st);
+  else enqueue_attend<__bf16, false>(a, shape, space, st);
+  if (shape.workers > 1) {
+    auto* k = half ? k_join<_Float16> : k_join<__bf16>;
+    hipLaunchKernelGGL(k, dim3((uint32_t)(a.queries * a.heads)), dim3(AT_THREADS), 0, st, a, shape, space, padded(a.cache.dim));
+  }
+  return hipGetLastError();
+}
+
+}  // namespace tt
