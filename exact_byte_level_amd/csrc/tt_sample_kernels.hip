@@ -23,11 +23,13 @@ __device__ inline uint32_t order_of(float x) {
 }
 __device__ inline float logit_of(uint32_t order) { return __uint_as_float(order >> 31 ? order & 0x7FFFFFFFu : ~order); }
 constexpr uint32_t NOTHING = 0x007FFFFFu;  // the order of -infinity
+constexpr uint32_t ALL = 0xFFFFFFFFu;
 
-// 2^t for t from -1100 to 0: the nearest whole number apart, 1 + f p(f) on -1/2 .. 1/2 with p through the 9 Chebyshev
-// nodes, off by less than 4e-14 of the value and exact at 0.
+// 2^t for t from -1010 to 0: the nearest whole number apart, which a large number added leaves in its lowest bits, 1 + f p(f) on
+// -1/2 .. 1/2 with p through the 9 Chebyshev nodes, off by less than 4e-14 of the value and exact at 0; the whole number goes to the exponent.
 __device__ inline double power_of_two(double t) {
-  const double n = __builtin_rint(t), f = t - n;
+  constexpr double LARGE = 6755399441055744.0;  // 1.5 * 2^52
+  const double n = t + LARGE, f = t - (n - LARGE);
   double y = 1.0203121113055101e-07;
   y = fma(y, f, 1.3255224878933224e-06);
   y = fma(y, f, 1.5252686846120593e-05);
@@ -38,27 +40,34 @@ __device__ inline double power_of_two(double t) {
   y = fma(y, f, 0.24022650695812989);
   y = fma(y, f, 0.69314718055994529);
   y = fma(y, f, 1.0);
-  return __builtin_ldexp(y, (int)n);
+  return __hiloint2double(__double2hiint(y) + (int)((uint32_t)__double2loint(n) << 20), __double2loint(y));
 }
 
-// Weights of a row: e^((x - top) / temperature).
+// Weights of a row: e^((x - top) / temperature); below 2^-1000 they count as zero.
 struct Weigher {
+  float most;    // top as it was
+  float lowest;  // what is not above it weighs nothing
   double top, by;  // by = log2 e / temperature
-  bool endless;    // top is +infinity: everything below weighs nothing
-  __device__ Weigher(float most, float temperature)
-      : top(most), by(1.4426950408889634 / (double)temperature), endless(most == __builtin_inff()) {}
-  __device__ double operator()(float x) const {
-    // NaN, which -infinity gives where the temperature is infinite, becomes a weight of zero
-    const double w = power_of_two(__builtin_fmax(((double)x - top) * by, -1100.0));
-    return endless ? (x == __builtin_inff() ? 1.0 : 0.0) : w;
+  __device__ Weigher(float most_, float temperature) : most(most_), top(most_), by(1.4426950408889634 / (double)temperature) {
+    lowest = (float)(top - 1000.0 / by);
   }
+  // (top itself apart, for an infinite one and for temperatures at which nothing else weighs; NaN is not above anything)
+  __device__ double operator()(float x) const {
+    const double y = power_of_two(((double)x - top) * by);
+    return x == most ? 1.0 : x > lowest ? y : 0.0;
+  }
+  // Where the lowest is a number well below the top, sums that the top is in do not tell 2^-1000 from zero.
+  __device__ bool clear() const { return __builtin_fabsf(lowest) < __builtin_inff() && ((double)lowest - top) * by < -900.0; }
+  __device__ double roughly(float x) const { return power_of_two(((double)fmaxf(x, lowest) - top) * by); }
+  // log2 of the weight, 0 down to -2^25.
+  __device__ float depth(float x) const { return x == most ? 0.0f : x > lowest ? (float)(((double)x - top) * by) : -33554432.0f; }
 };
 
 // What is asked of a row.
 struct Limits {
   float temperature, top_p, min_p, uniform;
-  int64_t top_k;                     // 0: none
-  bool single, by_mass, by_weight;   // the first token alone; top_p limits; min_p limits
+  int64_t top_k;                    // 0: none
+  bool single, by_mass, by_weight;  // the first token alone; top_p limits; min_p limits
   __device__ bool limited() const { return top_k || by_mass || by_weight; }
 };
 __device__ inline Limits limits_of(const tt_sample_args& a, int64_t r) {
@@ -76,517 +85,804 @@ __device__ inline Limits limits_of(const tt_sample_args& a, int64_t r) {
   return l;
 }
 
+// ------------------------------------------------------------- over the lanes
+
+// What the lanes `CTRL` says (of the rows of 16 in ROWS) hold of v, 0 where there are none.
+template <int CTRL, int ROWS>
+__device__ inline uint32_t from_lanes(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ inline float from_lanes(float v) {
+  return __uint_as_float(from_lanes<CTRL, ROWS>(__float_as_uint(v)));
+}
+template <int CTRL, int ROWS>
+__device__ inline u64 from_lanes(u64 v) {
+  return (u64)from_lanes<CTRL, ROWS>((uint32_t)(v >> 32)) << 32 | from_lanes<CTRL, ROWS>((uint32_t)v);
+}
+template <int CTRL, int ROWS>
+__device__ inline double from_lanes(double v) {
+  return __longlong_as_double((long long)from_lanes<CTRL, ROWS>((u64)__double_as_longlong(v)));
+}
+__device__ inline uint32_t of_lane(uint32_t v, int lane) { return (uint32_t)__builtin_amdgcn_readlane((int)v, lane); }
+__device__ inline float of_lane(float v, int lane) { return __uint_as_float(of_lane(__float_as_uint(v), lane)); }
+__device__ inline u64 of_lane(u64 v, int lane) { return (u64)of_lane((uint32_t)(v >> 32), lane) << 32 | of_lane((uint32_t)v, lane); }
+__device__ inline double of_lane(double v, int lane) { return __longlong_as_double((long long)of_lane((u64)__double_as_longlong(v), lane)); }
+
+// op over the lanes up to each, of values whose op with 0 leaves them: shifts by 1, 2, 4, 8 in rows of 16, then the last lanes of
+// rows 0 and 2, then of row 1.
+template <class V, class Op>
+__device__ inline V upto_lane(V v, Op op) {
+  v = op(v, from_lanes<0x111, 0xf>(v));
+  v = op(v, from_lanes<0x112, 0xf>(v));
+  v = op(v, from_lanes<0x114, 0xf>(v));
+  v = op(v, from_lanes<0x118, 0xf>(v));
+  v = op(v, from_lanes<0x142, 0xa>(v));
+  return op(v, from_lanes<0x143, 0xc>(v));
+}
+template <class V>
+__device__ inline V sums_upto(V v) {
+  return upto_lane(v, [](V x, V y) { return x + y; });
+}
+template <class V>
+__device__ inline V sum_of_lanes(V v) {
+  return of_lane(sums_upto(v), WAVE - 1);
+}
+template <class V>
+__device__ inline V max_of_lanes(V v) {
+  return of_lane(upto_lane(v, [](V x, V y) { return x > y ? x : y; }), WAVE - 1);
+}
+
 // ------------------------------------------------------------ parts of a row
 //
-// A wavefront takes 2,048 logits into registers: their maximum, the sum of their weights by it, and, where the row has
+// A wavefront takes up to 2,048 logits into registers: their maximum, the sum of their weights by it, and, where the row has
 // limits, a list of its largest ones, all that are not below a bar of its own.  What is above the highest of
 // the bars is in the lists, so most rows need not be read again.
 
-constexpr int PT_TOKENS = 2048;  // of a part
-constexpr int PT_MINE = PT_TOKENS / WAVE;
+constexpr int PT_STEP = WAVE * 8;
 constexpr int PT_LIST = 64;
 constexpr int PT_THREADS = 256;
 constexpr int64_t PT_BATCH = 65536;  // parts of a launch
+constexpr int WD_SLOTS = 256;        // rows that are gone over again by many workgroups
+constexpr int WD_BINS = 2048;
+constexpr int WD_SEGMENT = 8;        // parts of a workgroup
 
 struct Part {
   double sum;
+  double kept;     // of rows gone over again: the weight of what is kept for certain
   float most;
   uint32_t bar;    // the order down to which all tokens are listed
-  uint32_t count;  // of the list
+  uint32_t count;  // of the list; above PT_LIST: it would have had more
   uint32_t unused;
 };
 struct Listed {
   uint32_t order, id;
 };
+struct Slot {
+  int64_t row;
+  u64 mass[WD_BINS];
+};
+struct Space {
+  uint32_t* slots_taken;
+  double* whole;    // of rows that are not done: what all tokens weigh
+  uint32_t* state;  // of each row: DONE, LEFT, or its slot
+  Part* parts;
+  Listed* lists;
+  Slot* slots;  // nullptr: rows are gone over again by a workgroup each
+  int64_t per_row, bytes;
+  uint32_t size;  // tokens of a part
+};
+constexpr uint32_t DONE = 0xFFFFFFFFu, LEFT = 0xFFFFFFFEu;
 
 template <class T>
 struct Eight {
   typedef T type __attribute__((ext_vector_type(8), aligned(alignof(T))));
 };
 
-template <class T>
-__global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, Part* parts, Listed* lists, int64_t per_row) {
-  const int lane = threadIdx.x % WAVE;
-  const int64_t id = (int64_t)blockIdx.x * (PT_THREADS / WAVE) + threadIdx.x / WAVE, r = id / per_row;
+// Q * 512 tokens a part.  256 x 262,144 float32 with limits take 56 us.
+template <class T, int Q>
+__global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, Space space) {
+  constexpr int MINE = Q * 8;
+  const int lane = threadIdx.x % WAVE, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  const int64_t id = (int64_t)blockIdx.x * (PT_THREADS / WAVE) + wave, r = id / space.per_row;
+  if (id == 0 && lane == 0) *space.slots_taken = 0;
   if (r >= a.rows) return;
-  const uint32_t vocab = (uint32_t)a.vocab, first = (uint32_t)(id - r * per_row) * PT_TOKENS;
+  const uint32_t vocab = (uint32_t)a.vocab, first = (uint32_t)(id - r * space.per_row) * (Q * PT_STEP);
   const T* row = static_cast<const T*>(a.logits) + r * a.logits_stride;
-  float x[PT_MINE];
-  if (first + PT_TOKENS <= vocab) {
-    typename Eight<T>::type v[PT_MINE / 8];
+  float x[MINE];
+  if (first + Q * PT_STEP <= vocab) {
+    typename Eight<T>::type v[Q];
 #pragma unroll
-    for (int q = 0; q < PT_MINE / 8; ++q) v[q] = *reinterpret_cast<const typename Eight<T>::type*>(row + first + q * 512 + lane * 8);
+    for (int q = 0; q < Q; ++q) v[q] = *reinterpret_cast<const typename Eight<T>::type*>(row + first + q * PT_STEP + lane * 8);
 #pragma unroll
-    for (int q = 0; q < PT_MINE / 8; ++q)
+    for (int q = 0; q < Q; ++q)
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[q * 8 + k] = (float)v[q][k];
   } else {
 #pragma unroll
-    for (int i = 0; i < PT_MINE; ++i) {
-      const uint32_t v = first + i / 8 * 512 + lane * 8 + i % 8;
+    for (int i = 0; i < MINE; ++i) {
+      const uint32_t v = first + i / 8 * PT_STEP + lane * 8 + i % 8;
       x[i] = v < vocab ? (float)row[v] : -__builtin_inff();
     }
   }
   const Limits limits = limits_of(a, r);
   float mine = -__builtin_inff();  // the maximum passes over NaN
 #pragma unroll
-  for (int i = 0; i < PT_MINE; ++i) mine = fmaxf(mine, x[i]);
-  float most = mine;
-#pragma unroll
-  for (int d = 1; d < WAVE; d *= 2) most = fmaxf(most, __shfl_xor(most, d));
-  Part part{0, most, NOTHING + 1, 0, 0};
-  if (most > -__builtin_inff() && !limits.single) {
-    const Weigher w(most, limits.temperature);
+  for (int i = 0; i < MINE; ++i) mine = fmaxf(mine, x[i]);
+  const uint32_t own = order_of(mine);
+  const uint32_t top = max_of_lanes(own);
+  Part part{0, 0, logit_of(top), NOTHING + 1, 0, 0};
+  if (top > NOTHING && !limits.single) {
+    const Weigher w(part.most, limits.temperature);
     double sum = 0;
+    if (w.clear()) {
 #pragma unroll
-    for (int i = 0; i < PT_MINE; ++i) sum += w(x[i]);
+      for (int i = 0; i < MINE; ++i) sum += w.roughly(x[i]);
+    } else {
 #pragma unroll
-    for (int d = 1; d < WAVE; d *= 2) sum += __shfl_xor(sum, d);
-    part.sum = sum;
+      for (int i = 0; i < MINE; ++i) sum += w(x[i]);
+    }
+    part.sum = sum_of_lanes(sum);
     if (limits.limited()) {
       // The bar is the 32nd largest of the lanes' maxima, which about 64 ln 2 = 44 tokens are not below; of the largest
       // 16, 8, 4, 2, 1 where the list would not hold them.
-      const uint32_t at_most = order_of(mine);
       uint32_t bar = 0, count = 0;
+      float from = 0;
       for (int among = WAVE / 2; among; among /= 2) {
         bar = 0;
         for (uint32_t bit = 1u << 31; bit; bit >>= 1)
-          if (__popcll(__ballot(at_most >= (bar | bit))) >= among) bar |= bit;
+          if (__popcll(__ballot(own >= (bar | bit))) >= among) bar |= bit;
         bar = max(bar, NOTHING + 1);
+        from = logit_of(bar);
         count = 0;
 #pragma unroll
-        for (int i = 0; i < PT_MINE; ++i) count += __popcll(__ballot(order_of(x[i]) >= bar));
+        for (int i = 0; i < MINE; ++i) count += __popcll(__ballot(x[i] >= from));
         if (count <= PT_LIST) break;
-        count = PT_LIST + 1;
       }
-      if (count > PT_LIST) bar = 0xFFFFFFFFu, count = 0;
+      if (count > PT_LIST) bar = ALL, count = 0;
       part.bar = bar, part.count = count;
       if (count) {
-        // places by ids: eight tokens of a lane, the lanes, the four steps; sums of at most 64 fit a byte each
+        // places by ids: eight tokens of a lane, the lanes, the steps; sums of at most 64 fit a byte each
         uint32_t counts = 0;
 #pragma unroll
-        for (int i = 0; i < PT_MINE; ++i) counts += (uint32_t)(order_of(x[i]) >= bar) << (i / 8 * 8);
-        uint32_t upto = counts;
-#pragma unroll
-        for (int d = 1; d < WAVE; d *= 2) {
-          const uint32_t other = __shfl_up(upto, d);
-          if (lane >= d) upto += other;
-        }
-        const uint32_t all = __shfl(upto, WAVE - 1);
+        for (int i = 0; i < MINE; ++i) counts += (uint32_t)(x[i] >= from) << (i / 8 * 8);
+        const uint32_t upto = sums_upto(counts), all = of_lane(upto, WAVE - 1);
         uint32_t step = 0;
-        Listed* to = lists + id * PT_LIST;
+        Listed* to = space.lists + id * PT_LIST;
 #pragma unroll
-        for (int q = 0; q < PT_MINE / 8; ++q) {
+        for (int q = 0; q < Q; ++q) {
           uint32_t at = step + ((upto - counts) >> (8 * q) & 255);
+          if (counts >> (8 * q) & 255) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (order_of(x[q * 8 + k]) >= bar) to[at++] = Listed{order_of(x[q * 8 + k]), first + q * 512 + lane * 8 + k};
+            for (int k = 0; k < 8; ++k)
+              if (x[q * 8 + k] >= from) to[at++] = Listed{order_of(x[q * 8 + k]), first + q * PT_STEP + lane * 8 + k};
+          }
           step += all >> (8 * q) & 255;
         }
       }
     }
   }
-  if (lane == 0) parts[id] = part;
+  if (lane == 0) space.parts[id] = part;
 }
 
-// ---------------------------------------------------------- a row by a workgroup
+// -------------------------------------------------------------- a workgroup
 
 constexpr int SA_THREADS = 1024;
 constexpr int SA_WAVES = SA_THREADS / WAVE;
-constexpr int SA_TILES = 1024;     // parts that a row is summed up in
-constexpr int SA_STEP = WAVE * 8;  // tokens of a wavefront at a time
-constexpr int SA_BINS = 2048;
-constexpr int SA_LIST = 8192;      // tokens of the lists that are above all bars
+constexpr int SA_TILES = SA_THREADS;  // parts that a row is summed up in
+constexpr int SA_LIST = 8 * SA_THREADS;  // tokens of the lists that are above all bars
 
 struct SampleShared {
   union {
-    u64 bin[SA_BINS];
+    u64 bin[WD_BINS];
     double tile[SA_TILES];
     uint32_t ties[SA_TILES];
   };
-  double sum[SA_WAVES];
-  u64 best[SA_WAVES];
-  double above;
-  uint32_t found, last, token;
+  u64 of_wave[SA_WAVES];
+  u64 above, of;
+  uint32_t found, last, place;
   uint32_t order[SA_LIST], id[SA_LIST];
 };
 
-// Where the logits come from: a row in memory, or the tokens listed.  eight(at, end, f) calls f(logit, place, k) for the places
-// from `at` on, eight at most.
+// Where the logits come from: a row in memory, or the tokens listed.
 template <class T>
 struct RowSource {
   const T* row;
   uint32_t size;
-  template <class F>
-  __device__ void eight(uint32_t at, uint32_t end, F f) const {
-    if (at + 8 <= end) {
-      const auto x = *reinterpret_cast<const typename Eight<T>::type*>(row + at);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) f((float)x[k], at + k, k);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (at + k < end) f((float)row[at + k], at + k, k);
-    }
-  }
+  __device__ float at(uint32_t place) const { return (float)row[place]; }
 };
 struct ListSource {
   const uint32_t* order;
   uint32_t size;
-  template <class F>
-  __device__ void eight(uint32_t at, uint32_t end, F f) const {
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (at + k < end) f(logit_of(order[at + k]), at + k, k);
-  }
+  __device__ float at(uint32_t place) const { return logit_of(order[place]); }
 };
 
-template <class Source>
-struct Sampler {
-  const Source& source;
+__device__ inline u64 bits(double v) { return (u64)__double_as_longlong(v); }
+__device__ inline u64 bits(u64 v) { return v; }
+__device__ inline u64 bits(uint32_t v) { return v; }
+template <class V>
+__device__ inline V value(u64 v) {
+  if constexpr (std::is_same<V, double>::value) return __longlong_as_double((long long)v);
+  else return (V)v;
+}
+
+// The threads of a workgroup and what they share.
+struct Group {
   SampleShared& s;
   int tid, lane, wave;
 
-  // f(logit, place) for every token that the thread has.
-  template <class F>
-  __device__ void each(F f) {
-    for (uint32_t at = tid * 8; at < source.size; at += SA_THREADS * 8) source.eight(at, source.size, f);
-  }
-
-  __device__ double sum_of(double x) {
-#pragma unroll
-    for (int d = 1; d < WAVE; d *= 2) x += __shfl_xor(x, d);
-    if (lane == 0) s.sum[wave] = x;
-    __syncthreads();
-    x = 0;
-    for (int w = 0; w < SA_WAVES; ++w) x += s.sum[w];
-    __syncthreads();
-    return x;
-  }
-
+  // The sum of x over the workgroup, and, in `before`, over the threads before this one.
   template <class V>
-  __device__ V sums_upto(V x) {
+  __device__ __forceinline__ V sum(V x, V& before) {
+    const V upto = sums_upto(x);
+    __syncthreads();
+    if (lane == WAVE - 1) s.of_wave[wave] = bits(upto);
+    __syncthreads();
+    V all = 0;
+    before = upto - x;
 #pragma unroll
-    for (int d = 1; d < WAVE; d *= 2) {
-      const V other = __shfl_up(x, d);
-      if (lane >= d) x += other;
+    for (int k = 0; k < SA_WAVES; ++k) {
+      const V y = value<V>(s.of_wave[k]);
+      if (k < wave) before += y;
+      all += y;
     }
+    return all;
+  }
+  template <class V>
+  __device__ __forceinline__ V sum(V x) {
+    V before;
+    return sum(x, before);
+  }
+  __device__ __forceinline__ u64 most(u64 x) {
+    x = max_of_lanes(x);
+    __syncthreads();
+    if (lane == 0) s.of_wave[wave] = x;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < SA_WAVES; ++k) x = max(x, s.of_wave[k]);
     return x;
   }
 
-  // The order at which, from the largest down to `least`, as many tokens (or as much weight) as `target` are reached,
+  // The first thread at which the running sum of x satisfies enough(sum, sum of all), which once true stays so; the last one with a
+  // sum above 0 if none does.  `before`: the sum of the threads before it.
+  template <class V, class F>
+  __device__ __forceinline__ uint32_t first(V x, F enough, V& before, V& all) {
+    if (tid == 0) s.found = s.last = 0;
+    V at;
+    all = sum(x, at);
+    const uint32_t less = (uint32_t)__popcll(__ballot(!enough(at + x, all)));
+    const u64 some = __ballot(x > 0);
+    if (lane == 0 && less) atomicAdd(&s.found, less);
+    if (lane == 0 && some) atomicMax(&s.last, (uint32_t)(wave * WAVE + 63 - __builtin_clzll(some)));
+    __syncthreads();
+    const uint32_t found = min(s.found, s.last);
+    if (found == (uint32_t)tid) s.above = bits(at);
+    __syncthreads();
+    before = value<V>(s.above);
+    return found;
+  }
+};
+
+// The first place from `from` up to `end` at which `before` and the running sum of f(logit, place) are above `goal`, the last one with a
+// weight if none is, and its f; by the workgroup, some places a thread.
+template <class V, class Source, class F>
+__device__ __forceinline__ uint32_t locate(const Source& source, Group& g, uint32_t from, uint32_t end, V before, V goal, F f, V& mine) {
+  const uint32_t per = (end - from + SA_THREADS - 1) / SA_THREADS, own = from + g.tid * per, stop = min(own + per, end);
+  V sum = 0;
+#pragma unroll 1
+  for (uint32_t i = own; i < stop; ++i) sum += f(source.at(i), i);
+  V at, all;
+  const uint32_t thread = g.first(sum, [&](V upto, V) { return before + upto > goal; }, at, all);
+  if (thread == (uint32_t)g.tid) {
+    V run = before + at, of = 0;
+    uint32_t place = own;
+#pragma unroll 1
+    for (uint32_t i = own; i < stop; ++i) {
+      const V x = f(source.at(i), i);
+      run += x;
+      if (x > 0) {
+        place = i, of = x;
+        if (run > goal) break;
+      }
+    }
+    g.s.place = place, g.s.of = bits(of);
+  }
+  __syncthreads();
+  mine = value<V>(g.s.of);
+  return g.s.place;
+}
+
+// Sums of weights in 64 bits of fixed point, which are the same in any order: this is 1.
+__device__ inline double one_of(uint32_t tokens) { return __builtin_ldexp(1.0, 62 - (32 - __builtin_clz(tokens))); }
+
+// What is kept of a source of logits: orders above `least`, and those at it up to the place `until`, of a weight of min_p or more.
+struct Kept {
+  uint32_t least, until;
+  double min_p;
+  __device__ double of(uint32_t order, uint32_t place, double weight) const {
+    return order < least || (order == least && place > until) || weight < min_p ? 0.0 : weight;
+  }
+};
+
+// A source of logits that a workgroup passes over for every question.
+template <class Source>
+struct Sampler {
+  const Source& source;
+  Group& g;
+  SampleShared& s;
+
+  template <class F>
+  __device__ __forceinline__ double sum(F f) {
+    double sum = 0;
+#pragma unroll 1
+    for (uint32_t i = g.tid; i < source.size; i += SA_THREADS) sum += f(source.at(i));
+    return g.sum(sum);
+  }
+
+  // The order at which, from the largest down to `least`, as many tokens (or, by mass, as much weight) as `target` are reached,
   // digit by digit of 11, 11 and 10 bits; `above` receives how many (how much) there are above it.
-  template <bool MASS>
-  __device__ uint32_t reach(const Weigher& w, uint32_t least, double target, double scale, double& above) {
-    const double unit = MASS ? 1 / scale : 1.0;
+  __device__ __forceinline__ uint32_t reach(bool mass, const Weigher& w, uint32_t least, double target, double& above) {
+    const double one = mass ? one_of(source.size) : 1.0, unit = 1 / one;
     uint32_t prefix = 0;
     above = 0;
+#pragma unroll 1
     for (int shift = 21;; shift = shift == 21 ? 10 : 0) {
-      const int bits = shift ? 11 : 10;
-      for (int i = tid; i < SA_BINS; i += SA_THREADS) s.bin[i] = 0;
-      if (tid == 0) s.found = s.last = 0;
+      const int width = shift ? 11 : 10;
       __syncthreads();
-      each([&](float x, uint32_t, int) {
+      s.bin[g.tid] = s.bin[g.tid + SA_THREADS] = 0;
+      __syncthreads();
+#pragma unroll 1
+      for (uint32_t i = g.tid; i < source.size; i += SA_THREADS) {
+        const float x = source.at(i);
         const uint32_t o = order_of(x);
-        if (o < least || (shift < 21 && o >> (shift + bits) != prefix)) return;
-        // weights are summed in 64 bits of fixed point: in any order the same
-        atomicAdd(&s.bin[o >> shift & ((1u << bits) - 1)], MASS ? (u64)__builtin_rint(w(x) * scale) : (u64)1);
-      });
-      __syncthreads();
-      // bins from the largest down, two a thread
-      const u64 mine[2] = {s.bin[SA_BINS - 1 - 2 * tid], s.bin[SA_BINS - 2 - 2 * tid]};
-      const u64 upto = sums_upto(mine[0] + mine[1]);
-      if (lane == WAVE - 1) s.best[wave] = upto;
-      __syncthreads();
-      u64 sum[3] = {upto - mine[0] - mine[1]};
-      for (int k = 0; k < wave; ++k) sum[0] += s.best[k];
-      sum[1] = sum[0] + mine[0], sum[2] = sum[1] + mine[1];
-      uint32_t less = 0;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        less += above + (double)sum[k + 1] * unit < target;
-        if (mine[k]) atomicMax(&s.last, (uint32_t)(2 * tid + k));
+        if (o < least || (shift < 21 && o >> (shift + width) != prefix)) continue;
+        atomicAdd(&s.bin[o >> shift & ((1u << width) - 1)], mass ? (u64)__builtin_rint(w(x) * one) : (u64)1);
       }
-      if (less) atomicAdd(&s.found, less);
       __syncthreads();
-      const uint32_t found = min(s.found, s.last);  // sums that are rounded may end just below the target
-      if (found / 2 == (uint32_t)tid) s.above = above + (double)(found % 2 ? sum[1] : sum[0]) * unit;
-      __syncthreads();
-      above = s.above;
-      prefix = prefix << bits | (SA_BINS - 1 - found);
-      __syncthreads();
+      const int b = WD_BINS - 1 - 2 * g.tid;  // from the largest down, two a thread
+      const u64 first = s.bin[b], second = s.bin[b - 1];
+      u64 before, all;
+      const uint32_t thread = g.first(first + second, [&](u64 upto, u64) { return above + (double)upto * unit >= target; }, before, all);
+      // of the thread's two the first if it is enough by itself, or all there is
+      const uint32_t bin = WD_BINS - 1 - 2 * thread;
+      const u64 one_bin = s.bin[bin];
+      const bool take = one_bin && (above + (double)(before + one_bin) * unit >= target || !s.bin[bin - 1]);
+      above += (double)(before + (take ? 0 : one_bin)) * unit;
+      prefix = prefix << width | (take ? bin : bin - 1);
       if (!shift) return prefix;
     }
   }
 
-  // Parts of the row, whole numbers of wavefronts' steps, one behind the other.
-  __device__ uint32_t tile_size() const { return (source.size + SA_TILES * SA_STEP - 1) / (SA_TILES * SA_STEP) * SA_STEP; }
-
-  // Tile t's sum of f(logit, id), put into `to`.
-  template <class V, class F>
-  __device__ void tile_sums(V* to, F f) {
-    const uint32_t size = tile_size(), tiles = (source.size + size - 1) / size;
-    for (uint32_t t = wave; t < SA_TILES; t += SA_WAVES) {
+  // The first place at which the running sum of f(logit, place) is above goal(sum of all); mine: its f.
+  template <class V, class F, class G>
+  __device__ __forceinline__ uint32_t find(V* tiles, F f, G goal, V& mine, V& all) {
+    const uint32_t size = (source.size + SA_TILES - 1) / SA_TILES, per = (size + WAVE - 1) / WAVE * WAVE;  // of a tile
+    uint32_t from = 0, end = source.size;
+    V before = 0, least;
+    if (source.size > SA_LIST) {
+      __syncthreads();
+#pragma unroll 1
+      for (uint32_t t = g.wave; t < SA_TILES; t += SA_WAVES) {
+        V sum = 0;
+#pragma unroll 1
+        for (uint32_t i = t * per + g.lane; i < min((t + 1) * per, source.size); i += WAVE) sum += f(source.at(i), i);
+        sum = sum_of_lanes(sum);
+        if (g.lane == 0) tiles[t] = sum;
+      }
+      __syncthreads();
+      const V x = tiles[g.tid];
+      const uint32_t t = g.first(x, [&](V upto, V total) { return upto > goal(total); }, before, all);
+      from = t * per, end = min(from + per, source.size);
+      least = goal(all);
+    } else {
+      const uint32_t each = (source.size + SA_THREADS - 1) / SA_THREADS;
       V sum = 0;
-      if (t < tiles) {
-        const uint32_t end = min((t + 1) * size, source.size);
-        for (uint32_t at = t * size + lane * 8; at < end; at += SA_STEP) source.eight(at, end, [&](float x, uint32_t id, int) { sum += f(x, id); });
-#pragma unroll
-        for (int d = 1; d < WAVE; d *= 2) sum += __shfl_xor(sum, d);
-      }
-      if (lane == 0) to[t] = sum;
+#pragma unroll 1
+      for (uint32_t i = g.tid * each; i < min((g.tid + 1) * each, source.size); ++i) sum += f(source.at(i), i);
+      all = g.sum(sum);
+      least = goal(all);
     }
-    __syncthreads();
+    return locate(source, g, from, end, before, least, f, mine);
   }
 
-  // The first tile at which the running sum of the tiles' sums `of` passes goal(all of them), and the sum before it; the last
-  // tile with a sum if none does.
-  template <class V, class G>
-  __device__ uint32_t passing(const V* of, G goal, V& before, V& total) {
-    V* sums = reinterpret_cast<V*>(s.sum);
-    const V mine = of[tid], upto = sums_upto(mine);
-    if (lane == WAVE - 1) sums[wave] = upto;
-    if (tid == 0) s.found = s.last = 0;
-    __syncthreads();
-    V sum = upto;
-    total = 0;
-    for (int k = 0; k < SA_WAVES; ++k) {
-      if (k < wave) sum += sums[k];
-      total += sums[k];
-    }
-    if (!(sum > goal(total))) atomicAdd(&s.found, 1u);
-    if (mine > 0) atomicMax(&s.last, (uint32_t)tid);
-    __syncthreads();
-    const uint32_t found = min(s.found, s.last);
-    if ((uint32_t)tid == found) reinterpret_cast<V*>(&s.above)[0] = sum - mine;
-    __syncthreads();
-    before = reinterpret_cast<V*>(&s.above)[0];
-    __syncthreads();
-    return found;
+  // The last place kept of those of order `least`, if the first `ties` of them are.
+  __device__ __forceinline__ uint32_t until(uint32_t least, double ties) {
+    const uint32_t goal = (uint32_t)__builtin_fmin(ties, 4e9) - 1;
+    uint32_t one, all;
+    const uint32_t place = find(s.ties, [&](float x, uint32_t) { return (uint32_t)(order_of(x) == least); }, [&](uint32_t) { return goal; }, one, all);
+    return goal < all ? place : ALL;
   }
 
-  // The first token of tile t at which `before` and the running sum of f are above `goal`, the last one with a
-  // weight if none is; by one wavefront.
-  template <class V, class F>
-  __device__ uint32_t token_passing(uint32_t t, V before, V goal, F f, V& mine, uint32_t size) {
-    const uint32_t end = min((t + 1) * size, source.size);
-    uint32_t last = t * size;
-    mine = 0;
-    for (uint32_t at = t * size; at < end; at += SA_STEP) {
-      V x[8], sum = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = 0;
-      if (at + lane * 8 < end) source.eight(at + lane * 8, end, [&](float l, uint32_t id, int k) { x[k] = f(l, id); });
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum += x[k];
-      const V upto = sums_upto(sum);
-      V run = before + (upto - sum);
-      uint32_t hit = 8, some = 8;
-      V of = 0, of_some = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        run += x[k];
-        if (x[k] > 0) {
-          some = k, of_some = x[k];
-          if (hit == 8 && run > goal) hit = k, of = x[k];
-        }
-      }
-      const u64 hits = __ballot(hit < 8), somes = __ballot(some < 8);
-      if (hits) {
-        const int l = __builtin_ctzll(hits);
-        mine = __shfl(of, l);
-        return at + l * 8 + __shfl(hit, l);
-      }
-      if (somes) {
-        const int l = 63 - __builtin_clzll(somes);
-        mine = __shfl(of_some, l);
-        last = at + l * 8 + __shfl(some, l);
-      }
-      before += __shfl(upto, WAVE - 1);
-    }
-    return last;
+  // Of the orders from `least` on, the fewest that weigh `target`: the last one of them; `needed` receives how many of it.
+  __device__ __forceinline__ uint32_t heaviest(const Weigher& w, uint32_t least, double target, double& needed) {
+    double above;
+    const uint32_t o = reach(true, w, least, target, above);
+    above = sum([&](float x) { return order_of(x) > o ? w(x) : 0.0; });
+    needed = __builtin_fmax(__builtin_ceil((target - above) / w(logit_of(o))), 1.0);
+    return o;
   }
 
-  // The token drawn, as its place, and what it and all that are kept weigh.  `sum`: what the tokens that top_k leaves weigh if it does
-  // not limit.
-  __device__ uint32_t draw(const Limits& l, const Weigher& w, double sum, double& mine, double& all) {
-    // kept: orders above `least`, and of those at it the first `ties` (all of them if negative)
+  // The token drawn, as its place, and what it and all that are kept weigh.  `whole`: what the tokens that top_k leaves weigh if it
+  // does not limit.
+  __device__ __forceinline__ uint32_t draw(const Limits& l, const Weigher& w, double whole, double& mine, double& all) {
     uint32_t least = NOTHING + 1;
-    double ties = -1, above;
-    if (l.top_k) {
-      const uint32_t o = reach<false>(w, 0, (double)l.top_k, 1.0, above);
-      if (o > NOTHING) least = o, ties = (double)l.top_k - above;
-      if (l.by_mass) {
-        sum = 0;
-        each([&](float x, uint32_t, int) { sum += order_of(x) > least || (ties < 0 && order_of(x) == least) ? w(x) : 0.0; });
-        sum = sum_of(sum) + (ties > 0 ? ties * w(logit_of(least)) : 0.0);
+    double ties = -1;  // of those at `least` so many are kept; all of them if negative
+    double target = (double)l.top_k;
+#pragma unroll 1
+    for (int by_mass = 0; by_mass < 2; ++by_mass) {  // the same code for both limits
+      if (!(by_mass ? l.by_mass : l.top_k != 0)) continue;
+      if (by_mass) {
+        if (l.top_k)
+          whole = sum([&](float x) { return order_of(x) > least || (ties < 0 && order_of(x) == least) ? w(x) : 0.0; }) +
+                  (ties > 0 ? ties * w(logit_of(least)) : 0.0);
+        target = (double)l.top_p * whole;
       }
-    }
-    if (l.by_mass) {
-      const double target = (double)l.top_p * sum, scale = __builtin_ldexp(1.0, 62 - (32 - __builtin_clz(source.size)));
-      const uint32_t o = reach<true>(w, least, target, scale, above);
-      above = 0;
-      each([&](float x, uint32_t, int) { above += order_of(x) > o ? w(x) : 0.0; });
-      above = sum_of(above);
+      double above;
+      const uint32_t o = reach(by_mass, w, by_mass ? least : 0, target, above);
+      if (!by_mass) {
+        if (o > NOTHING) least = o, ties = target - above;
+        continue;
+      }
+      above = sum([&](float x) { return order_of(x) > o ? w(x) : 0.0; });
       const double needed = __builtin_fmax(__builtin_ceil((target - above) / w(logit_of(o))), 1.0);
       ties = o == least && ties >= 0 ? __builtin_fmin(ties, needed) : needed;
       least = o;
     }
-    uint32_t until = 0xFFFFFFFFu;  // the last place kept of those at `least`
-    if (ties >= 0) {
-      auto tie = [&](float x, uint32_t) { return (uint32_t)(order_of(x) == least); };
-      tile_sums(s.ties, tie);
-      const uint32_t goal = (uint32_t)__builtin_fmin(ties, 4e9) - 1;
-      uint32_t before, total, one;
-      const uint32_t tile = passing(s.ties, [&](uint32_t) { return goal; }, before, total);
-      if (goal < total) until = token_passing(tile, before, goal, tie, one, tile_size());
-      __syncthreads();
-    }
-    auto weight = [&](float x, uint32_t place) {
-      const uint32_t o = order_of(x);
-      if (o < least || (o == least && place > until)) return 0.0;
-      const double y = w(x);
-      return l.by_weight && y < (double)l.min_p ? 0.0 : y;
-    };
-    tile_sums(s.tile, weight);
-    double before;
-    const uint32_t tile = passing(s.tile, [&](double total) { return (double)l.uniform * total; }, before, all);
-    const uint32_t token = token_passing(tile, before, (double)l.uniform * all, weight, mine, tile_size());
-    __syncthreads();
-    return token;
+    const Kept kept{least, ties >= 0 ? until(least, ties) : ALL, l.by_weight ? (double)l.min_p : 0.0};
+    return find(s.tile, [&](float x, uint32_t place) { return kept.of(order_of(x), place, w(x)); },
+                [&](double total) { return (double)l.uniform * total; }, mine, all);
   }
 };
 
+// Puts out a row's token.
+__device__ inline void put_token(const tt_sample_args& a, int64_t r, uint32_t token, double mine, double all) {
+  a.tokens[r] = (int32_t)token;
+  if (a.logprobs) a.logprobs[r] = token == ALL ? -__builtin_inff() : (float)log(mine / all);
+}
+
+// The tokens that the parts' lists hold from the order `bar` on, in the order of ids, to s.order and s.id; how many there are, which may
+// be more than there is room for: then none are taken.  `start`: where those of part tid begin.
+__device__ __forceinline__ uint32_t gather(Group& g, const Part* parts, const Listed* lists, int n, uint32_t bar, uint32_t& start) {
+  SampleShared& s = g.s;
+  __syncthreads();
+  s.ties[g.tid] = 0;
+  __syncthreads();
+  for (int p = g.wave; p < n; p += SA_WAVES) {
+    const uint32_t order = lists[(int64_t)p * PT_LIST + g.lane].order;  // past the count there is anything
+    const uint32_t count = __popcll(__ballot(g.lane < (int)parts[p].count && order >= bar));
+    if (g.lane == 0) s.ties[p] = count;
+  }
+  __syncthreads();
+  const uint32_t size = g.sum(s.ties[g.tid], start);
+  s.ties[g.tid] = start;
+  __syncthreads();
+  if (size <= SA_LIST) {
+    for (int p = g.wave; p < n; p += SA_WAVES) {
+      const Listed entry = lists[(int64_t)p * PT_LIST + g.lane];
+      const bool take = g.lane < (int)parts[p].count && entry.order >= bar;
+      const u64 in = __ballot(take);
+      const uint32_t to = s.ties[p] + __popcll(in & (((u64)1 << g.lane) - 1));
+      if (take) s.order[to] = entry.order, s.id[to] = entry.id;
+    }
+  }
+  __syncthreads();
+  return size;
+}
+
+// The largest logit of a row's parts.
+__device__ inline float most_of(const Part* parts, int64_t n) {
+  uint32_t best = 0;
+  for (int64_t p = threadIdx.x % WAVE; p < n; p += WAVE) best = max(best, order_of(parts[p].most));
+  return logit_of(max_of_lanes(best));
+}
+
 // A row by a workgroup, from its parts.  Without limits the part that the random number falls into is read again; with limits
-// the tokens listed decide if the last one kept is above all bars; else the row is passed over for every question.
+// the tokens listed decide if the last one kept is above all bars; else the row is left to be gone over again.
 template <class T>
-__global__ __launch_bounds__(SA_THREADS) void k_sample(tt_sample_args a, const Part* parts, const Listed* lists, int64_t per_row) {
+__global__ __launch_bounds__(SA_THREADS) void k_sample(tt_sample_args a, Space space) {
   __shared__ SampleShared s;
   const int64_t r = blockIdx.x;
-  const int tid = threadIdx.x, lane = tid % WAVE, wave = tid / WAVE;
-  parts += r * per_row;
-  lists += r * per_row * PT_LIST;
-  const Limits l = limits_of(a, r);
-  const int n = (int)per_row;
-  const RowSource<T> whole{static_cast<const T*>(a.logits) + r * a.logits_stride, (uint32_t)a.vocab};
-  Sampler<RowSource<T>> row{whole, s, tid, lane, wave};
+  const int tid = threadIdx.x;
+  const Part* parts = space.parts + r * space.per_row;
+  Limits l = limits_of(a, r);
+  const int n = (int)space.per_row;
+  const RowSource<T> row{static_cast<const T*>(a.logits) + r * a.logits_stride, (uint32_t)a.vocab};
+  Group g{s, tid, tid % WAVE, tid / WAVE};
 
-  // the largest logit, and its first part
-  u64 best = 0;
-  uint32_t bar = NOTHING + 1;
+  u64 best = 0, bar = NOTHING + 1;  // the largest logit and its first part; the highest bar
   for (int p = tid; p < n; p += SA_THREADS) {
     best = max(best, (u64)order_of(parts[p].most) << 32 | ~(uint32_t)p);
-    bar = max(bar, parts[p].bar);
+    bar = max(bar, (u64)parts[p].bar);
   }
-#pragma unroll
-  for (int d = 1; d < WAVE; d *= 2) {
-    best = max(best, __shfl_xor(best, d));
-    bar = max(bar, __shfl_xor(bar, d));
-  }
-  if (lane == 0) s.best[wave] = best, s.ties[wave] = bar;
-  __syncthreads();
-  for (int w = 0; w < SA_WAVES; ++w) best = max(best, s.best[w]), bar = max(bar, s.ties[w]);
-  __syncthreads();
+  best = g.most(best);
   const float most = logit_of((uint32_t)(best >> 32));
+  if (tid == 0) space.state[r] = DONE;
   if (best >> 32 <= NOTHING) {
-    if (tid == 0) {
-      a.tokens[r] = -1;
-      if (a.logprobs) a.logprobs[r] = -__builtin_inff();
-    }
+    if (tid == 0) put_token(a, r, ALL, 0, 1);
     return;
   }
-  if (l.single) {
-    const uint32_t first = ~(uint32_t)best * PT_TOKENS, end = min(first + PT_TOKENS, whole.size);
-    if (tid == 0) s.token = 0xFFFFFFFFu;
-    __syncthreads();
-    for (uint32_t v = first + tid; v < end; v += SA_THREADS)
-      if (order_of((float)whole.row[v]) == best >> 32) atomicMin(&s.token, v);
-    __syncthreads();
-    if (tid == 0) {
-      a.tokens[r] = (int32_t)s.token;
-      if (a.logprobs) a.logprobs[r] = 0.0f;
-    }
-    return;
-  }
+  double mine = 1, all = 1, before;
+  uint32_t token;
   const Weigher w(most, l.temperature);
   auto weight_of = [&](int p) { return p < n && parts[p].sum > 0 ? parts[p].sum * w(parts[p].most) : 0.0; };
-  double mine = 0, all = 0;
-  uint32_t token;
-  if (!l.limited() && n <= SA_TILES) {
-    s.tile[tid] = weight_of(tid);
-    __syncthreads();
-    double before;
-    const uint32_t part = row.passing(s.tile, [&](double sum) { return (double)l.uniform * sum; }, before, all);
-    const RowSource<T> some{whole.row, min((part + 1) * (uint32_t)PT_TOKENS, whole.size)};
-    Sampler<RowSource<T>> last{some, s, tid, lane, wave};
-    token = last.token_passing(part, before, (double)l.uniform * all, [&](float x, uint32_t) { return w(x); }, mine, PT_TOKENS);
-  } else {
-    double sum = 0;
-    for (int p = tid; p < n; p += SA_THREADS) sum += weight_of(p);
-    sum = row.sum_of(sum);
-    // what the lists hold above the bar, in the order of ids
-    bool listed = l.limited() && n <= SA_TILES && bar != 0xFFFFFFFFu;
-    uint32_t size = 0;
-    if (listed) {
-      for (int p = wave; p < SA_TILES; p += SA_WAVES) {
-        const bool in = p < n && lane < (int)parts[p].count && lists[(int64_t)p * PT_LIST + lane].order >= bar;
-        const uint32_t count = __popcll(__ballot(in));
-        if (lane == 0) s.ties[p] = count;
-      }
-      __syncthreads();
-      const uint32_t count = s.ties[tid], upto = row.sums_upto(count);
-      if (lane == WAVE - 1) s.best[wave] = upto;
-      __syncthreads();
-      uint32_t at = upto - count;
-      for (int k = 0; k < SA_WAVES; ++k) {
-        if (k < wave) at += (uint32_t)s.best[k];
-        size += (uint32_t)s.best[k];
-      }
-      s.ties[tid] = at;
-      __syncthreads();
-      listed = size <= SA_LIST;
-      if (listed) {
-        for (int p = wave; p < n; p += SA_WAVES) {
-          const Listed entry = lane < (int)parts[p].count ? lists[(int64_t)p * PT_LIST + lane] : Listed{0, 0};
-          const u64 in = __ballot(entry.order >= bar);
-          const uint32_t to = s.ties[p] + __popcll(in & (((u64)1 << lane) - 1));
-          if (entry.order >= bar) s.order[to] = entry.order, s.id[to] = entry.id;
-        }
-      }
-      __syncthreads();
+  if (l.single || (!l.limited() && n <= SA_TILES)) {
+    uint32_t p = ~(uint32_t)best;
+    double goal = 0;
+    before = 0;
+    if (!l.single) {
+      p = g.first(weight_of(tid), [&](double upto, double total) { return upto > (double)l.uniform * total; }, before, all);
+      goal = (double)l.uniform * all;
     }
-    const ListSource top{s.order, size};
-    Sampler<ListSource> short_list{top, s, tid, lane, wave};
-    if (listed && bar > NOTHING + 1) {
-      // tokens below the bar are not listed: none of them may be kept, or be needed for a sum
-      const bool light = l.by_weight && w(logit_of(bar)) < (double)l.min_p;
-      if (l.top_k && size < l.top_k) {
-        listed = light && !l.by_mass;
-      } else if (l.by_mass && !l.top_k) {
-        double there = 0;
-        short_list.each([&](float x, uint32_t, int) { there += w(x); });
-        listed = short_list.sum_of(there) >= (double)l.top_p * sum * (1 + 1e-12);
-      } else if (!l.top_k) {
-        listed = light;
-      }
-    }
-    if (listed) token = s.id[short_list.draw(l, w, sum, mine, all)];
-    else token = row.draw(l, w, sum, mine, all);
+    token = locate(row, g, p * space.size, min((p + 1) * space.size, row.size), before, goal,
+                   [&](float x, uint32_t) { return l.single ? (x == most ? 1.0 : 0.0) : w(x); }, mine);
+    if (tid == 0) put_token(a, r, token, mine, all);
+    return;
   }
+  double whole = 0;
+  for (int p = tid; p < n; p += SA_THREADS) whole += weight_of(p);
+  whole = g.sum(whole);
+  bar = g.most(bar);
+  bool listed = l.limited() && n <= SA_TILES && bar != ALL;
+  uint32_t size = 0, start;
+  if (listed) {
+    size = gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, (uint32_t)bar, start);
+    listed = size <= SA_LIST;
+  }
+  const ListSource top{s.order, size};
+  Sampler<ListSource> list{top, g, s};
+  if (listed && bar > NOTHING + 1) {
+    // tokens below the bar are not listed: none of them may be kept, or be needed for a sum
+    const bool light = l.by_weight && w(logit_of((uint32_t)bar)) < (double)l.min_p;
+    if (l.top_k && size < l.top_k) {
+      listed = light && !l.by_mass;
+    } else if (l.by_mass && !l.top_k) {
+      if (!(list.sum([&](float x) { return w(x); }) >= (double)l.top_p * whole * (1 + 1e-12))) {
+        listed = light;  // the nucleus goes below the bar, what min_p leaves does not
+        l.by_mass = false;
+      }
+    } else if (!l.top_k) {
+      listed = light;
+    }
+  }
+  if (listed) {
+    token = s.id[list.draw(l, w, whole, mine, all)];
+    if (tid == 0) put_token(a, r, token, mine, all);
+    return;
+  }
+  __syncthreads();
   if (tid == 0) {
-    a.tokens[r] = (int32_t)token;
-    if (a.logprobs) a.logprobs[r] = (float)log(mine / all);
+    space.whole[r] = whole;
+    s.found = WD_SLOTS;
+    if (space.slots && !l.top_k && n <= SA_TILES) s.found = atomicAdd(space.slots_taken, 1u);
+    space.state[r] = s.found < WD_SLOTS ? s.found : LEFT;
+    if (s.found < WD_SLOTS) space.slots[s.found].row = r;
+  }
+  __syncthreads();
+  if (s.found < WD_SLOTS)
+    for (int i = tid; i < WD_BINS; i += SA_THREADS) space.slots[s.found].mass[i] = 0;
+}
+
+// ------------------------------------------- rows that have to be gone over again
+//
+// Where the nucleus goes below the bars, weights are summed by depth (32 bins to a halving), which gives the bin that it ends in;
+// then each part sums up what is above that bin and lists what is in it.
+
+// The bin of a token.
+__device__ inline uint32_t bin_of(const Weigher& w, float x) { return min((uint32_t)(w.depth(x) * -32.0f), (uint32_t)WD_BINS - 1); }
+
+// The weight of the places from `at` up to `end` into bins of LDS, by a workgroup.
+template <class T>
+__device__ __forceinline__ void add_to_bins(const RowSource<T>& row, uint32_t at, uint32_t end, int threads, const Weigher& w, double one, u64* bin) {
+  for (uint32_t i = at + threadIdx.x; i < end; i += threads) {
+    const float x = row.at(i);
+    const double y = w(x);
+    if (y > 0) atomicAdd(&bin[bin_of(w, x)], (u64)__builtin_rint(y * one));
   }
 }
 
-int64_t parts_of(int64_t vocab) { return std::max((vocab + PT_TOKENS - 1) / PT_TOKENS, (int64_t)1); }
-int64_t batch_of(int64_t rows, int64_t vocab) { return std::min(rows, std::max(PT_BATCH / parts_of(vocab), (int64_t)1)); }
+// A part of such a row, by a wavefront: kept, and sum, are what weighs above bin `last`; of the bin the tokens are listed.
+template <class T>
+__device__ __forceinline__ void part_above(const RowSource<T>& row, const Space& space, int64_t id, uint32_t p, const Weigher& w, uint32_t last,
+                                           double min_p) {
+  const int lane = threadIdx.x % WAVE;
+  const uint32_t first = p * space.size, end = min(first + space.size, row.size);
+  double sum = 0, kept = 0;
+  uint32_t count = 0;
+  Listed* to = space.lists + id * PT_LIST;
+  for (uint32_t at = first; at < end; at += WAVE) {
+    const float x = at + lane < end ? row.at(at + lane) : -__builtin_inff();
+    const double y = w(x);
+    const uint32_t b = bin_of(w, x);
+    if (y > 0 && b < last) sum += y, kept += y < min_p ? 0.0 : y;
+    const u64 in = __ballot(y > 0 && b == last);
+    const uint32_t place = count + __popcll(in & (((u64)1 << lane) - 1));
+    if ((in >> lane & 1) && place < PT_LIST) to[place] = Listed{order_of(x), at + lane};
+    count += __popcll(in);
+  }
+  sum = sum_of_lanes(sum), kept = sum_of_lanes(kept);
+  if (lane == 0) {
+    Part& part = space.parts[id];
+    part.sum = sum, part.kept = kept, part.count = count;
+  }
+}
+
+// The last bin of the nucleus, by a workgroup of WD_BINS / N threads.
+template <int N>
+__device__ __forceinline__ uint32_t last_bin(const u64* bin, double target, u64* of_wave, uint32_t* found) {
+  const int tid = threadIdx.x, lane = tid % WAVE, wave = tid / WAVE;
+  u64 x[N], mine = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) mine += x[k] = bin[N * tid + k];
+  const u64 upto = sums_upto(mine);
+  __syncthreads();  // what is shared may still be read
+  if (tid == 0) *found = 0;
+  if (lane == WAVE - 1) of_wave[wave] = upto;
+  __syncthreads();
+  u64 run = upto - mine;
+  for (int k = 0; k < wave; ++k) run += of_wave[k];
+  uint32_t less = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) run += x[k], less += !((double)run >= target);
+  less = sum_of_lanes(less);
+  if (lane == 0 && less) atomicAdd(found, less);
+  __syncthreads();
+  const uint32_t last = *found;
+  __syncthreads();
+  return min(last, (uint32_t)WD_BINS - 1);
+}
+
+// The rows in slots: the bins of their weights.
+template <class T>
+__global__ __launch_bounds__(PT_THREADS) void k_sample_bins(tt_sample_args a, Space space) {
+  __shared__ u64 s_bin[WD_BINS];
+  const uint32_t slots = min(*space.slots_taken, (uint32_t)WD_SLOTS), across = (uint32_t)((space.per_row + WD_SEGMENT - 1) / WD_SEGMENT);
+  for (uint32_t item = blockIdx.x; item < slots * across; item += gridDim.x) {
+    Slot& slot = space.slots[item / across];
+    const int64_t r = slot.row;
+    const Limits l = limits_of(a, r);
+    if (!l.by_mass) continue;
+    const RowSource<T> row{static_cast<const T*>(a.logits) + r * a.logits_stride, (uint32_t)a.vocab};
+    const Weigher w(most_of(space.parts + r * space.per_row, space.per_row), l.temperature);
+    const uint32_t from = item % across * WD_SEGMENT * space.size;
+    for (int i = threadIdx.x; i < WD_BINS; i += PT_THREADS) s_bin[i] = 0;
+    __syncthreads();
+    add_to_bins(row, from, min(from + WD_SEGMENT * space.size, row.size), PT_THREADS, w, one_of((uint32_t)a.vocab), s_bin);
+    __syncthreads();
+    for (int i = threadIdx.x; i < WD_BINS; i += PT_THREADS)
+      if (s_bin[i]) atomicAdd(&slot.mass[i], s_bin[i]);
+    __syncthreads();
+  }
+}
+
+// Their parts.
+template <class T>
+__global__ __launch_bounds__(PT_THREADS) void k_sample_above(tt_sample_args a, Space space) {
+  __shared__ u64 s_wave[PT_THREADS / WAVE];
+  __shared__ uint32_t s_found;
+  const uint32_t slots = min(*space.slots_taken, (uint32_t)WD_SLOTS), across = (uint32_t)((space.per_row + WD_SEGMENT - 1) / WD_SEGMENT);
+  for (uint32_t item = blockIdx.x; item < slots * across; item += gridDim.x) {
+    const Slot& slot = space.slots[item / across];
+    const int64_t r = slot.row;
+    const Limits l = limits_of(a, r);
+    const RowSource<T> row{static_cast<const T*>(a.logits) + r * a.logits_stride, (uint32_t)a.vocab};
+    const Weigher w(most_of(space.parts + r * space.per_row, space.per_row), l.temperature);
+    const double target = (double)l.top_p * space.whole[r] * one_of((uint32_t)a.vocab);
+    const uint32_t last = l.by_mass ? last_bin<WD_BINS / PT_THREADS>(slot.mass, target, s_wave, &s_found) : WD_BINS;
+    const uint32_t stop = min((item % across + 1) * WD_SEGMENT, (uint32_t)space.per_row);
+    for (uint32_t p = item % across * WD_SEGMENT + threadIdx.x / WAVE; p < stop; p += PT_THREADS / WAVE)
+      part_above(row, space, r * space.per_row + p, p, w, last, l.by_weight ? (double)l.min_p : 0.0);
+  }
+}
+
+// The tokens of rows that are left, or whose parts know what is above their last bin: the bin's tokens are put in order, the part
+// is found, and the token in it.
+template <class T>
+__global__ __launch_bounds__(SA_THREADS) void k_sample_rest(tt_sample_args a, Space space) {
+  __shared__ SampleShared s;
+  const int64_t r = blockIdx.x;
+  const uint32_t state = space.state[r];
+  if (state == DONE) return;
+  const int tid = threadIdx.x, n = (int)space.per_row;
+  const Limits l = limits_of(a, r);
+  const RowSource<T> row{static_cast<const T*>(a.logits) + r * a.logits_stride, (uint32_t)a.vocab};
+  Group g{s, tid, tid % WAVE, tid / WAVE};
+  const Part* parts = space.parts + r * space.per_row;
+  const Weigher w(most_of(parts, n), l.temperature);
+  const double whole = space.whole[r], target = (double)l.top_p * whole, one = one_of((uint32_t)a.vocab);
+  const double min_p = l.by_weight ? (double)l.min_p : 0.0;
+  double mine = 0, all = 0;
+  uint32_t token, last = WD_BINS, start = 0, size = 0;
+  bool again = l.top_k || n > SA_TILES;
+  if (!again) {
+    if (l.by_mass) {
+      const u64* bins = s.bin;
+      if (state == LEFT) {
+        __syncthreads();
+        s.bin[tid] = s.bin[tid + SA_THREADS] = 0;
+        __syncthreads();
+        add_to_bins(row, 0, row.size, SA_THREADS, w, one, s.bin);
+        __syncthreads();
+      } else {
+        bins = space.slots[state].mass;
+      }
+      last = last_bin<WD_BINS / SA_THREADS>(bins, target * one, s.of_wave, &s.found);
+    }
+    if (state == LEFT)
+      for (int p = g.wave; p < n; p += SA_WAVES) part_above(row, space, r * space.per_row + p, p, w, last, min_p);
+    __syncthreads();  // a workgroup sees what it has written itself
+    u64 longest = 0;
+    for (int p = tid; p < n; p += SA_THREADS) longest = max(longest, (u64)parts[p].count);
+    longest = g.most(longest);
+    again = longest > PT_LIST;  // too many tokens of the same depth
+    if (!again) size = gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, 0, start);
+    again = again || size > SA_LIST;
+  }
+  if (again) {
+    Sampler<RowSource<T>> whole_row{row, g, s};
+    token = whole_row.draw(l, w, whole, mine, all);
+  } else {
+    Kept kept{0, ALL, min_p};
+    uint32_t until = ALL;  // as an id
+    if (size) {
+      const ListSource in_bin{s.order, size};
+      Sampler<ListSource> list{in_bin, g, s};
+      const double above = g.sum(tid < n ? parts[tid].sum : 0.0);
+      double needed;
+      kept.least = list.heaviest(w, NOTHING + 1, target - above, needed);
+      kept.until = list.until(kept.least, needed);
+      if (kept.until < size) until = s.id[kept.until];
+    }
+    double sum = 0, before;
+    if (tid < n) {
+      sum = parts[tid].kept;
+      const uint32_t count = size ? parts[tid].count : 0;
+#pragma unroll 1
+      for (uint32_t k = start; k < start + count; ++k) sum += kept.of(s.order[k], k, w(logit_of(s.order[k])));
+    }
+    const uint32_t p = g.first(sum, [&](double upto, double total) { return upto > (double)l.uniform * total; }, before, all);
+    token = locate(row, g, p * space.size, min((p + 1) * space.size, row.size), before, (double)l.uniform * all,
+                   [&](float x, uint32_t id) {
+                     const double y = w(x);
+                     const uint32_t b = bin_of(w, x), o = order_of(x);
+                     if (b > last || y < min_p) return 0.0;
+                     return b == last && (o < kept.least || (o == kept.least && id > until)) ? 0.0 : y;
+                   },
+                   mine);
+  }
+  if (tid == 0) put_token(a, r, token, mine, all);
+}
+
+// Parts of 2,048 tokens, which keep the card busy with a wavefront each and their lists short; where that would leave most of it
+// idle, of 512 or 1,024 as long as a row has at most 128.
+uint32_t part_steps(int64_t rows, int64_t vocab) {
+  if (rows * vocab >= (int64_t)1 << 20) return 4;
+  return vocab <= 128 * PT_STEP ? 1 : vocab <= 256 * PT_STEP ? 2 : 4;
+}
+
+Space space_of(int64_t rows, int64_t vocab, void* at) {
+  Space s{};
+  s.size = part_steps(rows, vocab) * PT_STEP;
+  s.per_row = std::max((vocab + s.size - 1) / s.size, (int64_t)1);
+  const int64_t batch = std::min(rows, std::max(PT_BATCH / s.per_row, (int64_t)1)), parts = batch * s.per_row;
+  // Many workgroups go over a row again where that is three more launches to a call that is long anyway.
+  const bool wide = parts >= 2048 && s.per_row >= 16 && s.per_row <= SA_TILES;
+  s.slots_taken = static_cast<uint32_t*>(at);
+  s.whole = reinterpret_cast<double*>(static_cast<char*>(at) + 16);
+  s.parts = reinterpret_cast<Part*>(s.whole + batch);
+  s.lists = reinterpret_cast<Listed*>(s.parts + parts);
+  s.state = reinterpret_cast<uint32_t*>(s.lists + parts * PT_LIST);
+  s.bytes = 16 + batch * 8 + parts * (int64_t)(sizeof(Part) + PT_LIST * sizeof(Listed)) + (batch + 1) / 2 * 8;
+  if (wide) {
+    s.slots = reinterpret_cast<Slot*>(s.state + (batch + 1) / 2 * 2);
+    s.bytes += WD_SLOTS * (int64_t)sizeof(Slot);
+  }
+  return s;
+}
 
 template <class T>
 void enqueue_sample(const tt_sample_args& a, hipStream_t st) {
-  const int64_t per_row = parts_of(a.vocab), batch = batch_of(a.rows, a.vocab);
-  Part* parts = static_cast<Part*>(a.workspace);
-  Listed* lists = reinterpret_cast<Listed*>(parts + batch * per_row);
+  const Space space = space_of(a.rows, a.vocab, a.workspace);
+  const int64_t batch = std::min(a.rows, std::max(PT_BATCH / space.per_row, (int64_t)1));
   for (int64_t r = 0; r < a.rows; r += batch) {
     tt_sample_args some = a;
     some.rows = std::min(batch, a.rows - r);
@@ -597,17 +893,23 @@ void enqueue_sample(const tt_sample_args& a, hipStream_t st) {
     if (some.top_k) some.top_k += r;
     if (some.logprobs) some.logprobs += r;
     constexpr int64_t waves = PT_THREADS / WAVE;
-    hipLaunchKernelGGL(k_sample_parts<T>, dim3((uint32_t)((some.rows * per_row + waves - 1) / waves)), dim3(PT_THREADS), 0, st, some, parts,
-                       lists, per_row);
-    hipLaunchKernelGGL(k_sample<T>, dim3((uint32_t)some.rows), dim3(SA_THREADS), 0, st, some, parts, lists, per_row);
+    auto* k = space.size == PT_STEP ? k_sample_parts<T, 1> : space.size == 2 * PT_STEP ? k_sample_parts<T, 2> : k_sample_parts<T, 4>;
+    hipLaunchKernelGGL(k, dim3((uint32_t)((some.rows * space.per_row + waves - 1) / waves)), dim3(PT_THREADS), 0, st, some, space);
+    hipLaunchKernelGGL(k_sample<T>, dim3((uint32_t)some.rows), dim3(SA_THREADS), 0, st, some, space);
+    if (!a.top_k && !a.top_p && !a.min_p && space.per_row <= SA_TILES) continue;  // no row is left
+    if (space.slots && (a.top_p || a.min_p)) {
+      const int64_t items = std::min(some.rows, (int64_t)WD_SLOTS) * ((space.per_row + WD_SEGMENT - 1) / WD_SEGMENT);
+      const dim3 grid((uint32_t)std::min(items, (int64_t)1024));
+      hipLaunchKernelGGL(k_sample_bins<T>, grid, dim3(PT_THREADS), 0, st, some, space);
+      hipLaunchKernelGGL(k_sample_above<T>, grid, dim3(PT_THREADS), 0, st, some, space);
+    }
+    hipLaunchKernelGGL(k_sample_rest<T>, dim3((uint32_t)some.rows), dim3(SA_THREADS), 0, st, some, space);
   }
 }
 
 }  // namespace
 
-int64_t sample_workspace(int64_t rows, int64_t vocab) {
-  return batch_of(rows, vocab) * parts_of(vocab) * (int64_t)(sizeof(Part) + PT_LIST * sizeof(Listed));
-}
+int64_t sample_workspace(int64_t rows, int64_t vocab) { return space_of(rows, vocab, nullptr).bytes; }
 
 hipError_t launch_sample(const tt_sample_args& a, hipStream_t st) {
   if (a.type == TT_F32) enqueue_sample<float>(a, st);

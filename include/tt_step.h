@@ -128,7 +128,7 @@ typedef struct tt_sample_args {
  * that weigh min_p or more (all limits keep the first token).  The token drawn is the
  * first, by ids, at which the running sum of the kept weights is above uniform times their sum;
  * logprobs receives ln(w / sum of the kept weights).
- * Weights and sums are held in 64 bits.  A logit that is NaN counts as -infinity; a
+ * Weights and sums are held in 64 bits; a weight below 2^-1000 is zero.  A logit that is NaN counts as -infinity; a
  * token of -infinity is never drawn, and a row without any other gets token -1 and
  * -infinity.  Where logits are +infinity the others weigh nothing.
  * Returns TT_OK, TT_EINVAL, TT_ETOOBIG or TT_EHIP. */

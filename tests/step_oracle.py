@@ -101,7 +101,7 @@ def sample(logits, uniform, temperature=None, top_k=None, top_p=None, min_p=None
         else:
             with np.errstate(invalid="ignore"):
                 w = np.exp((x[order] - top) / t)
-            w[x[order] == -np.inf] = 0
+            w[(x[order] == -np.inf) | (w < 2.0**-1000)] = 0
         n = len(order)
         if top_k is not None and top_k[r] > 0:
             n = min(n, int(top_k[r]))
