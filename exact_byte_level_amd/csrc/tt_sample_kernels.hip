@@ -226,38 +226,35 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, S
     if (limits.limited()) {
       // The bar is the 32nd largest of the lanes' maxima, which about 64 ln 2 = 44 tokens are not below; of the largest
       // 16, 8, 4, 2, 1 where the list would not hold them.
-      uint32_t bar = 0, count = 0;
-      float from = 0;
+      uint32_t bar = 0, count = 0, counts = 0, in = 0;  // in: a bit for each token of the lane
       for (int among = WAVE / 2; among; among /= 2) {
         bar = 0;
         for (uint32_t bit = 1u << 31; bit; bit >>= 1)
           if (__popcll(__ballot(own >= (bar | bit))) >= among) bar |= bit;
         bar = max(bar, NOTHING + 1);
-        from = logit_of(bar);
-        count = 0;
+        const float from = logit_of(bar);
+        in = 0;
 #pragma unroll
-        for (int i = 0; i < MINE; ++i) count += __popcll(__ballot(x[i] >= from));
+        for (int i = MINE - 1; i >= 0; --i) in = in + in + (uint32_t)(x[i] >= from);
+        // counts of the steps, a byte each, which hold what a list does: eight tokens of a lane, the lanes, the steps
+        counts = in - (in >> 1 & 0x55555555u);
+        counts = (counts & 0x33333333u) + (counts >> 2 & 0x33333333u);
+        counts = (counts + (counts >> 4)) & 0x0F0F0F0Fu;
+        count = sum_of_lanes((uint32_t)__popc(in));
         if (count <= PT_LIST) break;
       }
       if (count > PT_LIST) bar = ALL, count = 0;
       part.bar = bar, part.count = count;
       if (count) {
-        // places by ids: eight tokens of a lane, the lanes, the steps; sums of at most 64 fit a byte each
-        uint32_t counts = 0;
-#pragma unroll
-        for (int i = 0; i < MINE; ++i) counts += (uint32_t)(x[i] >= from) << (i / 8 * 8);
         const uint32_t upto = sums_upto(counts), all = of_lane(upto, WAVE - 1);
-        uint32_t step = 0;
+        // where the lane's tokens of each step go, a byte each again
+        const uint32_t at = upto - counts + (all << 8) + (all << 16) + (all << 24);
         Listed* to = space.lists + id * PT_LIST;
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-          uint32_t at = step + ((upto - counts) >> (8 * q) & 255);
-          if (counts >> (8 * q) & 255) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (x[q * 8 + k] >= from) to[at++] = Listed{order_of(x[q * 8 + k]), first + q * PT_STEP + lane * 8 + k};
-          }
-          step += all >> (8 * q) & 255;
+        for (uint32_t left = in; left; left &= left - 1) {  // a few; registers have no numbers, so they are read again
+          const uint32_t i = __builtin_ctz(left), q = i / 8;
+          const uint32_t place = (at >> (8 * q) & 255) + __popc(in & ((1u << i) - 1) & ~((1u << (8 * q)) - 1));
+          const uint32_t v = first + q * PT_STEP + lane * 8 + i % 8;
+          to[place] = Listed{order_of((float)row[v]), v};
         }
       }
     }
@@ -290,6 +287,17 @@ struct RowSource {
   const T* row;
   uint32_t size;
   __device__ float at(uint32_t place) const { return (float)row[place]; }
+  // Eight from `place` on; -infinity from `end` on.
+  __device__ void eight(uint32_t place, uint32_t end, float (&x)[8]) const {
+    if (place + 8 <= end) {
+      const auto v = *reinterpret_cast<const typename Eight<T>::type*>(row + place);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = (float)v[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = place + k < end ? (float)row[place + k] : -__builtin_inff();
+    }
+  }
 };
 struct ListSource {
   const uint32_t* order;
@@ -547,22 +555,40 @@ __device__ __forceinline__ uint32_t gather(Group& g, const Part* parts, const Li
   __syncthreads();
   s.ties[g.tid] = 0;
   __syncthreads();
-  for (int p = g.wave; p < n; p += SA_WAVES) {
-    const uint32_t order = lists[(int64_t)p * PT_LIST + g.lane].order;  // past the count there is anything
-    const uint32_t count = __popcll(__ballot(g.lane < (int)parts[p].count && order >= bar));
-    if (g.lane == 0) s.ties[p] = count;
+  constexpr int MANY = 8;  // lists of a wavefront that are on their way together
+  Listed entry[MANY];
+  uint32_t count[MANY];
+  auto take = [&](int from) {
+#pragma unroll
+    for (int k = 0; k < MANY; ++k) {
+      const int p = min(from + k * SA_WAVES, n - 1);
+      entry[k] = lists[(int64_t)p * PT_LIST + g.lane];  // past the count there is anything
+      count[k] = parts[p].count;
+    }
+  };
+  for (int from = g.wave; from < n; from += MANY * SA_WAVES) {
+    take(from);
+#pragma unroll
+    for (int k = 0; k < MANY; ++k) {
+      const uint32_t some = __popcll(__ballot(g.lane < (int)count[k] && entry[k].order >= bar));
+      if (g.lane == 0 && from + k * SA_WAVES < n) s.ties[from + k * SA_WAVES] = some;
+    }
   }
   __syncthreads();
   const uint32_t size = g.sum(s.ties[g.tid], start);
   s.ties[g.tid] = start;
   __syncthreads();
   if (size <= SA_LIST) {
-    for (int p = g.wave; p < n; p += SA_WAVES) {
-      const Listed entry = lists[(int64_t)p * PT_LIST + g.lane];
-      const bool take = g.lane < (int)parts[p].count && entry.order >= bar;
-      const u64 in = __ballot(take);
-      const uint32_t to = s.ties[p] + __popcll(in & (((u64)1 << g.lane) - 1));
-      if (take) s.order[to] = entry.order, s.id[to] = entry.id;
+    for (int from = g.wave; from < n; from += MANY * SA_WAVES) {
+      if (n > MANY * SA_WAVES) take(from);
+#pragma unroll
+      for (int k = 0; k < MANY; ++k) {
+        const bool here = from + k * SA_WAVES < n && g.lane < (int)count[k] && entry[k].order >= bar;
+        const u64 in = __ballot(here);
+        if (!in) continue;
+        const uint32_t to = s.ties[from + k * SA_WAVES] + __popcll(in & (((u64)1 << g.lane) - 1));
+        if (here) s.order[to] = entry[k].order, s.id[to] = entry[k].id;
+      }
     }
   }
   __syncthreads();
@@ -673,10 +699,14 @@ __device__ inline uint32_t bin_of(const Weigher& w, float x) { return min((uint3
 // The weight of the places from `at` up to `end` into bins of LDS, by a workgroup.
 template <class T>
 __device__ __forceinline__ void add_to_bins(const RowSource<T>& row, uint32_t at, uint32_t end, int threads, const Weigher& w, double one, u64* bin) {
-  for (uint32_t i = at + threadIdx.x; i < end; i += threads) {
-    const float x = row.at(i);
-    const double y = w(x);
-    if (y > 0) atomicAdd(&bin[bin_of(w, x)], (u64)__builtin_rint(y * one));
+  for (uint32_t i = at + threadIdx.x * 8; i < end; i += threads * 8) {
+    float x[8];
+    row.eight(i, end, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const double y = w(x[k]);
+      if (y > 0) atomicAdd(&bin[bin_of(w, x[k])], (u64)__builtin_rint(y * one));
+    }
   }
 }
 
@@ -689,15 +719,28 @@ __device__ __forceinline__ void part_above(const RowSource<T>& row, const Space&
   double sum = 0, kept = 0;
   uint32_t count = 0;
   Listed* to = space.lists + id * PT_LIST;
-  for (uint32_t at = first; at < end; at += WAVE) {
-    const float x = at + lane < end ? row.at(at + lane) : -__builtin_inff();
-    const double y = w(x);
-    const uint32_t b = bin_of(w, x);
-    if (y > 0 && b < last) sum += y, kept += y < min_p ? 0.0 : y;
-    const u64 in = __ballot(y > 0 && b == last);
-    const uint32_t place = count + __popcll(in & (((u64)1 << lane) - 1));
-    if ((in >> lane & 1) && place < PT_LIST) to[place] = Listed{order_of(x), at + lane};
-    count += __popcll(in);
+  for (uint32_t step = first; step < end; step += PT_STEP) {
+    float x[8];
+    const uint32_t at = step + lane * 8;
+    row.eight(at, end, x);
+    uint32_t in = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const double y = w(x[k]);
+      const uint32_t b = bin_of(w, x[k]);
+      if (y > 0 && b < last) sum += y, kept += y < min_p ? 0.0 : y;
+      in |= (uint32_t)(y > 0 && b == last) << k;
+    }
+    if (!__ballot(in != 0)) continue;
+    const uint32_t mine = __popc(in), upto = sums_upto(mine);
+    uint32_t place = count + upto - mine;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (in >> k & 1) {
+        if (place < PT_LIST) to[place] = Listed{order_of(x[k]), at + k};
+        ++place;
+      }
+    count += of_lane(upto, WAVE - 1);
   }
   sum = sum_of_lanes(sum), kept = sum_of_lanes(kept);
   if (lane == 0) {
