@@ -68,7 +68,7 @@ struct Limits {
   float temperature, top_p, min_p, uniform;
   int64_t top_k;                    // 0: none
   bool single, by_mass, by_weight;  // the first token alone; top_p limits; min_p limits
-  __device__ bool limited() const { return top_k || by_mass || by_weight; }
+  __device__ __forceinline__ bool limited() const { return top_k || by_mass || by_weight; }
 };
 __device__ inline Limits limits_of(const tt_sample_args& a, int64_t r) {
   Limits l;
@@ -153,7 +153,7 @@ struct Part {
   float most;
   uint32_t bar;    // the order down to which all tokens are listed
   uint32_t count;  // of the list; above PT_LIST: it would have had more
-  uint32_t unused;
+  uint32_t high;   // a higher bar, which a few of the tokens listed are not below
 };
 struct Listed {
   uint32_t order, id;
@@ -211,7 +211,7 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, S
   for (int i = 0; i < MINE; ++i) mine = fmaxf(mine, x[i]);
   const uint32_t own = order_of(mine);
   const uint32_t top = max_of_lanes(own);
-  Part part{0, 0, logit_of(top), NOTHING + 1, 0, 0};
+  Part part{0, 0, logit_of(top), NOTHING + 1, 0, NOTHING + 1};
   if (top > NOTHING && !limits.single) {
     const Weigher w(part.most, limits.temperature);
     double sum = 0;
@@ -224,14 +224,18 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, S
     }
     part.sum = sum_of_lanes(sum);
     if (limits.limited()) {
-      // The bar is the 32nd largest of the lanes' maxima, which about 64 ln 2 = 44 tokens are not below; of the largest
-      // 16, 8, 4, 2, 1 where the list would not hold them.
-      uint32_t bar = 0, count = 0, counts = 0, in = 0;  // in: a bit for each token of the lane
-      for (int among = WAVE / 2; among; among /= 2) {
-        bar = 0;
+      // The high bar is one that leaves 100 to 450 tokens of a row, of the logits' distributions there are.  The bar is the 32nd largest of the lanes' maxima, which about 64 ln 2 = 44 tokens are not below; the 16th where the lists of
+      // a row would be too many, and the 16th, 8th, 4th, 2nd or largest where a list would not hold them.
+      auto largest = [&](int among) {
+        uint32_t bar = 0;
         for (uint32_t bit = 1u << 31; bit; bit >>= 1)
           if (__popcll(__ballot(own >= (bar | bit))) >= among) bar |= bit;
-        bar = max(bar, NOTHING + 1);
+        return max(bar, NOTHING + 1);
+      };
+      part.high = largest(min((int)(512 / space.per_row) + 3, WAVE / 2));
+      uint32_t bar = 0, count = 0, counts = 0, in = 0;  // in: a bit for each token of the lane
+      for (int among = space.per_row > 128 ? WAVE / 4 : WAVE / 2; among; among /= 2) {
+        bar = largest(among);
         const float from = logit_of(bar);
         in = 0;
 #pragma unroll
@@ -244,7 +248,7 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, S
         if (count <= PT_LIST) break;
       }
       if (count > PT_LIST) bar = ALL, count = 0;
-      part.bar = bar, part.count = count;
+      part.bar = bar, part.count = count, part.high = max(part.high, bar);
       if (count) {
         const uint32_t upto = sums_upto(counts), all = of_lane(upto, WAVE - 1);
         // where the lane's tokens of each step go, a byte each again
@@ -263,46 +267,31 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, S
 }
 
 // -------------------------------------------------------------- a workgroup
+//
+// The draw from the lists is a chain of sums over a workgroup with little to do in between, which eight wavefronts get through
+// sooner than sixteen; going over a row again takes sixteen.
 
-constexpr int SA_THREADS = 1024;
-constexpr int SA_WAVES = SA_THREADS / WAVE;
-constexpr int SA_TILES = SA_THREADS;  // parts that a row is summed up in
-constexpr int SA_LIST = 8 * SA_THREADS;  // tokens of the lists that are above all bars
+constexpr int DR_THREADS = 512;
+constexpr int RS_THREADS = 1024;
+constexpr int SA_PARTS = 256;   // of a row whose lists are put together
+constexpr int SA_LIST = 4096;   // tokens of the lists that are above all bars
+constexpr int SA_BINS = 256;
+constexpr int SA_COPIES = 2;    // of the bins
+constexpr int SA_TILES = 1024;  // that a row is summed up in
 
 struct SampleShared {
   union {
-    u64 bin[WD_BINS];
+    u64 key[DR_THREADS];
+    u64 depth[WD_BINS];
     double tile[SA_TILES];
     uint32_t ties[SA_TILES];
   };
-  u64 of_wave[SA_WAVES];
+  uint32_t order[SA_LIST], id[SA_LIST];
+  uint32_t start[SA_PARTS];
+  u64 digit[SA_COPIES][SA_BINS + 1];
+  u64 of_wave[2][RS_THREADS / WAVE];
   u64 above, of;
   uint32_t found, last, place;
-  uint32_t order[SA_LIST], id[SA_LIST];
-};
-
-// Where the logits come from: a row in memory, or the tokens listed.
-template <class T>
-struct RowSource {
-  const T* row;
-  uint32_t size;
-  __device__ float at(uint32_t place) const { return (float)row[place]; }
-  // Eight from `place` on; -infinity from `end` on.
-  __device__ void eight(uint32_t place, uint32_t end, float (&x)[8]) const {
-    if (place + 8 <= end) {
-      const auto v = *reinterpret_cast<const typename Eight<T>::type*>(row + place);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = (float)v[k];
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = place + k < end ? (float)row[place + k] : -__builtin_inff();
-    }
-  }
-};
-struct ListSource {
-  const uint32_t* order;
-  uint32_t size;
-  __device__ float at(uint32_t place) const { return logit_of(order[place]); }
 };
 
 __device__ inline u64 bits(double v) { return (u64)__double_as_longlong(v); }
@@ -314,231 +303,337 @@ __device__ inline V value(u64 v) {
   else return (V)v;
 }
 
-// The threads of a workgroup and what they share.
+// The N threads of a workgroup and what they share.
+template <int N>
 struct Group {
+  static constexpr int THREADS = N, WAVES = N / WAVE;
   SampleShared& s;
   int tid, lane, wave;
 
-  // The sum of x over the workgroup, and, in `before`, over the threads before this one.
+  // The sum of x over the workgroup, and over the threads before this one and up to it, the one of a thread being the other's of the next.
   template <class V>
-  __device__ __forceinline__ V sum(V x, V& before) {
-    const V upto = sums_upto(x);
+  __device__ __forceinline__ V sum(V x, V& before, V& upto) {
+    upto = sums_upto(x);
+    before = from_lanes<0x138, 0xf>(upto);  // of the lane before
     __syncthreads();
-    if (lane == WAVE - 1) s.of_wave[wave] = bits(upto);
+    if (lane == WAVE - 1) s.of_wave[0][wave] = bits(upto);
     __syncthreads();
-    V all = 0;
-    before = upto - x;
+    V all = 0, base = 0;
 #pragma unroll
-    for (int k = 0; k < SA_WAVES; ++k) {
-      const V y = value<V>(s.of_wave[k]);
-      if (k < wave) before += y;
-      all += y;
+    for (int k = 0; k < WAVES; ++k) {
+      if (k == wave) base = all;
+      all += value<V>(s.of_wave[0][k]);
     }
+    before += base, upto += base;
     return all;
   }
   template <class V>
   __device__ __forceinline__ V sum(V x) {
-    V before;
-    return sum(x, before);
+    V before, upto;
+    return sum(x, before, upto);
   }
-  __device__ __forceinline__ u64 most(u64 x) {
-    x = max_of_lanes(x);
+  // The largest x and y.
+  __device__ __forceinline__ void most(u64& x, u64& y) {
+    x = max_of_lanes(x), y = max_of_lanes(y);
     __syncthreads();
-    if (lane == 0) s.of_wave[wave] = x;
+    if (lane == 0) s.of_wave[0][wave] = x, s.of_wave[1][wave] = y;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < SA_WAVES; ++k) x = max(x, s.of_wave[k]);
-    return x;
+    for (int k = 0; k < WAVES; ++k) x = max(x, s.of_wave[0][k]), y = max(y, s.of_wave[1][k]);
+  }
+  // The same for four of 32 bits.
+  __device__ __forceinline__ void most(uint32_t& x, uint32_t& y, uint32_t& z, uint32_t& u) {
+    x = max_of_lanes(x), y = max_of_lanes(y), z = max_of_lanes(z), u = max_of_lanes(u);
+    __syncthreads();
+    if (lane == 0) s.of_wave[0][wave] = (u64)x << 32 | y, s.of_wave[1][wave] = (u64)z << 32 | u;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < WAVES; ++k) {
+      const u64 v = s.of_wave[0][k], w = s.of_wave[1][k];
+      x = max(x, (uint32_t)(v >> 32)), y = max(y, (uint32_t)v), z = max(z, (uint32_t)(w >> 32)), u = max(u, (uint32_t)w);
+    }
   }
 
-  // The first thread at which the running sum of x satisfies enough(sum, sum of all), which once true stays so; the last one with a
-  // sum above 0 if none does.  `before`: the sum of the threads before it.
+  // The first thread at which the running sum of x satisfies enough(sum, sum of all), which 0 does not and which once true stays so; the last
+  // one with an x above 0 if none does.  `before`: the sum of the threads before it.
   template <class V, class F>
   __device__ __forceinline__ uint32_t first(V x, F enough, V& before, V& all) {
-    if (tid == 0) s.found = s.last = 0;
-    V at;
-    all = sum(x, at);
-    const uint32_t less = (uint32_t)__popcll(__ballot(!enough(at + x, all)));
-    const u64 some = __ballot(x > 0);
-    if (lane == 0 && less) atomicAdd(&s.found, less);
-    if (lane == 0 && some) atomicMax(&s.last, (uint32_t)(wave * WAVE + 63 - __builtin_clzll(some)));
+    if (tid == 0) s.found = ALL, s.last = 0;
+    V at, upto;
+    all = sum(x, at, upto);
+    if (enough(upto, all) && !enough(at, all)) s.found = tid, s.above = bits(at);
     __syncthreads();
-    const uint32_t found = min(s.found, s.last);
-    if (found == (uint32_t)tid) s.above = bits(at);
-    __syncthreads();
+    uint32_t found = s.found;
+    if (found == ALL) {  // sums that are rounded may stay just below
+      const u64 some = __ballot(x > 0);
+      if (lane == 0 && some) atomicMax(&s.last, (uint32_t)(wave * WAVE + 63 - __builtin_clzll(some)));
+      __syncthreads();
+      found = s.last;
+      if (found == (uint32_t)tid) s.above = bits(at);
+      __syncthreads();
+    }
     before = value<V>(s.above);
     return found;
   }
 };
 
-// The first place from `from` up to `end` at which `before` and the running sum of f(logit, place) are above `goal`, the last one with a
-// weight if none is, and its f; by the workgroup, some places a thread.
-template <class V, class Source, class F>
-__device__ __forceinline__ uint32_t locate(const Source& source, Group& g, uint32_t from, uint32_t end, V before, V goal, F f, V& mine) {
-  const uint32_t per = (end - from + SA_THREADS - 1) / SA_THREADS, own = from + g.tid * per, stop = min(own + per, end);
-  V sum = 0;
+// Where the logits come from: a row in memory, or the tokens listed with their weights.  each: f(order, weight, place), the weight to be
+// called for, for the tokens of the thread in any order; in_row: for those of its share of the places from `from` up to `end`,
+// in order, as long as f returns true.
+template <class T>
+struct RowSource {
+  // logits of 16 bits leave the lowest bits of their order alike
+  static constexpr bool LISTED = false;
+  static constexpr int LOW = std::is_same<T, float>::value ? 0 : std::is_same<T, _Float16>::value ? 13 : 16;
+  const T* row;
+  uint32_t size;
+  // Eight from `place` on; -infinity from `end` on.
+  __device__ void eight(uint32_t place, uint32_t end, float (&x)[8]) const {
+    if (place + 8 <= end) {
+      const auto v = *reinterpret_cast<const typename Eight<T>::type*>(row + place);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = (float)v[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = place + k < end ? (float)row[place + k] : -__builtin_inff();
+    }
+  }
+  template <int N, class F>
+  __device__ __forceinline__ void each(const Weigher& w, F f) const {
 #pragma unroll 1
-  for (uint32_t i = own; i < stop; ++i) sum += f(source.at(i), i);
-  V at, all;
-  const uint32_t thread = g.first(sum, [&](V upto, V) { return before + upto > goal; }, at, all);
+    for (uint32_t i = threadIdx.x * 8; i < size; i += N * 8) {
+      float x[8];
+      eight(i, size, x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i + k < size) f(order_of(x[k]), [&] { return w(x[k]); }, i + k);
+    }
+  }
+  template <int N, class F>
+  __device__ __forceinline__ void in_row(const Weigher& w, uint32_t from, uint32_t end, F f) const {
+    const uint32_t per = (end - from + N - 1) / N, own = from + threadIdx.x * per, stop = min(own + per, end);
+    bool more = true;
+#pragma unroll 1
+    for (uint32_t at = own; at < stop && more; at += 8) {
+      float x[8];
+      eight(at, stop, x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (at + k < stop && more) more = f(order_of(x[k]), [&] { return w(x[k]); }, at + k);
+    }
+  }
+};
+// In registers, the same number of places to each of N threads: reading them from LDS for every question, one after the other with a
+// wavefront to each SIMD, takes three times as long.
+template <class T, int N>
+struct ListSource {
+  static constexpr int LOW = RowSource<T>::LOW, MINE = SA_LIST / N;
+  static constexpr bool LISTED = true;
+  uint32_t size, per, own;
+  uint32_t order[MINE];
+  double weight[MINE];
+  __device__ __forceinline__ ListSource(const SampleShared& s, uint32_t size_, const Weigher& w) : size(size_) {
+    per = (size + N - 1) / N, own = threadIdx.x * per;
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) order[k] = k < (int)per && own + k < size ? s.order[own + k] : 0;
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) weight[k] = k < (int)per && order[k] ? w(logit_of(order[k])) : 0.0;
+  }
+  template <int, class F>
+  __device__ __forceinline__ void each(const Weigher&, F f) const {
+#pragma unroll
+    for (int k = 0; k < MINE; ++k)
+      if (k < (int)per) f(order[k], [&] { return weight[k]; }, own + k);  // an order of 0 past the last
+  }
+  template <int, class F>
+  __device__ __forceinline__ void in_row(const Weigher&, uint32_t, uint32_t, F f) const {
+    bool more = true;
+#pragma unroll
+    for (int k = 0; k < MINE; ++k)
+      if (k < (int)per && more) more = f(order[k], [&] { return weight[k]; }, own + k);
+  }
+};
+
+// The place from `from` up to `end` at which the running sum of f(order, weight, place), `before` at first, gets above goal(sum of these), the last one
+// with a sum if it does not, and its f; by the workgroup.
+template <class V, class Source, class Threads, class F, class G>
+__device__ __forceinline__ uint32_t locate(const Source& source, const Weigher& w, Threads& g, uint32_t from, uint32_t end, V before, F f, G goal, V& mine,
+                                           V& all) {
+  constexpr int N = Threads::THREADS;
+  V sum = 0, at;
+  source.template in_row<N>(w, from, end, [&](uint32_t o, auto weight, uint32_t place) {
+    sum += f(o, weight, place);
+    return true;
+  });
+  const uint32_t thread = g.first(sum, [&](V upto, V total) { return before + upto > goal(total); }, at, all);
   if (thread == (uint32_t)g.tid) {
     V run = before + at, of = 0;
-    uint32_t place = own;
-#pragma unroll 1
-    for (uint32_t i = own; i < stop; ++i) {
-      const V x = f(source.at(i), i);
+    uint32_t found = from;
+    source.template in_row<N>(w, from, end, [&](uint32_t o, auto weight, uint32_t place) {
+      const V x = f(o, weight, place);
       run += x;
-      if (x > 0) {
-        place = i, of = x;
-        if (run > goal) break;
-      }
-    }
-    g.s.place = place, g.s.of = bits(of);
+      if (x > 0) found = place, of = x;
+      return !(x > 0 && run > goal(all));
+    });
+    g.s.place = found, g.s.of = bits(of);
   }
   __syncthreads();
   mine = value<V>(g.s.of);
   return g.s.place;
 }
 
-// Sums of weights in 64 bits of fixed point, which are the same in any order: this is 1.
+// Sums of weights in 64 bits of fixed point, which are the same in any order.  A value from 0 to 2^62, rounded at its lowest bits.
+__device__ inline u64 fixed(double x) {
+  const double high = __builtin_floor(x * 0x1p-32), low = fma(high, -0x1p32, x);
+  return (u64)(uint32_t)high << 32 | (uint32_t)low;
+}
+// This is 1.
 __device__ inline double one_of(uint32_t tokens) { return __builtin_ldexp(1.0, 62 - (32 - __builtin_clz(tokens))); }
 
 // What is kept of a source of logits: orders above `least`, and those at it up to the place `until`, of a weight of min_p or more.
 struct Kept {
   uint32_t least, until;
   double min_p;
-  __device__ double of(uint32_t order, uint32_t place, double weight) const {
-    return order < least || (order == least && place > until) || weight < min_p ? 0.0 : weight;
+  template <class W>
+  __device__ __forceinline__ double of(uint32_t order, W weight, uint32_t place) const {
+    if (order < least || (order == least && place > until)) return 0.0;
+    const double y = weight();
+    return y < min_p ? 0.0 : y;
   }
 };
 
 // A source of logits that a workgroup passes over for every question.
-template <class Source>
+template <class Source, class Threads>
 struct Sampler {
+  static constexpr int N = Threads::THREADS;
   const Source& source;
-  Group& g;
+  const Weigher& w;
+  Threads& g;
   SampleShared& s;
+  uint32_t most;  // the largest order
 
+  // What the tokens weigh whose order `take` takes.
   template <class F>
-  __device__ __forceinline__ double sum(F f) {
+  __device__ __forceinline__ double sum(F take) {
     double sum = 0;
-#pragma unroll 1
-    for (uint32_t i = g.tid; i < source.size; i += SA_THREADS) sum += f(source.at(i));
+    source.template each<N>(w, [&](uint32_t o, auto weight, uint32_t) {
+      if (o && take(o)) sum += weight();
+    });
     return g.sum(sum);
   }
 
   // The order at which, from the largest down to `least`, as many tokens (or, by mass, as much weight) as `target` are reached,
-  // digit by digit of 11, 11 and 10 bits; `above` receives how many (how much) there are above it.
-  __device__ __forceinline__ uint32_t reach(bool mass, const Weigher& w, uint32_t least, double target, double& above) {
+  // by digits of 8 bits, each from the first bit on that tells the candidates apart.  `above` receives how many (how much) there are above it,
+  // `there` how many (how much) at it.
+  __device__ __forceinline__ uint32_t reach(bool mass, uint32_t least, double target, double& above, double& there) {
     const double one = mass ? one_of(source.size) : 1.0, unit = 1 / one;
-    uint32_t prefix = 0;
+    u64 largest = most, smallest = least;  // of the orders that it may be
     above = 0;
 #pragma unroll 1
-    for (int shift = 21;; shift = shift == 21 ? 10 : 0) {
-      const int width = shift ? 11 : 10;
+    while (true) {
+      const uint32_t apart = (uint32_t)(largest ^ smallest);
+      const int top = max(apart ? 32 - __builtin_clz(apart) : 0, Source::LOW), width = min(8, top - Source::LOW), shift = top - width;
+      const uint32_t prefix = top < 32 ? (uint32_t)largest >> top : 0;
       __syncthreads();
-      s.bin[g.tid] = s.bin[g.tid + SA_THREADS] = 0;
+      for (int i = g.tid; i < SA_COPIES * (SA_BINS + 1); i += N) s.digit[0][i] = 0;
       __syncthreads();
-#pragma unroll 1
-      for (uint32_t i = g.tid; i < source.size; i += SA_THREADS) {
-        const float x = source.at(i);
-        const uint32_t o = order_of(x);
-        if (o < least || (shift < 21 && o >> (shift + width) != prefix)) continue;
-        atomicAdd(&s.bin[o >> shift & ((1u << width) - 1)], mass ? (u64)__builtin_rint(w(x) * one) : (u64)1);
+      source.template each<N>(w, [&](uint32_t o, auto weight, uint32_t) {
+        if (o >= least && (top == 32 || o >> top == prefix))
+          atomicAdd(&s.digit[g.lane % SA_COPIES][o >> shift & ((1u << width) - 1)], mass ? fixed(weight() * one) : (u64)1);
+      });
+      __syncthreads();
+      u64 x = 0;  // from the largest down
+      if (g.tid < SA_BINS) {
+#pragma unroll
+        for (int k = 0; k < SA_COPIES; ++k) x += s.digit[k][SA_BINS - 1 - g.tid];
       }
-      __syncthreads();
-      const int b = WD_BINS - 1 - 2 * g.tid;  // from the largest down, two a thread
-      const u64 first = s.bin[b], second = s.bin[b - 1];
       u64 before, all;
-      const uint32_t thread = g.first(first + second, [&](u64 upto, u64) { return above + (double)upto * unit >= target; }, before, all);
-      // of the thread's two the first if it is enough by itself, or all there is
-      const uint32_t bin = WD_BINS - 1 - 2 * thread;
-      const u64 one_bin = s.bin[bin];
-      const bool take = one_bin && (above + (double)(before + one_bin) * unit >= target || !s.bin[bin - 1]);
-      above += (double)(before + (take ? 0 : one_bin)) * unit;
-      prefix = prefix << width | (take ? bin : bin - 1);
-      if (!shift) return prefix;
+      const uint32_t digit = SA_BINS - 1 - g.first(x, [&](u64 upto, u64) { return upto && above + (double)upto * unit >= target; }, before, all);
+      above += (double)before * unit;
+      there = 0;
+#pragma unroll
+      for (int k = 0; k < SA_COPIES; ++k) there += (double)s.digit[k][digit] * unit;
+      const uint32_t found = prefix << width | digit;
+      // the largest and the smallest that are left; the rest of the digits that they share is skipped
+      largest = 0;
+      u64 inverse = 0;
+      source.template each<N>(w, [&](uint32_t o, auto, uint32_t) {
+        if (o >= least && o >> shift == found) largest = max(largest, (u64)o), inverse = max(inverse, (u64)(uint32_t)~o);
+      });
+      g.most(largest, inverse);
+      smallest = (uint32_t)~inverse;
+      if (!inverse) return most;  // nothing weighs anything
+      if (largest == smallest || !width) return (uint32_t)largest;
     }
   }
 
-  // The first place at which the running sum of f(logit, place) is above goal(sum of all); mine: its f.
+  // The first place at which the running sum of f(order, weight, place) is above goal(sum of all); mine: its f.
   template <class V, class F, class G>
   __device__ __forceinline__ uint32_t find(V* tiles, F f, G goal, V& mine, V& all) {
-    const uint32_t size = (source.size + SA_TILES - 1) / SA_TILES, per = (size + WAVE - 1) / WAVE * WAVE;  // of a tile
-    uint32_t from = 0, end = source.size;
-    V before = 0, least;
-    if (source.size > SA_LIST) {
+    if constexpr (Source::LISTED) {
+      return locate(source, w, g, 0, source.size, (V)0, f, goal, mine, all);
+    } else {
+      static_assert(N == SA_TILES, "a tile for each thread");
+      const uint32_t size = (source.size + SA_TILES - 1) / SA_TILES, per = (size + WAVE - 1) / WAVE * WAVE;  // of a tile
       __syncthreads();
 #pragma unroll 1
-      for (uint32_t t = g.wave; t < SA_TILES; t += SA_WAVES) {
+      for (uint32_t t = g.wave; t < SA_TILES; t += N / WAVE) {
         V sum = 0;
 #pragma unroll 1
-        for (uint32_t i = t * per + g.lane; i < min((t + 1) * per, source.size); i += WAVE) sum += f(source.at(i), i);
+        for (uint32_t i = t * per + g.lane; i < min((t + 1) * per, source.size); i += WAVE) {
+          const float x = (float)source.row[i];
+          sum += f(order_of(x), [&] { return w(x); }, i);
+        }
         sum = sum_of_lanes(sum);
         if (g.lane == 0) tiles[t] = sum;
       }
       __syncthreads();
       const V x = tiles[g.tid];
+      V before, some;
       const uint32_t t = g.first(x, [&](V upto, V total) { return upto > goal(total); }, before, all);
-      from = t * per, end = min(from + per, source.size);
-      least = goal(all);
-    } else {
-      const uint32_t each = (source.size + SA_THREADS - 1) / SA_THREADS;
-      V sum = 0;
-#pragma unroll 1
-      for (uint32_t i = g.tid * each; i < min((g.tid + 1) * each, source.size); ++i) sum += f(source.at(i), i);
-      all = g.sum(sum);
-      least = goal(all);
+      const V least = goal(all);
+      return locate(source, w, g, t * per, min((t + 1) * per, source.size), before, f, [&](V) { return least; }, mine, some);
     }
-    return locate(source, g, from, end, before, least, f, mine);
   }
 
   // The last place kept of those of order `least`, if the first `ties` of them are.
   __device__ __forceinline__ uint32_t until(uint32_t least, double ties) {
     const uint32_t goal = (uint32_t)__builtin_fmin(ties, 4e9) - 1;
     uint32_t one, all;
-    const uint32_t place = find(s.ties, [&](float x, uint32_t) { return (uint32_t)(order_of(x) == least); }, [&](uint32_t) { return goal; }, one, all);
+    const uint32_t place = find(s.ties, [&](uint32_t o, auto, uint32_t) { return (uint32_t)(o == least); }, [&](uint32_t) { return goal; }, one, all);
     return goal < all ? place : ALL;
   }
 
-  // Of the orders from `least` on, the fewest that weigh `target`: the last one of them; `needed` receives how many of it.
-  __device__ __forceinline__ uint32_t heaviest(const Weigher& w, uint32_t least, double target, double& needed) {
-    double above;
-    const uint32_t o = reach(true, w, least, target, above);
-    above = sum([&](float x) { return order_of(x) > o ? w(x) : 0.0; });
-    needed = __builtin_fmax(__builtin_ceil((target - above) / w(logit_of(o))), 1.0);
-    return o;
-  }
-
-  // The token drawn, as its place, and what it and all that are kept weigh.  `whole`: what the tokens that top_k leaves weigh if it
-  // does not limit.
-  __device__ __forceinline__ uint32_t draw(const Limits& l, const Weigher& w, double whole, double& mine, double& all) {
+  // The token drawn, as its place, and what it and all that are kept weigh.  `by_mass`, if it is not negative: what the nucleus has
+  // to weigh, or, of the tokens that top_k leaves, what share of them.
+  __device__ __forceinline__ Kept kept(const Limits& l, double by_mass) {
     uint32_t least = NOTHING + 1;
     double ties = -1;  // of those at `least` so many are kept; all of them if negative
-    double target = (double)l.top_k;
 #pragma unroll 1
-    for (int by_mass = 0; by_mass < 2; ++by_mass) {  // the same code for both limits
-      if (!(by_mass ? l.by_mass : l.top_k != 0)) continue;
-      if (by_mass) {
-        if (l.top_k)
-          whole = sum([&](float x) { return order_of(x) > least || (ties < 0 && order_of(x) == least) ? w(x) : 0.0; }) +
-                  (ties > 0 ? ties * w(logit_of(least)) : 0.0);
-        target = (double)l.top_p * whole;
-      }
-      double above;
-      const uint32_t o = reach(by_mass, w, by_mass ? least : 0, target, above);
-      if (!by_mass) {
-        if (o > NOTHING) least = o, ties = target - above;
+    for (int mass = 0; mass < 2; ++mass) {  // the same code for both limits
+      if (!(mass ? by_mass >= 0 : l.top_k != 0)) continue;
+      double target = mass ? by_mass : (double)l.top_k, above, there;
+      if (mass && l.top_k)
+        target *= sum([&](uint32_t o) { return o > least || (ties < 0 && o == least); }) + (ties > 0 ? ties * w(logit_of(least)) : 0.0);
+      const uint32_t last = reach(mass, mass ? least : NOTHING, target, above, there);
+      if (!mass) {
+        if (last > NOTHING) least = last, ties = target - above < there ? target - above : -1;
         continue;
       }
-      above = sum([&](float x) { return order_of(x) > o ? w(x) : 0.0; });
-      const double needed = __builtin_fmax(__builtin_ceil((target - above) / w(logit_of(o))), 1.0);
-      ties = o == least && ties >= 0 ? __builtin_fmin(ties, needed) : needed;
-      least = o;
+      above = sum([&](uint32_t o) { return o > last; });
+      const double one = w(logit_of(last)), needed = __builtin_fmax(__builtin_ceil((target - above) / one), 1.0);
+      // all of them, where their weight says for certain how many they are
+      const bool every = one * one_of(source.size) > 0x1p28 && needed >= __builtin_rint(there / one);
+      if (last == least && ties >= 0) ties = __builtin_fmin(ties, needed);
+      else ties = every ? -1 : needed;
+      least = last;
     }
-    const Kept kept{least, ties >= 0 ? until(least, ties) : ALL, l.by_weight ? (double)l.min_p : 0.0};
-    return find(s.tile, [&](float x, uint32_t place) { return kept.of(order_of(x), place, w(x)); },
-                [&](double total) { return (double)l.uniform * total; }, mine, all);
+    return Kept{least, ties >= 0 ? until(least, ties) : ALL, l.by_weight ? (double)l.min_p : 0.0};
+  }
+  __device__ __forceinline__ uint32_t draw(const Limits& l, double by_mass, double& mine, double& all) {
+    const Kept k = kept(l, by_mass);
+    return find(s.tile, [&](uint32_t o, auto weight, uint32_t place) { return k.of(o, weight, place); }, [&](double total) { return (double)l.uniform * total; },
+                mine, all);
   }
 };
 
@@ -548,45 +643,52 @@ __device__ inline void put_token(const tt_sample_args& a, int64_t r, uint32_t to
   if (a.logprobs) a.logprobs[r] = token == ALL ? -__builtin_inff() : (float)log(mine / all);
 }
 
-// The tokens that the parts' lists hold from the order `bar` on, in the order of ids, to s.order and s.id; how many there are, which may
-// be more than there is room for: then none are taken.  `start`: where those of part tid begin.
-__device__ __forceinline__ uint32_t gather(Group& g, const Part* parts, const Listed* lists, int n, uint32_t bar, uint32_t& start) {
+// The tokens that the parts' lists hold from the order `bar` on, in the order of ids, to s.order and s.id; how many there are, which may be
+// more than there is room for: then none are taken.  s.start[p]: where those of part p begin.
+template <class Threads>
+__device__ __forceinline__ uint32_t gather(Threads& g, const Part* parts, const Listed* lists, int n, uint32_t bar) {
+  constexpr int WAVES = Threads::WAVES, MANY = 8;  // lists of a wavefront that are on their way together
   SampleShared& s = g.s;
   __syncthreads();
-  s.ties[g.tid] = 0;
+  if (g.tid < SA_PARTS) s.start[g.tid] = 0;
   __syncthreads();
-  constexpr int MANY = 8;  // lists of a wavefront that are on their way together
   Listed entry[MANY];
   uint32_t count[MANY];
   auto take = [&](int from) {
 #pragma unroll
     for (int k = 0; k < MANY; ++k) {
-      const int p = min(from + k * SA_WAVES, n - 1);
+      const int p = from + k * WAVES;
+      if (from + k * WAVES >= n) continue;
       entry[k] = lists[(int64_t)p * PT_LIST + g.lane];  // past the count there is anything
       count[k] = parts[p].count;
     }
   };
-  for (int from = g.wave; from < n; from += MANY * SA_WAVES) {
+  for (int from = g.wave; from < n; from += MANY * WAVES) {
     take(from);
 #pragma unroll
     for (int k = 0; k < MANY; ++k) {
+      if (from + k * WAVES >= n) continue;
       const uint32_t some = __popcll(__ballot(g.lane < (int)count[k] && entry[k].order >= bar));
-      if (g.lane == 0 && from + k * SA_WAVES < n) s.ties[from + k * SA_WAVES] = some;
+      if (g.lane == 0) s.start[from + k * WAVES] = some;
     }
   }
   __syncthreads();
-  const uint32_t size = g.sum(s.ties[g.tid], start);
-  s.ties[g.tid] = start;
+  uint32_t start, upto;
+  const uint32_t size = g.sum(g.tid < SA_PARTS ? s.start[g.tid] : 0, start, upto);
+  if (g.tid < SA_PARTS) s.start[g.tid] = start;
   __syncthreads();
   if (size <= SA_LIST) {
-    for (int from = g.wave; from < n; from += MANY * SA_WAVES) {
-      if (n > MANY * SA_WAVES) take(from);
+    for (int from = g.wave; from < n; from += MANY * WAVES) {
+      if (n > MANY * WAVES) take(from);
+      uint32_t start[MANY];
+#pragma unroll
+      for (int k = 0; k < MANY; ++k) start[k] = s.start[min(from + k * WAVES, SA_PARTS - 1)];
 #pragma unroll
       for (int k = 0; k < MANY; ++k) {
-        const bool here = from + k * SA_WAVES < n && g.lane < (int)count[k] && entry[k].order >= bar;
+        if (from + k * WAVES >= n) continue;
+        const bool here = g.lane < (int)count[k] && entry[k].order >= bar;
         const u64 in = __ballot(here);
-        if (!in) continue;
-        const uint32_t to = s.ties[from + k * SA_WAVES] + __popcll(in & (((u64)1 << g.lane) - 1));
+        const uint32_t to = start[k] + __popcll(in & (((u64)1 << g.lane) - 1));
         if (here) s.order[to] = entry[k].order, s.id[to] = entry[k].id;
       }
     }
@@ -595,97 +697,139 @@ __device__ __forceinline__ uint32_t gather(Group& g, const Part* parts, const Li
   return size;
 }
 
-// The largest logit of a row's parts.
+// The largest logit of a row's parts, by each wavefront.
 __device__ inline float most_of(const Part* parts, int64_t n) {
   uint32_t best = 0;
   for (int64_t p = threadIdx.x % WAVE; p < n; p += WAVE) best = max(best, order_of(parts[p].most));
   return logit_of(max_of_lanes(best));
 }
 
+// The keys of the workgroup's threads, the largest first; `size` of them are not 0.  Bitonic: exchanges between threads whose numbers differ in one bit.
+template <class Threads>
+__device__ __forceinline__ u64 sorted(Threads& g, u64 key, uint32_t size) {
+  SampleShared& s = g.s;
+#pragma unroll 1
+  for (int run = 2; run < 2 * Threads::THREADS; run *= 2) {
+    if (run / 2 >= (int)size) break;  // what is not 0 is sorted
+#pragma unroll 1
+    for (int apart = run / 2; apart; apart /= 2) {
+      u64 other;
+      if (apart < WAVE) {
+        other = __shfl_xor(key, apart);
+      } else {
+        __syncthreads();
+        s.key[g.tid] = key;
+        __syncthreads();
+        other = s.key[g.tid ^ apart];
+      }
+      // the first of the two takes the larger, in every second run the smaller
+      const bool larger = !(g.tid & apart) == !(g.tid & run);
+      key = larger == (other > key) ? other : key;
+    }
+  }
+  return key;
+}
+
 // A row by a workgroup, from its parts.  Without limits the part that the random number falls into is read again; with limits
-// the tokens listed decide if the last one kept is above all bars; else the row is left to be gone over again.
+// the tokens above all high bars, if they are few, are sorted, which answers everything that is asked of them; if the last one kept is not
+// among them the row is left to be gone over again.
 template <class T>
-__global__ __launch_bounds__(SA_THREADS) void k_sample(tt_sample_args a, Space space) {
+__global__ __launch_bounds__(DR_THREADS) void k_sample(tt_sample_args a, Space space) {
   __shared__ SampleShared s;
   const int64_t r = blockIdx.x;
   const int tid = threadIdx.x;
   const Part* parts = space.parts + r * space.per_row;
-  Limits l = limits_of(a, r);
-  const int n = (int)space.per_row;
+  const Limits l = limits_of(a, r);
+  const int n = (int)space.per_row, per = (n + DR_THREADS - 1) / DR_THREADS;  // parts of a thread, one behind the other
   const RowSource<T> row{static_cast<const T*>(a.logits) + r * a.logits_stride, (uint32_t)a.vocab};
-  Group g{s, tid, tid % WAVE, tid / WAVE};
+  Group<DR_THREADS> g{s, tid, tid % WAVE, tid / WAVE};
 
-  u64 best = 0, bar = NOTHING + 1;  // the largest logit and its first part; the highest bar
-  for (int p = tid; p < n; p += SA_THREADS) {
-    best = max(best, (u64)order_of(parts[p].most) << 32 | ~(uint32_t)p);
-    bar = max(bar, (u64)parts[p].bar);
-  }
-  best = g.most(best);
-  const float most = logit_of((uint32_t)(best >> 32));
+  uint32_t top = 0, bar = NOTHING + 1, high = NOTHING + 1, none = 0;  // the largest order; the highest of the bars and of the high ones
+  for (int p = tid * per; p < min((tid + 1) * per, n); ++p)
+    top = max(top, order_of(parts[p].most)), bar = max(bar, parts[p].bar), high = max(high, parts[p].high);
+  g.most(top, bar, high, none);
   if (tid == 0) space.state[r] = DONE;
-  if (best >> 32 <= NOTHING) {
+  if (top <= NOTHING) {
     if (tid == 0) put_token(a, r, ALL, 0, 1);
     return;
   }
-  double mine = 1, all = 1, before;
+  double mine = 1, all = 1, whole = 0, some;
   uint32_t token;
-  const Weigher w(most, l.temperature);
-  auto weight_of = [&](int p) { return p < n && parts[p].sum > 0 ? parts[p].sum * w(parts[p].most) : 0.0; };
-  if (l.single || (!l.limited() && n <= SA_TILES)) {
-    uint32_t p = ~(uint32_t)best;
-    double goal = 0;
-    before = 0;
-    if (!l.single) {
-      p = g.first(weight_of(tid), [&](double upto, double total) { return upto > (double)l.uniform * total; }, before, all);
+  const Weigher w(logit_of(top), l.temperature);
+  auto weight_of = [&](int p) { return parts[p].sum > 0 ? parts[p].sum * w(parts[p].most) : 0.0; };
+  if (!l.single)
+    for (int p = tid * per; p < min((tid + 1) * per, n); ++p) whole += weight_of(p);
+  if (l.single || !l.limited()) {
+    uint32_t p = 0;
+    double goal = 0, before = 0;
+    if (l.single) {  // the first part that has it
+      uint32_t first = 0;
+      for (int q = tid; q < n; q += DR_THREADS)
+        if (order_of(parts[q].most) == top) first = max(first, ~(uint32_t)q);
+      uint32_t none_too = 0, nor_this = 0;
+      g.most(first, none, none_too, nor_this);
+      p = ~first;
+    } else {
+      const uint32_t thread = g.first(whole, [&](double upto, double total) { return upto > (double)l.uniform * total; }, before, all);
       goal = (double)l.uniform * all;
-    }
-    token = locate(row, g, p * space.size, min((p + 1) * space.size, row.size), before, goal,
-                   [&](float x, uint32_t) { return l.single ? (x == most ? 1.0 : 0.0) : w(x); }, mine);
-    if (tid == 0) put_token(a, r, token, mine, all);
-    return;
-  }
-  double whole = 0;
-  for (int p = tid; p < n; p += SA_THREADS) whole += weight_of(p);
-  whole = g.sum(whole);
-  bar = g.most(bar);
-  bool listed = l.limited() && n <= SA_TILES && bar != ALL;
-  uint32_t size = 0, start;
-  if (listed) {
-    size = gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, (uint32_t)bar, start);
-    listed = size <= SA_LIST;
-  }
-  const ListSource top{s.order, size};
-  Sampler<ListSource> list{top, g, s};
-  if (listed && bar > NOTHING + 1) {
-    // tokens below the bar are not listed: none of them may be kept, or be needed for a sum
-    const bool light = l.by_weight && w(logit_of((uint32_t)bar)) < (double)l.min_p;
-    if (l.top_k && size < l.top_k) {
-      listed = light && !l.by_mass;
-    } else if (l.by_mass && !l.top_k) {
-      if (!(list.sum([&](float x) { return w(x); }) >= (double)l.top_p * whole * (1 + 1e-12))) {
-        listed = light;  // the nucleus goes below the bar, what min_p leaves does not
-        l.by_mass = false;
+      p = thread * per;
+      for (uint32_t end = min(p + per, (uint32_t)n); p + 1 < end; ++p) {
+        const double y = weight_of(p);
+        if (before + y > goal) break;
+        before += y;
       }
-    } else if (!l.top_k) {
-      listed = light;
     }
-  }
-  if (listed) {
-    token = s.id[list.draw(l, w, whole, mine, all)];
+    token = locate(row, w, g, p * space.size, min((p + 1) * space.size, row.size), before,
+                   [&](uint32_t o, auto weight, uint32_t) { return l.single ? (o == top ? 1.0 : 0.0) : weight(); }, [&](double) { return goal; }, mine, some);
     if (tid == 0) put_token(a, r, token, mine, all);
     return;
+  }
+  whole = g.sum(whole);
+  uint32_t size = ALL;
+  if (n <= SA_PARTS && high != ALL) size = gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, high);
+  if (size <= DR_THREADS) {
+    const bool here = (uint32_t)tid < size;
+    const uint32_t own = here ? s.order[tid] : 0;
+    const double weight = here ? w(logit_of(own)) : 0.0;
+    const u64 key = here ? (u64)own << 32 | ~(uint32_t)tid : 0;  // the larger the earlier
+    const u64 nth = sorted(g, key, size);
+    double before, upto;
+    g.sum(nth ? w(logit_of((uint32_t)(nth >> 32))) : 0.0, before, upto);
+    // tokens below the bar are not there: none of them may be kept, or be needed for a sum
+    const bool light = high == NOTHING + 1 || (l.by_weight && w(logit_of(high)) < (double)l.min_p), limit = l.top_k && l.top_k <= size;
+    const bool sums = high == NOTHING + 1 || limit || !l.top_k;  // what the nucleus is a share of is known
+    const uint32_t most = limit ? (uint32_t)l.top_k : size;
+    if ((uint32_t)tid == most - 1) s.above = bits(upto);
+    __syncthreads();
+    const double of = value<double>(s.above);  // what the first `most` weigh
+    const double target = (double)l.top_p * (limit || high == NOTHING + 1 ? of : whole);
+    const bool by_mass = l.by_mass && sums && of >= target * (limit ? 1 : 1 + 1e-12);
+    // the last one kept
+    if (tid == 0) s.found = most - 1;
+    __syncthreads();
+    if (by_mass && upto >= target && (tid == 0 || before < target)) atomicMin(&s.found, (uint32_t)tid);
+    __syncthreads();
+    if ((uint32_t)tid == s.found) s.of = nth;
+    __syncthreads();
+    const bool decided = l.by_mass ? by_mass || (sums && light) : limit || light;
+    if (decided) {
+      const double mine = key >= s.of && here && weight >= (l.by_weight ? (double)l.min_p : 0.0) ? weight : 0.0;
+      const uint32_t thread = g.first(mine, [&](double sum, double total) { return sum > (double)l.uniform * total; }, before, all);
+      if ((uint32_t)tid == thread) put_token(a, r, s.id[tid], mine, all);
+      return;
+    }
   }
   __syncthreads();
   if (tid == 0) {
     space.whole[r] = whole;
     s.found = WD_SLOTS;
-    if (space.slots && !l.top_k && n <= SA_TILES) s.found = atomicAdd(space.slots_taken, 1u);
+    if (space.slots && !l.top_k && n <= SA_PARTS) s.found = atomicAdd(space.slots_taken, 1u);
     space.state[r] = s.found < WD_SLOTS ? s.found : LEFT;
     if (s.found < WD_SLOTS) space.slots[s.found].row = r;
   }
   __syncthreads();
   if (s.found < WD_SLOTS)
-    for (int i = tid; i < WD_BINS; i += SA_THREADS) space.slots[s.found].mass[i] = 0;
+    for (int i = tid; i < WD_BINS; i += DR_THREADS) space.slots[s.found].mass[i] = 0;
 }
 
 // ------------------------------------------- rows that have to be gone over again
@@ -705,7 +849,7 @@ __device__ __forceinline__ void add_to_bins(const RowSource<T>& row, uint32_t at
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const double y = w(x[k]);
-      if (y > 0) atomicAdd(&bin[bin_of(w, x[k])], (u64)__builtin_rint(y * one));
+      if (y > 0) atomicAdd(&bin[bin_of(w, x[k])], fixed(y * one));
     }
   }
 }
@@ -820,7 +964,7 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_above(tt_sample_args a, S
 // The tokens of rows that are left, or whose parts know what is above their last bin: the bin's tokens are put in order, the part
 // is found, and the token in it.
 template <class T>
-__global__ __launch_bounds__(SA_THREADS) void k_sample_rest(tt_sample_args a, Space space) {
+__global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Space space) {
   __shared__ SampleShared s;
   const int64_t r = blockIdx.x;
   const uint32_t state = space.state[r];
@@ -828,69 +972,104 @@ __global__ __launch_bounds__(SA_THREADS) void k_sample_rest(tt_sample_args a, Sp
   const int tid = threadIdx.x, n = (int)space.per_row;
   const Limits l = limits_of(a, r);
   const RowSource<T> row{static_cast<const T*>(a.logits) + r * a.logits_stride, (uint32_t)a.vocab};
-  Group g{s, tid, tid % WAVE, tid / WAVE};
+  Group<RS_THREADS> g{s, tid, tid % WAVE, tid / WAVE};
   const Part* parts = space.parts + r * space.per_row;
-  const Weigher w(most_of(parts, n), l.temperature);
-  const double whole = space.whole[r], target = (double)l.top_p * whole, one = one_of((uint32_t)a.vocab);
-  const double min_p = l.by_weight ? (double)l.min_p : 0.0;
+  const float most = most_of(parts, n);
+  const Weigher w(most, l.temperature);
+  const double whole = space.whole[r], target = (double)l.top_p * whole, min_p = l.by_weight ? (double)l.min_p : 0.0;
   double mine = 0, all = 0;
-  uint32_t token, last = WD_BINS, start = 0, size = 0;
-  bool again = l.top_k || n > SA_TILES;
+  uint32_t token, last = WD_BINS, size = 0;
+  if (state == LEFT && n <= SA_PARTS) {
+    uint32_t bar = NOTHING + 1, none[3] = {0, 0, 0};
+    for (int p = tid; p < n; p += RS_THREADS) bar = max(bar, parts[p].bar);
+    g.most(bar, none[0], none[1], none[2]);
+    size = bar == ALL ? ALL : gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, bar);
+    if (size <= SA_LIST) {
+      const ListSource<T, RS_THREADS> listed(s, size, w);
+      Sampler<ListSource<T, RS_THREADS>, Group<RS_THREADS>> list{listed, w, g, s, order_of(most)};
+      double by_mass = !l.by_mass ? -1 : l.top_k ? (double)l.top_p : target;
+      bool decided = true;
+      if (bar > NOTHING + 1) {
+        // tokens below the bar are not there: none of them may be kept, or be needed for a sum
+        const bool light = l.by_weight && w(logit_of(bar)) < min_p;
+        if (l.top_k && size < l.top_k) {
+          decided = light && !l.by_mass;
+        } else if (l.by_mass && !l.top_k) {
+          if (!(list.sum([](uint32_t) { return true; }) >= by_mass * (1 + 1e-12))) {
+            decided = light;  // the nucleus goes below the bar, what min_p leaves does not
+            by_mass = -1;
+          }
+        } else if (!l.top_k) {
+          decided = light;
+        }
+      }
+      if (decided) {
+        token = s.id[list.draw(l, by_mass, mine, all)];
+        if (tid == 0) put_token(a, r, token, mine, all);
+        return;
+      }
+    }
+    size = 0;
+  }
+  bool again = l.top_k || n > SA_PARTS;
   if (!again) {
     if (l.by_mass) {
-      const u64* bins = s.bin;
+      const double one = one_of((uint32_t)a.vocab);
+      const u64* bins = s.depth;
       if (state == LEFT) {
         __syncthreads();
-        s.bin[tid] = s.bin[tid + SA_THREADS] = 0;
+        for (int i = tid; i < WD_BINS; i += RS_THREADS) s.depth[i] = 0;
         __syncthreads();
-        add_to_bins(row, 0, row.size, SA_THREADS, w, one, s.bin);
+        add_to_bins(row, 0, row.size, RS_THREADS, w, one, s.depth);
         __syncthreads();
       } else {
         bins = space.slots[state].mass;
       }
-      last = last_bin<WD_BINS / SA_THREADS>(bins, target * one, s.of_wave, &s.found);
+      last = last_bin<WD_BINS / RS_THREADS>(bins, target * one, s.of_wave[0], &s.found);
     }
     if (state == LEFT)
-      for (int p = g.wave; p < n; p += SA_WAVES) part_above(row, space, r * space.per_row + p, p, w, last, min_p);
+      for (int p = g.wave; p < n; p += g.WAVES) part_above(row, space, r * space.per_row + p, p, w, last, min_p);
     __syncthreads();  // a workgroup sees what it has written itself
-    u64 longest = 0;
-    for (int p = tid; p < n; p += SA_THREADS) longest = max(longest, (u64)parts[p].count);
-    longest = g.most(longest);
+    u64 longest = 0, none = 0;
+    if (tid < n) longest = parts[tid].count;
+    g.most(longest, none);
     again = longest > PT_LIST;  // too many tokens of the same depth
-    if (!again) size = gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, 0, start);
+    if (!again) size = gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, 0);
     again = again || size > SA_LIST;
   }
   if (again) {
-    Sampler<RowSource<T>> whole_row{row, g, s};
-    token = whole_row.draw(l, w, whole, mine, all);
+    Sampler<RowSource<T>, Group<RS_THREADS>> whole_row{row, w, g, s, order_of(most)};
+    token = whole_row.draw(l, !l.by_mass ? -1 : l.top_k ? (double)l.top_p : target, mine, all);
   } else {
     Kept kept{0, ALL, min_p};
     uint32_t until = ALL;  // as an id
+    double sum = 0, before, some;
+    if (tid < n) sum = parts[tid].kept;
     if (size) {
-      const ListSource in_bin{s.order, size};
-      Sampler<ListSource> list{in_bin, g, s};
       const double above = g.sum(tid < n ? parts[tid].sum : 0.0);
-      double needed;
-      kept.least = list.heaviest(w, NOTHING + 1, target - above, needed);
-      kept.until = list.until(kept.least, needed);
+      const ListSource<T, RS_THREADS> in_bin(s, size, w);
+      u64 largest = 0, none = 0;
+      for (uint32_t i = tid; i < size; i += RS_THREADS) largest = max(largest, (u64)s.order[i]);
+      g.most(largest, none);
+      Sampler<ListSource<T, RS_THREADS>, Group<RS_THREADS>> list{in_bin, w, g, s, (uint32_t)largest};
+      kept = list.kept(l, __builtin_fmax(target - above, 0.0));
       if (kept.until < size) until = s.id[kept.until];
-    }
-    double sum = 0, before;
-    if (tid < n) {
-      sum = parts[tid].kept;
-      const uint32_t count = size ? parts[tid].count : 0;
+      if (tid < n) {
+        const uint32_t end = s.start[tid] + parts[tid].count;
 #pragma unroll 1
-      for (uint32_t k = start; k < start + count; ++k) sum += kept.of(s.order[k], k, w(logit_of(s.order[k])));
+        for (uint32_t k = s.start[tid]; k < end; ++k) sum += kept.of(s.order[k], [&] { return w(logit_of(s.order[k])); }, k);
+      }
     }
     const uint32_t p = g.first(sum, [&](double upto, double total) { return upto > (double)l.uniform * total; }, before, all);
-    token = locate(row, g, p * space.size, min((p + 1) * space.size, row.size), before, (double)l.uniform * all,
-                   [&](float x, uint32_t id) {
-                     const double y = w(x);
-                     const uint32_t b = bin_of(w, x), o = order_of(x);
-                     if (b > last || y < min_p) return 0.0;
-                     return b == last && (o < kept.least || (o == kept.least && id > until)) ? 0.0 : y;
+    const double goal = (double)l.uniform * all;
+    token = locate(row, w, g, p * space.size, min((p + 1) * space.size, row.size), before,
+                   [&](uint32_t o, auto weight, uint32_t id) {
+                     const uint32_t b = bin_of(w, logit_of(o));
+                     if (b > last || (b == last && (o < kept.least || (o == kept.least && id > until)))) return 0.0;
+                     const double y = weight();
+                     return y < min_p ? 0.0 : y;
                    },
-                   mine);
+                   [&](double) { return goal; }, mine, some);
   }
   if (tid == 0) put_token(a, r, token, mine, all);
 }
@@ -908,7 +1087,7 @@ Space space_of(int64_t rows, int64_t vocab, void* at) {
   s.per_row = std::max((vocab + s.size - 1) / s.size, (int64_t)1);
   const int64_t batch = std::min(rows, std::max(PT_BATCH / s.per_row, (int64_t)1)), parts = batch * s.per_row;
   // Many workgroups go over a row again where that is three more launches to a call that is long anyway.
-  const bool wide = parts >= 2048 && s.per_row >= 16 && s.per_row <= SA_TILES;
+  const bool wide = parts >= 2048 && s.per_row >= 16 && s.per_row <= SA_PARTS;
   s.slots_taken = static_cast<uint32_t*>(at);
   s.whole = reinterpret_cast<double*>(static_cast<char*>(at) + 16);
   s.parts = reinterpret_cast<Part*>(s.whole + batch);
@@ -938,15 +1117,15 @@ void enqueue_sample(const tt_sample_args& a, hipStream_t st) {
     constexpr int64_t waves = PT_THREADS / WAVE;
     auto* k = space.size == PT_STEP ? k_sample_parts<T, 1> : space.size == 2 * PT_STEP ? k_sample_parts<T, 2> : k_sample_parts<T, 4>;
     hipLaunchKernelGGL(k, dim3((uint32_t)((some.rows * space.per_row + waves - 1) / waves)), dim3(PT_THREADS), 0, st, some, space);
-    hipLaunchKernelGGL(k_sample<T>, dim3((uint32_t)some.rows), dim3(SA_THREADS), 0, st, some, space);
-    if (!a.top_k && !a.top_p && !a.min_p && space.per_row <= SA_TILES) continue;  // no row is left
+    hipLaunchKernelGGL(k_sample<T>, dim3((uint32_t)some.rows), dim3(DR_THREADS), 0, st, some, space);
+    if (!a.top_k && !a.top_p && !a.min_p) continue;  // no row is left
     if (space.slots && (a.top_p || a.min_p)) {
       const int64_t items = std::min(some.rows, (int64_t)WD_SLOTS) * ((space.per_row + WD_SEGMENT - 1) / WD_SEGMENT);
       const dim3 grid((uint32_t)std::min(items, (int64_t)1024));
       hipLaunchKernelGGL(k_sample_bins<T>, grid, dim3(PT_THREADS), 0, st, some, space);
       hipLaunchKernelGGL(k_sample_above<T>, grid, dim3(PT_THREADS), 0, st, some, space);
     }
-    hipLaunchKernelGGL(k_sample_rest<T>, dim3((uint32_t)some.rows), dim3(SA_THREADS), 0, st, some, space);
+    hipLaunchKernelGGL(k_sample_rest<T>, dim3((uint32_t)some.rows), dim3(RS_THREADS), 0, st, some, space);
   }
 }
 
