@@ -224,7 +224,7 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, S
     }
     part.sum = sum_of_lanes(sum);
     if (limits.limited()) {
-      // The high bar is one that leaves 100 to 450 tokens of a row, of the logits' distributions there are.  The bar is the 32nd largest of the lanes' maxima, which about 64 ln 2 = 44 tokens are not below; the 16th where the lists of
+      // The high bar leaves about 440 tokens of a row whose logits are in no order.  The bar is the 32nd largest of the lanes' maxima, which about 64 ln 2 = 44 tokens are not below; the 16th where the lists of
       // a row would be too many, and the 16th, 8th, 4th, 2nd or largest where a list would not hold them.
       auto largest = [&](int among) {
         uint32_t bar = 0;
@@ -232,7 +232,7 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, S
           if (__popcll(__ballot(own >= (bar | bit))) >= among) bar |= bit;
         return max(bar, NOTHING + 1);
       };
-      part.high = largest(min((int)(512 / space.per_row) + 3, WAVE / 2));
+      part.high = largest(min((int)(400 / space.per_row) + 6, WAVE / 2));
       uint32_t bar = 0, count = 0, counts = 0, in = 0;  // in: a bit for each token of the lane
       for (int among = space.per_row > 128 ? WAVE / 4 : WAVE / 2; among; among /= 2) {
         bar = largest(among);
@@ -281,7 +281,7 @@ constexpr int SA_TILES = 1024;  // that a row is summed up in
 
 struct SampleShared {
   union {
-    u64 key[DR_THREADS];
+    u64 key[RS_THREADS];
     u64 depth[WD_BINS];
     double tile[SA_TILES];
     uint32_t ties[SA_TILES];
@@ -730,6 +730,48 @@ __device__ __forceinline__ u64 sorted(Threads& g, u64 key, uint32_t size) {
   return key;
 }
 
+// What is kept of a list of at most as many tokens as threads, a token a thread.
+struct Picked {
+  bool decided;
+  double weight;  // of the thread's token, 0 if it is not kept
+  u64 last;       // the key of the last one kept: its order, and the inverse of its place
+};
+
+// `complete`: there are no other tokens; `light`: the others weigh less than min_p; `above`: what tokens before the list weigh, all of them kept;
+// `whole`: what all tokens of the row weigh.
+template <class Threads>
+__device__ __forceinline__ Picked pick(Threads& g, uint32_t size, const Limits& l, const Weigher& w, bool complete, bool light, double above, double whole) {
+  SampleShared& s = g.s;
+  const uint32_t tid = g.tid;
+  const bool here = tid < size;
+  const uint32_t own = here ? s.order[tid] : 0;
+  const double weight = here ? w(logit_of(own)) : 0.0;
+  const u64 key = here ? (u64)own << 32 | ~tid : 0;  // the larger the earlier
+  const u64 nth = sorted(g, key, size);
+  double before, upto;
+  g.sum(nth ? w(logit_of((uint32_t)(nth >> 32))) : 0.0, before, upto);
+  before += above, upto += above;
+  const bool limit = l.top_k && l.top_k <= size;
+  const uint32_t most = limit ? (uint32_t)l.top_k : size;
+  if (tid == most - 1) s.above = bits(upto);
+  __syncthreads();
+  const double of = value<double>(s.above);  // what the first `most` weigh
+  const double target = (double)l.top_p * (limit || (complete && l.top_k) ? of : whole);
+  const bool known = complete || limit || !l.top_k;  // what the nucleus is a share of
+  const bool by_mass = l.by_mass && known && (complete || of >= target * (limit ? 1 : 1 + 1e-12));
+  if (tid == 0) s.found = most - 1;
+  __syncthreads();
+  if (by_mass && upto >= target && (tid == 0 || before < target)) atomicMin(&s.found, tid);
+  __syncthreads();
+  if (tid == s.found) s.of = nth;
+  __syncthreads();
+  Picked p;
+  p.last = s.of;
+  p.decided = l.by_mass ? by_mass || (known && light) : complete || limit || light;
+  p.weight = here && key >= p.last && weight >= (l.by_weight ? (double)l.min_p : 0.0) ? weight : 0.0;
+  return p;
+}
+
 // A row by a workgroup, from its parts.  Without limits the part that the random number falls into is read again; with limits
 // the tokens above all high bars, if they are few, are sorted, which answers everything that is asked of them; if the last one kept is not
 // among them the row is left to be gone over again.
@@ -788,34 +830,12 @@ __global__ __launch_bounds__(DR_THREADS) void k_sample(tt_sample_args a, Space s
   uint32_t size = ALL;
   if (n <= SA_PARTS && high != ALL) size = gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, high);
   if (size <= DR_THREADS) {
-    const bool here = (uint32_t)tid < size;
-    const uint32_t own = here ? s.order[tid] : 0;
-    const double weight = here ? w(logit_of(own)) : 0.0;
-    const u64 key = here ? (u64)own << 32 | ~(uint32_t)tid : 0;  // the larger the earlier
-    const u64 nth = sorted(g, key, size);
-    double before, upto;
-    g.sum(nth ? w(logit_of((uint32_t)(nth >> 32))) : 0.0, before, upto);
-    // tokens below the bar are not there: none of them may be kept, or be needed for a sum
-    const bool light = high == NOTHING + 1 || (l.by_weight && w(logit_of(high)) < (double)l.min_p), limit = l.top_k && l.top_k <= size;
-    const bool sums = high == NOTHING + 1 || limit || !l.top_k;  // what the nucleus is a share of is known
-    const uint32_t most = limit ? (uint32_t)l.top_k : size;
-    if ((uint32_t)tid == most - 1) s.above = bits(upto);
-    __syncthreads();
-    const double of = value<double>(s.above);  // what the first `most` weigh
-    const double target = (double)l.top_p * (limit || high == NOTHING + 1 ? of : whole);
-    const bool by_mass = l.by_mass && sums && of >= target * (limit ? 1 : 1 + 1e-12);
-    // the last one kept
-    if (tid == 0) s.found = most - 1;
-    __syncthreads();
-    if (by_mass && upto >= target && (tid == 0 || before < target)) atomicMin(&s.found, (uint32_t)tid);
-    __syncthreads();
-    if ((uint32_t)tid == s.found) s.of = nth;
-    __syncthreads();
-    const bool decided = l.by_mass ? by_mass || (sums && light) : limit || light;
-    if (decided) {
-      const double mine = key >= s.of && here && weight >= (l.by_weight ? (double)l.min_p : 0.0) ? weight : 0.0;
-      const uint32_t thread = g.first(mine, [&](double sum, double total) { return sum > (double)l.uniform * total; }, before, all);
-      if ((uint32_t)tid == thread) put_token(a, r, s.id[tid], mine, all);
+    const bool complete = high == NOTHING + 1, light = l.by_weight && w(logit_of(high)) < (double)l.min_p;
+    const Picked some = pick(g, size, l, w, complete, light, 0, whole);
+    if (some.decided) {
+      double before;
+      const uint32_t thread = g.first(some.weight, [&](double sum, double total) { return sum > (double)l.uniform * total; }, before, all);
+      if ((uint32_t)tid == thread) put_token(a, r, s.id[tid], some.weight, all);
       return;
     }
   }
@@ -984,7 +1004,15 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
     for (int p = tid; p < n; p += RS_THREADS) bar = max(bar, parts[p].bar);
     g.most(bar, none[0], none[1], none[2]);
     size = bar == ALL ? ALL : gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, bar);
-    if (size <= SA_LIST) {
+    if (size <= RS_THREADS) {
+      const Picked some = pick(g, size, l, w, bar == NOTHING + 1, l.by_weight && w(logit_of(bar)) < min_p, 0, whole);
+      if (some.decided) {
+        double before;
+        const uint32_t thread = g.first(some.weight, [&](double sum, double total) { return sum > (double)l.uniform * total; }, before, all);
+        if ((uint32_t)tid == thread) put_token(a, r, s.id[tid], some.weight, all);
+        return;
+      }
+    } else if (size <= SA_LIST) {
       const ListSource<T, RS_THREADS> listed(s, size, w);
       Sampler<ListSource<T, RS_THREADS>, Group<RS_THREADS>> list{listed, w, g, s, order_of(most)};
       double by_mass = !l.by_mass ? -1 : l.top_k ? (double)l.top_p : target;
@@ -1047,12 +1075,19 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
     if (tid < n) sum = parts[tid].kept;
     if (size) {
       const double above = g.sum(tid < n ? parts[tid].sum : 0.0);
-      const ListSource<T, RS_THREADS> in_bin(s, size, w);
-      u64 largest = 0, none = 0;
-      for (uint32_t i = tid; i < size; i += RS_THREADS) largest = max(largest, (u64)s.order[i]);
-      g.most(largest, none);
-      Sampler<ListSource<T, RS_THREADS>, Group<RS_THREADS>> list{in_bin, w, g, s, (uint32_t)largest};
-      kept = list.kept(l, __builtin_fmax(target - above, 0.0));
+      if (size <= RS_THREADS) {
+        Limits by_mass = l;
+        by_mass.top_k = 0;
+        const Picked some = pick(g, size, by_mass, w, true, false, above, whole);
+        kept.least = (uint32_t)(some.last >> 32), kept.until = ~(uint32_t)some.last;
+      } else {
+        const ListSource<T, RS_THREADS> in_bin(s, size, w);
+        u64 largest = 0, none = 0;
+        for (uint32_t i = tid; i < size; i += RS_THREADS) largest = max(largest, (u64)s.order[i]);
+        g.most(largest, none);
+        Sampler<ListSource<T, RS_THREADS>, Group<RS_THREADS>> list{in_bin, w, g, s, (uint32_t)largest};
+        kept = list.kept(l, __builtin_fmax(target - above, 0.0));
+      }
       if (kept.until < size) until = s.id[kept.until];
       if (tid < n) {
         const uint32_t end = s.start[tid] + parts[tid].count;
