@@ -128,35 +128,49 @@ constexpr int AT_TILE = 32;                  // tokens of a wavefront at a time
 constexpr int AT_UNIT = AT_TILE * AT_WAVES;  // tokens of a workgroup at a time
 constexpr int AT_HEADS = 16;                 // query heads of a workgroup
 constexpr int AT_QUERIES = 1024;             // most queries of a call whose tokens are dealt out
-constexpr int AT_GROUPS = 512;               // workgroups that they are dealt out to
 
-// How a call is cut up.
+int padded(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
+
+// How a call is cut up.  An item is a query, or a bundle of queries of the same row.
 struct AttendShape {
-  int group, parts, rows;  // query heads of a head of keys; workgroups that they take; heads of a workgroup
+  int group, parts, rows;  // query heads of a head of keys; workgroups that they take; rows of a product that are in use
+  int bundle;              // most queries of an item
   int64_t lanes;           // heads of keys times parts
   int workers;             // workgroups that the tokens of each lane are dealt out to; 0: one for each query
 };
 
-AttendShape attend_shape(int64_t queries, int64_t heads, int64_t cache_heads) {
+// Tokens are dealt out where a workgroup for each query would not fill the card a few times over: 256 CUs take three workgroups each
+// of heads of up to 64 elements, two of 128, one of 256.  Where there are more queries than rows, some go by the
+// same row, and those that a product has room for are attended to together.
+AttendShape attend_shape(int64_t queries, int64_t heads, int64_t cache_heads, int64_t dim, int64_t table_rows, bool by_rows) {
   AttendShape s;
   s.group = (int)(heads / cache_heads);
   s.parts = (int)div_up(s.group, AT_HEADS);
-  s.rows = std::min(s.group, AT_HEADS);
   s.lanes = cache_heads * s.parts;
-  const bool deal = queries <= AT_QUERIES && queries * s.lanes < 8 * AT_GROUPS;
-  s.workers = deal ? (int)std::max((int64_t)1, AT_GROUPS / s.lanes) : 0;
+  const int groups = padded(dim) == 256 ? 256 : padded(dim) == 64 ? 768 : 512;
+  const bool shared = by_rows && queries > table_rows && queries <= AT_QUERIES && s.group <= AT_HEADS / 2;
+  const bool deal = shared || (queries <= AT_QUERIES && queries * s.lanes < 4096);
+  s.workers = deal ? (int)std::max((int64_t)1, groups / s.lanes) : 0;
+  s.bundle = shared ? AT_HEADS / s.group : 1;
+  s.rows = std::min(s.group, AT_HEADS) * s.bundle;
   return s;
 }
 
-int padded(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
-
-// A workspace: two pieces of output for every worker of every lane, their maxima and sums, and for each
-// query and lane the first piece (-1: there is only one, which was put out at once) and the last worker.
+// A workspace: two pieces of output for every worker of every lane, their maxima and sums, and for each item and lane its first piece and
+// how many it has (one: it was put out at once); with bundles also the items, their first units, the queries in their order
+// and each query's place among them.
+struct Item {
+  int32_t row, members, first;  // of the ordered queries
+  uint32_t from, upto;
+};
 struct AttendSpace {
   float* piece;
   float* statistic;
-  int32_t* first;
-  int32_t* last;
+  int2* pieces;
+  int64_t* start;
+  Item* item;
+  int32_t* order;
+  int32_t* place;  // item * AT_HEADS + which of its queries
   int64_t bytes;
 };
 AttendSpace attend_space(const AttendShape& s, int64_t queries, int64_t dim, void* at) {
@@ -165,23 +179,29 @@ AttendSpace attend_space(const AttendShape& s, int64_t queries, int64_t dim, voi
   const int64_t pieces = 2 * s.workers * s.lanes * s.rows;
   w.piece = static_cast<float*>(at);
   w.statistic = w.piece + pieces * padded(dim);
-  w.first = reinterpret_cast<int32_t*>(w.statistic + 2 * pieces);
-  w.last = w.first + queries * s.lanes;
-  w.bytes = pieces * (padded(dim) + 2) * 4 + 2 * queries * s.lanes * 4;
+  w.pieces = reinterpret_cast<int2*>(w.statistic + 2 * pieces);
+  w.start = reinterpret_cast<int64_t*>(w.pieces + queries * s.lanes);
+  w.bytes = pieces * (padded(dim) + 2) * 4 + queries * s.lanes * 8;
+  if (s.bundle > 1) {
+    w.item = reinterpret_cast<Item*>(w.start + AT_QUERIES + 1);
+    w.order = reinterpret_cast<int32_t*>(w.item + AT_QUERIES);
+    w.place = w.order + AT_QUERIES;
+    w.bytes += (AT_QUERIES + 1) * 8 + AT_QUERIES * (int64_t)(sizeof(Item) + 8);
+  }
   return w;
 }
 
 // Which tokens of which row a query sees.
 struct Seen {
-  int64_t row;
+  int32_t row;
   uint32_t from, upto;
 };
 __device__ inline Seen seen(const tt_attend_args& a, int64_t i) {
   Seen s;
-  s.row = a.rows ? a.rows[i] : i;
-  const int64_t most = a.width * a.cache.block_size;
+  const int64_t row = a.rows ? a.rows[i] : i, most = a.width * a.cache.block_size;
   int64_t n = min((int64_t)a.lengths[i], most);
-  if (n < 0 || s.row < 0 || s.row >= a.table_rows) n = 0;
+  if (n < 0 || row < 0 || row >= a.table_rows) n = 0;
+  s.row = n ? (int32_t)row : 0;
   s.upto = (uint32_t)n;
   s.from = a.window > 0 && n > a.window ? (uint32_t)(n - a.window) : 0;
   return s;
@@ -221,6 +241,8 @@ __device__ inline float over_groups(float x, bool sum) {
   return sum ? z + u : fmaxf(z, u);
 }
 
+constexpr uint32_t ALL = 0xFFFFFFFFu;
+
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
 
 // One workgroup: a lane's heads, for some tokens of a query after the other.
@@ -246,15 +268,28 @@ struct Attend {
   Division by_block;
   Shared& s;
   int lane, wave, c, g;
-  int64_t head;   // of keys
-  int part, here;  // query heads: which of the lane's, how many of them
+  int64_t head;  // of keys
+  int part;      // which of its query heads
 
-  // Tokens upto `end` of query i; slot: where the piece goes, negative: it is the whole output.
-  __device__ void run(int64_t i, const Seen& q, uint32_t from, uint32_t end, int64_t slot) {
+  // The query and the head of it that row r of a product stands for.
+  __device__ __forceinline__ int64_t query_of(int64_t i, const Item& q, int r) const { return shape.bundle > 1 ? space.order[q.first + r / shape.group] : i; }
+  __device__ __forceinline__ int64_t head_of(int r) const { return head * shape.group + part * AT_HEADS + (shape.bundle > 1 ? r % shape.group : r); }
+
+  // Tokens from `from` up to `end` of item i; slot: where the piece goes, negative: it is the whole output.
+  __device__ __forceinline__ void run(int64_t i, const Item& q, uint32_t from, uint32_t end, int64_t slot) {
     const tt_paged_cache& cache = a.cache;
     const uint32_t dim = (uint32_t)cache.dim;
+    const int here = shape.bundle > 1 ? q.members * shape.group : min(AT_HEADS, shape.group - part * AT_HEADS);
+    // what the lane's own query sees, of several; all of them see the tokens between
+    uint32_t own_from = 0, own_upto = ALL, all_from = 0, all_upto = ALL;
+    const int64_t own = c < here ? query_of(i, q, c) : 0;
+    if (shape.bundle > 1) {
+      const Seen mine = seen(a, own);
+      own_from = mine.from, own_upto = mine.upto;
+      all_upto = seen(a, space.order[q.first]).upto, all_from = seen(a, space.order[q.first + q.members - 1]).from;
+    }
     u32x4 query[STEPS];
-    const T* row = static_cast<const T*>(a.query) + i * a.query_stride + (head * shape.group + part * AT_HEADS + c) * a.query_head_stride;
+    const T* row = static_cast<const T*>(a.query) + own * a.query_stride + (c < here ? head_of(c) : 0) * a.query_head_stride;
 #pragma unroll
     for (int k = 0; k < STEPS; ++k) {
       const uint32_t d = EIGHT ? k / 2 * 64 + g * 16 + k % 2 * 8 : k * 32 + g * 8;
@@ -270,7 +305,7 @@ struct Attend {
       before *= LOG2E;
     }
 
-    const int32_t* table = a.table + q.row * a.table_stride;
+    const int32_t* table = a.table + (int64_t)q.row * a.table_stride;
     const char* keys = static_cast<const char*>(cache.keys) + head * cache.key_head_stride * SIZE;
     const char* values = static_cast<const char*>(cache.values) + head * cache.value_head_stride * SIZE;
     uint32_t base = from + wave * AT_TILE;
@@ -387,6 +422,13 @@ struct Attend {
               for (int w = 0; w < VWORDS; ++w) value[k][w] = 0;  // a weight of zero does not take out NaN
             }
         }
+        if (base < all_from || base + AT_TILE > all_upto) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t t = base + k / 4 * 16 + g * 4 + k % 4;
+            if (t < own_from || t >= own_upto) x[k] = -__builtin_inff();
+          }
+        }
       }
       if (there_next) load_keys();
       if (there) {
@@ -461,7 +503,7 @@ struct Attend {
     const int64_t unit = head * shape.parts + part;
     if (wave == 0 && g == 0 && c < here) {
       if (slot < 0) {
-        if (a.lse) a.lse[i * a.lse_stride + head * shape.group + part * AT_HEADS + c] = total == 0 ? -__builtin_inff() : (all + __log2f(total)) * LN2;
+        if (a.lse) a.lse[own * a.lse_stride + head_of(c)] = total == 0 ? -__builtin_inff() : (all + __log2f(total)) * LN2;
       } else {
         float* to = space.statistic + ((slot * shape.lanes + unit) * shape.rows + c) * 2;
         to[0] = all, to[1] = total;
@@ -482,8 +524,8 @@ struct Attend {
         typename Eight<T>::type z;
 #pragma unroll
         for (int k = 0; k < 8; ++k) z[k] = (T)(of == 0 ? 0.0f : y[k / 4][k % 4] * scale);
-        *reinterpret_cast<typename Eight<T>::type*>(static_cast<T*>(a.out) + i * a.out_stride +
-                                                    (head * shape.group + part * AT_HEADS + row) * a.out_head_stride + d) = z;
+        *reinterpret_cast<typename Eight<T>::type*>(static_cast<T*>(a.out) + query_of(i, q, row) * a.out_stride +
+                                                    head_of(row) * a.out_head_stride + d) = z;
       } else {
         float* to = space.piece + ((slot * shape.lanes + unit) * shape.rows + row) * D + d;
 #pragma unroll
@@ -494,58 +536,168 @@ struct Attend {
   }
 };
 
-// Units that a query's tokens take; one that sees nothing has one too, to put out its zeros.
-__device__ inline int64_t units_of(const Seen& q) { return max((q.upto - q.from + AT_UNIT - 1) / AT_UNIT, 1u); }
+// Units that an item's tokens take; one that sees nothing has one too, to put out its zeros.
+__device__ inline int64_t units_of(uint32_t from, uint32_t upto) { return max((upto - from + AT_UNIT - 1) / AT_UNIT, 1u); }
 
-// The first units of the queries, one behind the other, and the number of all.
-__device__ inline void starts_of(const tt_attend_args& a, int64_t* start, int64_t* sums) {
-  const int n = (int)a.queries, tid = threadIdx.x, per = (n + AT_THREADS - 1) / AT_THREADS;
-  int64_t mine = 0;
-  for (int i = tid * per; i < min(n, (tid + 1) * per); ++i) mine += units_of(seen(a, i));
-  int64_t upto = mine;  // inclusive sums over the wavefront
-#pragma unroll
-  for (int d = 1; d < WAVE; d *= 2) {
-    const int64_t other = __shfl_up(upto, d);
-    if (tid % WAVE >= d) upto += other;
-  }
-  if (tid % WAVE == WAVE - 1) sums[tid / WAVE] = upto;
-  __syncthreads();
-  int64_t at = upto - mine;
-  for (int w = 0; w < tid / WAVE; ++w) at += sums[w];
-  for (int i = tid * per; i < min(n, (tid + 1) * per); ++i) {
-    start[i] = at;
-    at += units_of(seen(a, i));
-  }
-  if (tid == AT_THREADS - 1) start[n] = at;
-  __syncthreads();
+// Inclusive sums over a wavefront: shifts by 1, 2, 4, 8 in rows of 16, then the last lanes of rows 0 and 2, then of row 1.
+template <int CTRL, int ROWS>
+__device__ inline int64_t plus_lanes(int64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xf, false);
+  return v + (int64_t)((uint64_t)hi << 32 | lo);
+}
+__device__ inline int64_t wave_sums(int64_t v) {
+  v = plus_lanes<0x118, 0xf>(plus_lanes<0x114, 0xf>(plus_lanes<0x112, 0xf>(plus_lanes<0x111, 0xf>(v))));
+  return plus_lanes<0x143, 0xc>(plus_lanes<0x142, 0xa>(v));
 }
 
-// Workgroups of the same lane share out the units of all queries evenly, so that short and long requests do not wait for
-// each other; where the cut goes through a query its pieces are joined by k_join.
+// Sums over the workgroup, with the sum of all.
+template <int N>
+__device__ inline int64_t group_sums(int64_t v, int64_t* of_wave, int64_t& all) {
+  const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
+  int64_t upto = wave_sums(v);
+  __syncthreads();
+  if (lane == WAVE - 1) of_wave[wave] = upto;
+  __syncthreads();
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < N / WAVE; ++w) {
+    if (w == wave) upto += all;
+    all += of_wave[w];
+  }
+  return upto;
+}
+
+constexpr int BU_THREADS = AT_QUERIES;
+
+// Puts the queries of a call in the order of rows and, within a row, of their last tokens, and those of a row that see some of the same tokens into bundles: so
+// no bundle reads more tokens than its queries do one by one.  By one workgroup, a query a thread.  301 queries of 40 rows
+// that see 1,024 tokens of 12 heads each take 133 us one by one.
+__global__ __launch_bounds__(BU_THREADS) void k_bundle(tt_attend_args a, AttendShape shape, AttendSpace space) {
+  __shared__ uint64_t s_key[BU_THREADS];
+  __shared__ int64_t s_wave[BU_THREADS / WAVE];
+  __shared__ int32_t s_first[BU_THREADS + 1];
+  __shared__ Seen s_seen[BU_THREADS];
+  const int tid = threadIdx.x, lane = tid % WAVE, wave = tid / WAVE, n = (int)a.queries;
+  uint64_t key = ~(uint64_t)0;
+  if (tid < n) {
+    s_seen[tid] = seen(a, tid);
+    // rows are fewer than queries, so below 2^10
+    key = ((uint64_t)s_seen[tid].row << 32 | s_seen[tid].upto) << 10 | (uint64_t)tid;
+  }
+  // bitonic: exchanges between threads whose numbers differ in one bit
+#pragma unroll 1
+  for (int run = 2; run / 2 < n; run *= 2) {
+#pragma unroll 1
+    for (int apart = run / 2; apart; apart /= 2) {
+      uint64_t other;
+      if (apart < WAVE) {
+        other = (uint64_t)__shfl_xor((unsigned long long)key, apart);
+      } else {
+        __syncthreads();
+        s_key[tid] = key;
+        __syncthreads();
+        other = s_key[tid ^ apart];
+      }
+      const bool smaller = !(tid & apart) == !(tid & run);
+      key = smaller == (other < key) ? other : key;
+    }
+  }
+  __syncthreads();
+  s_key[tid] = key;
+  __syncthreads();
+  const int i = (int)(key & (BU_THREADS - 1));
+  const Seen own = tid < n ? s_seen[i] : Seen{0, 0, 0};
+  bool first = tid < n;
+  if (tid > 0 && tid < n) {
+    const Seen before = s_seen[s_key[tid - 1] & (BU_THREADS - 1)];
+    first = before.row != own.row || own.from > before.upto;
+  }
+  // where the run of queries that this one is of starts: the number of starts, and each start's place
+  int64_t all;
+  const int64_t runs = group_sums<BU_THREADS>(first, s_wave, all);
+  if (first) s_first[runs - 1] = tid;
+  __syncthreads();
+  const int nth = tid < n ? tid - s_first[runs - 1] : 1;
+  const bool opens = tid < n && nth % shape.bundle == 0;
+  int64_t items;
+  const int64_t item = group_sums<BU_THREADS>(opens, s_wave, items) - 1;
+  __syncthreads();
+  if (opens) s_first[item] = tid;
+  if (tid == 0) s_first[items] = n;
+  __syncthreads();
+  if (tid < n) {
+    space.order[tid] = i;
+    space.place[i] = (int32_t)item * AT_HEADS + tid - s_first[item];
+  }
+  Item mine{0, 0, 0, 0, 0};
+  if (tid < items) {
+    mine.first = s_first[tid], mine.members = s_first[tid + 1] - mine.first;
+    const Seen from = s_seen[s_key[mine.first] & (BU_THREADS - 1)], upto = s_seen[s_key[mine.first + mine.members - 1] & (BU_THREADS - 1)];
+    mine.row = from.row, mine.from = from.from, mine.upto = upto.upto;
+    space.item[tid] = mine;
+  }
+  const int64_t units = tid < items ? units_of(mine.from, mine.upto) : 0;
+  int64_t sum;
+  const int64_t upto = group_sums<BU_THREADS>(units, s_wave, sum);
+  space.start[tid] = upto - units;  // past the last item: all units
+  if (tid == 0) space.start[BU_THREADS] = sum;
+  (void)lane, (void)wave;
+}
+
+// Workgroups of the same lane share out the units of all items evenly, so that short and long requests do not wait for
+// each other; where the cut goes through an item its pieces are joined by k_join.
 template <class T, bool EIGHT, int D, bool WHOLE>
-__global__ __launch_bounds__(AT_THREADS, D == 256 ? 1 : 2) void k_attend(tt_attend_args a, AttendShape shape, AttendSpace space,
-                                                                     Division by_block, int64_t first) {
+__global__ __launch_bounds__(AT_THREADS, D == 256 ? 1 : D == 64 ? 3 : 2) void k_attend(tt_attend_args a, AttendShape shape, AttendSpace space,
+                                                                                   Division by_block, int64_t first) {
   typedef Attend<T, EIGHT, D, WHOLE> Work;
   __shared__ typename Work::Shared s;
-  __shared__ int64_t s_start[AT_QUERIES + 1], s_sums[AT_WAVES];
+  __shared__ int64_t s_start[AT_QUERIES + 1], s_wave[AT_WAVES];
+  __shared__ Seen s_seen[AT_QUERIES];
   const int64_t id = first + blockIdx.x, unit = id % shape.lanes;
-  const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
-  const int part = (int)(unit % shape.parts);
-  Work work{a, shape, space, by_block, s, lane, wave, lane % 16, lane / 16, unit / shape.parts, part,
-            min(AT_HEADS, shape.group - part * AT_HEADS)};
+  const int tid = threadIdx.x, lane = tid % WAVE, wave = tid / WAVE;
+  Work work{a, shape, space, by_block, s, lane, wave, lane % 16, lane / 16, unit / shape.parts, (int)(unit % shape.parts)};
   if (!shape.workers) {
     const int64_t i = id / shape.lanes;
     const Seen q = seen(a, i);
-    work.run(i, q, q.from, q.upto, -1);
+    work.run(i, Item{q.row, 1, 0, q.from, q.upto}, q.from, q.upto, -1);
     return;
   }
-  starts_of(a, s_start, s_sums);
-  const int n = (int)a.queries, worker = (int)(id / shape.lanes);
-  const int64_t all = s_start[n], sharers = min((int64_t)shape.workers, all);  // each has a unit at least, so a query's pieces have workers in a row
+  constexpr int MANY = AT_QUERIES / AT_THREADS;
+  const int n = (int)a.queries;
+  if (shape.bundle > 1) {
+    for (int k = tid; k <= AT_QUERIES; k += AT_THREADS) s_start[k] = space.start[k];
+  } else {
+    const int per = (n + AT_THREADS - 1) / AT_THREADS;
+    Seen q[MANY];
+    int64_t units = 0, all;
+#pragma unroll
+    for (int k = 0; k < MANY; ++k) {
+      const int i = tid * per + k;
+      if (k < per && i < n) q[k] = seen(a, i);
+    }
+#pragma unroll
+    for (int k = 0; k < MANY; ++k)
+      if (k < per && tid * per + k < n) units += units_of(q[k].from, q[k].upto);
+    int64_t at = group_sums<AT_THREADS>(units, s_wave, all) - units;
+#pragma unroll
+    for (int k = 0; k < MANY; ++k) {
+      const int i = tid * per + k;
+      if (k < per && i < n) {
+        s_start[i] = at, s_seen[i] = q[k];
+        at += units_of(q[k].from, q[k].upto);
+      }
+    }
+    if (tid == 0) s_start[n] = all;
+  }
+  __syncthreads();
+  const int worker = (int)(id / shape.lanes);
+  // past the last item there are no units; each worker has one at least, so an item's pieces have workers in a row
+  const int64_t all = s_start[shape.bundle > 1 ? AT_QUERIES : n], sharers = min((int64_t)shape.workers, all);
   if (worker >= sharers) return;
   const int64_t upto = all * (worker + 1) / sharers;
   int64_t at = all * worker / sharers;
-  int lo = 0, hi = n;  // the query that unit `at` is of
+  int lo = 0, hi = n;  // the last item that starts at `at` or before, and has units
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
     if (s_start[mid] <= at) lo = mid;
@@ -555,60 +707,54 @@ __global__ __launch_bounds__(AT_THREADS, D == 256 ? 1 : 2) void k_attend(tt_atte
     const int64_t begin = s_start[lo], end = s_start[lo + 1], stop = min(end, upto);
     const int slot = 2 * worker + (nth > 0);
     const bool whole = at == begin && stop == end;
-    if (threadIdx.x == 0) {
-      if (at == begin) space.first[lo * shape.lanes + unit] = whole ? -1 : slot;
-      if (stop == end) space.last[lo * shape.lanes + unit] = worker;
-    }
-    const Seen q = seen(a, lo);
+    // the worker of its last unit: the first one whose share reaches the item's end
+    if (tid == 0 && at == begin) space.pieces[lo * shape.lanes + unit] = int2{slot, (int)((end * sharers + all - 1) / all) - worker};
+    const Item q = shape.bundle > 1 ? space.item[lo] : Item{s_seen[lo].row, 1, 0, s_seen[lo].from, s_seen[lo].upto};
     work.run(lo, q, q.from + (uint32_t)(at - begin) * AT_UNIT, stop == end ? q.upto : q.from + (uint32_t)(stop - begin) * AT_UNIT,
              whole ? -1 : slot);
     at = stop;
   }
 }
 
-// The pieces of a query head together: those of its first worker, and the first one of each worker up to its last.
+// The pieces of a query head together: the first one, and the first one of each worker after its own.  ACROSS threads go by the
+// elements, four each, of SPLIT workgroups a head; the others by the pieces, each with a maximum of its own.
 template <class T>
-__global__ __launch_bounds__(AT_THREADS) void k_join(tt_attend_args a, AttendShape shape, AttendSpace space, int wide) {
-  __shared__ float s_by[AT_GROUPS], s_max[AT_WAVES], s_sum[AT_WAVES];
+__global__ __launch_bounds__(AT_THREADS) void k_join(tt_attend_args a, AttendShape shape, AttendSpace space, int wide, int split) {
   __shared__ f32x4 s_out[AT_THREADS];
-  const int64_t i = blockIdx.x / a.heads;
-  const int h = (int)(blockIdx.x % a.heads), kv = h / shape.group, nth = h % shape.group;
-  const int64_t unit = (int64_t)kv * shape.parts + nth / AT_HEADS, row = nth % AT_HEADS;
-  const int first = space.first[i * shape.lanes + unit];
-  if (first < 0) return;
-  const int before = first / 2, pieces = space.last[i * shape.lanes + unit] - before + 1;
-  auto place = [&](int k) { return ((k ? 2 * (before + k) : first) * shape.lanes + unit) * shape.rows + row; };
-  const int tid = threadIdx.x;
-  float top = -__builtin_inff();
-  for (int k = tid; k < pieces; k += AT_THREADS) top = fmaxf(top, space.statistic[place(k) * 2]);
-#pragma unroll
-  for (int d = 1; d < WAVE; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-  if (tid % WAVE == 0) s_max[tid / WAVE] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < AT_WAVES; ++w) top = fmaxf(top, s_max[w]);
-  const float less = top == -__builtin_inff() ? 0.0f : top;
-  float sum = 0;
-  for (int k = tid; k < pieces; k += AT_THREADS) {
-    const float by = __builtin_amdgcn_exp2f(space.statistic[place(k) * 2] - less);
-    s_by[k] = by;
-    sum += by * space.statistic[place(k) * 2 + 1];
-  }
-#pragma unroll
-  for (int d = 1; d < WAVE; d *= 2) sum += __shfl_xor(sum, d);
-  if (tid % WAVE == 0) s_sum[tid / WAVE] = sum;
-  __syncthreads();
-  sum = 0;
-#pragma unroll
-  for (int w = 0; w < AT_WAVES; ++w) sum += s_sum[w];
-  const int across = wide / 4, side = AT_THREADS / across, d = tid % across * 4;
+  __shared__ float s_top[AT_THREADS], s_sum[AT_THREADS];
+  const int64_t id = blockIdx.x / split, i = id / a.heads;
+  const int h = (int)(id % a.heads), kv = h / shape.group, nth = h % shape.group;
+  const int64_t unit = (int64_t)kv * shape.parts + nth / AT_HEADS;
+  const int32_t place = shape.bundle > 1 ? space.place[i] : (int32_t)(i * AT_HEADS);
+  const int64_t row = place % AT_HEADS * shape.group + nth % AT_HEADS;
+  const int2 of = space.pieces[place / AT_HEADS * shape.lanes + unit];
+  if (of.y == 1) return;
+  const int before = of.x / 2, tid = threadIdx.x, across = wide / 4 / split, side = AT_THREADS / across;
+  const int d = (blockIdx.x % split * across + tid % across) * 4;
+  float top = -__builtin_inff(), sum = 0;
   f32x4 y = 0;
-  for (int k = tid / across; k < pieces; k += side) y += *reinterpret_cast<const f32x4*>(space.piece + place(k) * wide + d) * s_by[k];
-  s_out[tid] = y;
+#pragma unroll 4
+  for (int k = tid / across; k < of.y; k += side) {
+    const int64_t at = ((k ? 2 * (before + k) : of.x) * shape.lanes + unit) * shape.rows + row;
+    const float m = space.statistic[at * 2], l = space.statistic[at * 2 + 1];
+    const f32x4 x = *reinterpret_cast<const f32x4*>(space.piece + at * wide + d);
+    const float most = fmaxf(top, m), less = most == -__builtin_inff() ? 0.0f : most;
+    const float old = __builtin_amdgcn_exp2f(top - less), by = __builtin_amdgcn_exp2f(m - less);
+    y = y * old + x * by, sum = sum * old + l * by, top = most;
+  }
+  s_out[tid] = y, s_top[tid] = top, s_sum[tid] = sum;
   __syncthreads();
-  if (tid == 0 && a.lse) a.lse[i * a.lse_stride + h] = sum == 0 ? -__builtin_inff() : (top + __log2f(sum)) * LN2;
-  if (tid >= across || d >= a.cache.dim) return;
-  for (int k = 1; k < side; ++k) y += s_out[k * across + tid];
+  if (tid >= across) return;
+  float most = top;
+  for (int k = 1; k < side; ++k) most = fmaxf(most, s_top[k * across + tid]);
+  const float less = most == -__builtin_inff() ? 0.0f : most;
+  sum = 0, y = 0;
+  for (int k = 0; k < side; ++k) {
+    const float by = __builtin_amdgcn_exp2f(s_top[k * across + tid] - less);
+    y += s_out[k * across + tid] * by, sum += s_sum[k * across + tid] * by;
+  }
+  if (tid == 0 && blockIdx.x % split == 0 && a.lse) a.lse[i * a.lse_stride + h] = sum == 0 ? -__builtin_inff() : (most + __log2f(sum)) * LN2;
+  if (d >= a.cache.dim) return;
   const float scale = (a.cache.value_scale ? a.cache.value_scale[kv] : 1.0f) / sum;
   T* to = static_cast<T*>(a.out) + i * a.out_stride + h * a.out_head_stride + d;
 #pragma unroll
@@ -664,20 +810,27 @@ hipError_t launch_write(const tt_write_args& a, hipStream_t st) {
 }
 
 int64_t attend_workspace(int64_t queries, int64_t heads, int64_t cache_heads, int64_t dim) {
-  return attend_space(attend_shape(queries, heads, cache_heads), queries, dim, nullptr).bytes;
+  // of the calls of these sizes the one that needs most
+  int64_t bytes = 0;
+  for (bool shared : {false, true})
+    bytes = std::max(bytes, attend_space(attend_shape(queries, heads, cache_heads, dim, shared ? 0 : queries, shared), queries, dim, nullptr).bytes);
+  return bytes;
 }
 
 hipError_t launch_attend(const tt_attend_args& a, hipStream_t st) {
-  const AttendShape shape = attend_shape(a.queries, a.heads, a.cache.heads);
-  const AttendSpace space = attend_space(shape, a.queries, a.cache.dim, a.workspace);
   const bool eight = a.cache.type == TT_E4M3, half = a.type == TT_F16;
+  const AttendShape shape = attend_shape(a.queries, a.heads, a.cache.heads, a.cache.dim, a.table_rows, a.rows != nullptr);
+  const AttendSpace space = attend_space(shape, a.queries, a.cache.dim, a.workspace);
+  if (shape.bundle > 1) hipLaunchKernelGGL(k_bundle, dim3(1), dim3(BU_THREADS), 0, st, a, shape, space);
   if (half && eight) enqueue_attend<_Float16, true>(a, shape, space, st);
   else if (half) enqueue_attend<_Float16, false>(a, shape, space, st);
   else if (eight) enqueue_attend<__bf16, true>(a, shape, space, st);
   else enqueue_attend<__bf16, false>(a, shape, space, st);
   if (shape.workers > 1) {
+    // few heads are joined by several workgroups each: 32 heads of 256 pieces take 10 us with one
+    const int split = a.queries * a.heads <= 128 ? padded(a.cache.dim) / 32 : 1;
     auto* k = half ? k_join<_Float16> : k_join<__bf16>;
-    hipLaunchKernelGGL(k, dim3((uint32_t)(a.queries * a.heads)), dim3(AT_THREADS), 0, st, a, shape, space, padded(a.cache.dim));
+    hipLaunchKernelGGL(k, dim3((uint32_t)(a.queries * a.heads * split)), dim3(AT_THREADS), 0, st, a, shape, space, padded(a.cache.dim), split);
   }
   return hipGetLastError();
 }
