@@ -127,7 +127,7 @@ constexpr int AT_WAVES = AT_THREADS / WAVE;
 constexpr int AT_TILE = 32;                  // tokens of a wavefront at a time
 constexpr int AT_UNIT = AT_TILE * AT_WAVES;  // tokens of a workgroup at a time
 constexpr int AT_HEADS = 16;                 // query heads of a workgroup
-constexpr int AT_QUERIES = 1024;             // most queries of a call whose tokens are dealt out
+constexpr int AT_QUERIES = 512;              // most queries of a call whose tokens are dealt out
 
 int padded(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
@@ -200,7 +200,7 @@ __device__ inline Seen seen(const tt_attend_args& a, int64_t i) {
   Seen s;
   const int64_t row = a.rows ? a.rows[i] : i, most = a.width * a.cache.block_size;
   int64_t n = min((int64_t)a.lengths[i], most);
-  if (n < 0 || row < 0 || row >= a.table_rows) n = 0;
+  if (n < 0 || row < 0 || row >= a.table_rows || a.cache.blocks == 0) n = 0;
   s.row = n ? (int32_t)row : 0;
   s.upto = (uint32_t)n;
   s.from = a.window > 0 && n > a.window ? (uint32_t)(n - a.window) : 0;
@@ -383,15 +383,16 @@ struct Attend {
     int32_t entry = entry_of(base);
     uint32_t there = addresses(entry, base);
     entry = entry_of(base + AT_UNIT);
-    if (there) {
+    if (base < end) {
       load_keys();
       load_values();
     }
+    // Without branches: tokens that are not there are read from the cache's first place, and past the last tile nothing else is.
     while (base < end) {
       const uint32_t there_next = addresses(entry, base + AT_UNIT);
       entry = entry_of(base + 2 * AT_UNIT);
       float x[8];
-      if (there) {
+      {
         f32x4 score[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -430,8 +431,11 @@ struct Attend {
           }
         }
       }
-      if (there_next) load_keys();
-      if (there) {
+      // what follows is kept behind the loads, and the products behind the weights: moved ahead they take half as many registers again
+      __builtin_amdgcn_sched_barrier(0);
+      load_keys();
+      __builtin_amdgcn_sched_barrier(0);
+      {
         // weights go by a maximum that may be 8 too low: they stay below 2^8, and most tiles leave it as it is
         float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
         if (__any(most > top + 8.0f)) {
@@ -456,6 +460,7 @@ struct Attend {
           weight[k] = two<T>(x[2 * k], x[2 * k + 1]);
           rest[k] = two<T>(x[2 * k] - one_of<T>(weight[k], 0), x[2 * k + 1] - one_of<T>(weight[k], 1));
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < MINE; j += 2) {
           uint32_t pair[8];
@@ -476,7 +481,8 @@ struct Attend {
           out[j + 1] = product<T>(odd, rest, out[j + 1]);
         }
       }
-      if (there_next) load_values();
+      __builtin_amdgcn_sched_barrier(0);
+      load_values();
       there = there_next;
       base += AT_UNIT;
     }
@@ -582,8 +588,8 @@ __global__ __launch_bounds__(BU_THREADS) void k_bundle(tt_attend_args a, AttendS
   uint64_t key = ~(uint64_t)0;
   if (tid < n) {
     s_seen[tid] = seen(a, tid);
-    // rows are fewer than queries, so below 2^10
-    key = ((uint64_t)s_seen[tid].row << 32 | s_seen[tid].upto) << 10 | (uint64_t)tid;
+    // rows are fewer than queries, so below 2^9
+    key = ((uint64_t)s_seen[tid].row << 32 | s_seen[tid].upto) << 9 | (uint64_t)tid;
   }
   // bitonic: exchanges between threads whose numbers differ in one bit
 #pragma unroll 1
