@@ -51,16 +51,39 @@ struct Eight {
   typedef T type __attribute__((ext_vector_type(8), aligned(alignof(T))));
 };
 
+// A quotient by s, of which r is the rounded reciprocal, rounded as a division would: the product is put right by its remainder (Markstein's
+// theorem), which holds while neither leaves the normal range.  Where r is not used it is 0.
+__device__ inline float quotient(float x, float s, float r) {
+  const float q = x * r, y = fmaf(fmaf(-q, s, x), r, q);
+  return __builtin_isfpclass(q, 0x108) ? y : q;  // of normal numbers; zeros keep their sign, infinities and NaN what they are
+}
+// The reciprocal where quotients that are then taken into 2^-10 .. 448 may go by it.
+__device__ inline float reciprocal_of(float s) {
+  const float a = fabsf(s);
+  return a > 0x1p-60f && a < 0x1p60f ? 1.0f / s : 0.0f;
+}
+
 // Eight elements, divided by their scale, in the cache's type.
 template <class I, class O>
 __device__ inline void put_eight(typename Eight<I>::type x, const float* scale, int64_t head, O* to) {
   if constexpr (std::is_same<O, uint8_t>::value) {
-    const float s = scale ? scale[head] : 1.0f;
     float f[8];
 #pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = (float)x[k];
+    if (scale) {
+      const float s = scale[head], r = reciprocal_of(s);
+      if (r != 0.0f) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] = quotient(f[k], s, r);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] /= s;
+      }
+    }
+#pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float q = (float)x[k] / s;
-      f[k] = q > 448.0f ? 448.0f : q < -448.0f ? -448.0f : q;  // NaN stays
+      const float y = __builtin_amdgcn_fmed3f(f[k], -448.0f, 448.0f);
+      f[k] = f[k] != f[k] ? f[k] : y;  // NaN stays
     }
     typename Words<2>::type w;
 #pragma unroll
@@ -85,21 +108,19 @@ __device__ inline void put_eight(typename Eight<I>::type x, const float* scale, 
   }
 }
 
-// Each thread moves eight keys and the eight values beside them.
+// Each thread moves eight keys and the eight values beside them, of `total` of the tokens from `first` on.
 template <class I, class O>
-__global__ __launch_bounds__(WR_THREADS) void k_write(tt_write_args a, uint32_t per_head, uint32_t per_token, int64_t first,
-                                                      int64_t total) {
-  const int64_t at = first + (int64_t)blockIdx.x * WR_THREADS + threadIdx.x;
+__global__ __launch_bounds__(WR_THREADS) void k_write(tt_write_args a, Division by_token, Division by_head, Division by_block, int64_t first, uint32_t total) {
+  const uint32_t at = blockIdx.x * WR_THREADS + threadIdx.x;
   if (at >= total) return;
-  const int64_t token = at / per_token;
-  const uint32_t rest = (uint32_t)(at - token * per_token), head = rest / per_head, d = (rest - head * per_head) * 8;
-  const int64_t slot = a.slots[token];
+  const uint32_t nth = quotient(at, by_token), rest = at - nth * by_token.divisor, head = quotient(rest, by_head), d = (rest - head * by_head.divisor) * 8;
+  const int64_t token = first + nth, slot = a.slots[token];
   typedef typename Eight<I>::type In;
   const In k = *reinterpret_cast<const In*>(static_cast<const I*>(a.keys) + token * a.key_stride + head * a.key_head_stride + d);
   const In v = *reinterpret_cast<const In*>(static_cast<const I*>(a.values) + token * a.value_stride + head * a.value_head_stride + d);
   if (slot < 0) return;
   const tt_paged_cache& c = a.cache;
-  const int64_t block = slot <= 0xFFFFFFFF ? (uint32_t)slot / (uint32_t)c.block_size : slot / c.block_size;
+  const int64_t block = slot <= 0x7FFFFFFF ? quotient((uint32_t)slot, by_block) : slot / c.block_size;
   const int64_t place = slot - block * c.block_size;
   if (block >= c.blocks) return;
   put_eight<I, O>(k, c.key_scale, head,
@@ -790,11 +811,12 @@ void enqueue_attend(const tt_attend_args& a, const AttendShape& shape, const Att
 
 template <class I, class O>
 void enqueue_write(const tt_write_args& a, hipStream_t st) {
-  const uint32_t per_head = (uint32_t)(a.cache.dim / 8), per_token = (uint32_t)a.cache.heads * per_head;
-  const int64_t total = a.tokens * per_token, most = MAX_ITEMS / WR_THREADS * WR_THREADS;
-  for (int64_t at = 0; at < total; at += most)
-    hipLaunchKernelGGL((k_write<I, O>), dim3((uint32_t)div_up(std::min(most, total - at), WR_THREADS)), dim3(WR_THREADS), 0, st, a,
-                       per_head, per_token, at, total);
+  const int64_t per_head = a.cache.dim / 8, per_token = a.cache.heads * per_head, most = 0x7FFFFFFF / per_token;  // tokens of a launch
+  for (int64_t at = 0; at < a.tokens; at += most) {
+    const uint32_t total = (uint32_t)(std::min(most, a.tokens - at) * per_token);
+    hipLaunchKernelGGL((k_write<I, O>), dim3((uint32_t)div_up(total, WR_THREADS)), dim3(WR_THREADS), 0, st, a, division(per_token), division(per_head),
+                       division(a.cache.block_size), at, total);
+  }
 }
 
 template <class I>
