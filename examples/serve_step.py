@@ -1,10 +1,10 @@
-"""Answers to a batch of prompts, each a list of small whole numbers: tokenizer, block table, token sets, grammar
-masks and shaped logits together, as a serving program runs them.
+"""Answers to a batch of prompts, each a list of small whole numbers: tokenizer, block table, cached keys and values and the
+attention over them, token sets, grammar masks, shaped logits and drawn tokens together, as a serving program runs them.
 
     python examples/serve_step.py
 
-The model is a stand-in (random logits by last token, row and step); all the rest is what a server does around one.
-Nothing waits for the device inside the loop but the check whether every answer has ended.
+The model is a stand-in (random logits by last token, row and step, and one layer of attention with random weights); all the rest
+is what a server does around one.  Nothing waits for the device inside the loop but the check whether every answer has ended.
 """
 import os
 import sys
@@ -51,7 +51,18 @@ def answer(prompts, steps=48, seed=0):
     cache = tt.BlockTable(rows, width=width, blocks=width * rows, block_size=16)
     slots, positions, row_of = cache.plan(offsets)           # where the model puts the prompts' keys and values
 
-    model = torch.randn(vocab, vocab, device="cuda", generator=torch.Generator("cuda").manual_seed(seed)).bfloat16()
+    g = torch.Generator("cuda").manual_seed(seed)
+    model = torch.randn(vocab, vocab, device="cuda", generator=g).bfloat16()
+    heads, kv, dim = 4, 2, 64
+    embed, to_q, to_k, to_v, to_logits = (torch.randn(*shape, device="cuda", generator=g).mul_(shape[0]**-0.5).bfloat16() for shape in (
+        (vocab, dim), (dim, heads * dim), (dim, kv * dim), (dim, kv * dim), (heads * dim, vocab)))
+    layer = tt.KeyValueCache(cache, kv, dim)
+
+    def write(ids, slots):
+        x = embed[ids.long()]
+        layer.write((x @ to_k).view(-1, kv, dim), (x @ to_v).view(-1, kv, dim), slots)
+
+    write(ids, slots)
     made = torch.zeros(rows, steps, dtype=torch.int32, device="cuda")
     n_made = torch.zeros(rows, dtype=torch.int32, device="cuda")
     states = torch.zeros(rows, dtype=torch.int32, device="cuda")
@@ -59,16 +70,19 @@ def answer(prompts, steps=48, seed=0):
     # the prompts' last tokens; an empty one begins after an end token
     last = torch.cat([ids, ids.new_full((1,), end)])[torch.where(offsets[1:] > offsets[:-1], offsets[1:] - 1, len(ids))].long()
     fixed = {k: torch.full((rows,), v, device="cuda") for k, v in
-             dict(repetition=1.2, frequency=0.3, presence=0.1, temperature=0.8).items()}
+             dict(repetition=1.2, frequency=0.3, presence=0.1, temperature=0.8, top_p=0.95, min_p=0.02).items()}
+    shaping = {k: fixed[k] for k in ("repetition", "frequency", "presence", "temperature")}
     # closing gets likelier than random logits make it
     closing = dict(bias_offsets=torch.arange(rows + 1, device="cuda"), bias_values=torch.full((rows,), 1.5, device="cuda"),
                    bias_ids=torch.full((rows,), ord("]"), dtype=torch.int32, device="cuda"))
     slot, count = (torch.empty(n, dtype=torch.int64, device="cuda") for n in (rows, 1))
     for step in range(steps):
         logits = model[(last + 97 * torch.arange(rows, device="cuda") + step) % vocab]
+        seen_before = layer.attend((embed[last] @ to_q).view(rows, heads, dim))  # the last token over all that its row has cached
+        logits = logits + seen_before.view(rows, -1) @ to_logits
         out = tt.shape_logits(logits, seen=seen, generated=made, n_generated=n_made, allowed=allowed, allowed_rows=states,
-                              **fixed, **closing)
-        chosen = out.argmax(dim=1).int()
+                              **shaping, **closing)
+        chosen = tt.sample_tokens(out, torch.rand(rows, device="cuda", generator=g), top_p=fixed["top_p"], min_p=fixed["min_p"])
         ended = live & (chosen == end)
         live &= ~ended
         cache.release_into(ended, count)
@@ -77,6 +91,7 @@ def answer(prompts, steps=48, seed=0):
         n_made += live.int()
         cache.plan_into(slot, count)                         # a slot for each live answer's next token, -1 for the others
         last = torch.where(live, chosen.long(), last)
+        write(last, slot)
         if not bool(live.any()):
             break
     strings, off = tokens.strings.cpu().numpy().tobytes(), tokens.offsets.tolist()
