@@ -697,6 +697,15 @@ __device__ __forceinline__ uint32_t gather(Threads& g, const Part* parts, const 
   return size;
 }
 
+// All tokens of a row that is short enough, as a list.
+template <class Threads, class T>
+__device__ __forceinline__ uint32_t gather_row(Threads& g, const RowSource<T>& row) {
+  __syncthreads();
+  for (uint32_t i = g.tid; i < row.size; i += Threads::THREADS) g.s.order[i] = order_of((float)row.row[i]), g.s.id[i] = i;
+  __syncthreads();
+  return row.size;
+}
+
 // The largest logit of a row's parts, by each wavefront.
 __device__ inline float most_of(const Part* parts, int64_t n) {
   uint32_t best = 0;
@@ -828,7 +837,8 @@ __global__ __launch_bounds__(DR_THREADS) void k_sample(tt_sample_args a, Space s
   }
   whole = g.sum(whole);
   uint32_t size = ALL;
-  if (n <= SA_PARTS && high != ALL) size = gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, high);
+  if (row.size <= DR_THREADS) size = gather_row(g, row), high = NOTHING + 1;
+  else if (n <= SA_PARTS && high != ALL) size = gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, high);
   if (size <= DR_THREADS) {
     const bool complete = high == NOTHING + 1, light = l.by_weight && w(logit_of(high)) < (double)l.min_p;
     const Picked some = pick(g, size, l, w, complete, light, 0, whole);
@@ -1003,7 +1013,8 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
     uint32_t bar = NOTHING + 1, none[3] = {0, 0, 0};
     for (int p = tid; p < n; p += RS_THREADS) bar = max(bar, parts[p].bar);
     g.most(bar, none[0], none[1], none[2]);
-    size = bar == ALL ? ALL : gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, bar);
+    if (row.size <= SA_LIST) size = gather_row(g, row), bar = NOTHING + 1;
+    else size = bar == ALL ? ALL : gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, bar);
     if (size <= RS_THREADS) {
       const Picked some = pick(g, size, l, w, bar == NOTHING + 1, l.by_weight && w(logit_of(bar)) < min_p, 0, whole);
       if (some.decided) {
