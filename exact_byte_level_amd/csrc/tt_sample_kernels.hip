@@ -143,7 +143,7 @@ constexpr int PT_STEP = WAVE * 8;
 constexpr int PT_LIST = 64;
 constexpr int PT_THREADS = 256;
 constexpr int64_t PT_BATCH = 65536;  // parts of a launch
-constexpr int WD_SLOTS = 256;        // rows that are gone over again by many workgroups
+constexpr int WD_SLOTS = 256;        // most rows of a launch that are gone over again by many workgroups
 constexpr int WD_BINS = 2048;
 constexpr int WD_SEGMENT = 8;        // parts of a workgroup
 
@@ -169,6 +169,7 @@ struct Space {
   Part* parts;
   Listed* lists;
   Slot* slots;  // nullptr: rows are gone over again by a workgroup each
+  uint32_t slot_count;
   int64_t per_row, bytes;
   uint32_t size;  // tokens of a part
 };
@@ -224,17 +225,19 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, S
     }
     part.sum = sum_of_lanes(sum);
     if (limits.limited()) {
-      // The high bar leaves about 440 tokens of a row whose logits are in no order.  The bar is the 32nd largest of the lanes' maxima, which about 64 ln 2 = 44 tokens are not below; the 16th where the lists of
-      // a row would be too many, and the 16th, 8th, 4th, 2nd or largest where a list would not hold them.
+      // A bar is the n-th largest of the lanes' maxima, n halved where the list would not hold what is not below it.  The high one leaves 300
+      // to 400 tokens of a row; the other one, for where top_k may be more than that, about 64 ln 2 = 44 of a part, or half of that where the
+      // lists of a row would be too many.
       auto largest = [&](int among) {
         uint32_t bar = 0;
         for (uint32_t bit = 1u << 31; bit; bit >>= 1)
           if (__popcll(__ballot(own >= (bar | bit))) >= among) bar |= bit;
         return max(bar, NOTHING + 1);
       };
-      part.high = largest(min((int)(400 / space.per_row) + 6, WAVE / 2));
+      const int few = min((int)(300 / space.per_row) + 6, WAVE / 2);
+      const bool many = limits.top_k > 128;
       uint32_t bar = 0, count = 0, counts = 0, in = 0;  // in: a bit for each token of the lane
-      for (int among = space.per_row > 128 ? WAVE / 4 : WAVE / 2; among; among /= 2) {
+      for (int among = !many ? few : space.per_row > 128 ? WAVE / 4 : WAVE / 2; among; among /= 2) {
         bar = largest(among);
         const float from = logit_of(bar);
         in = 0;
@@ -248,7 +251,7 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, S
         if (count <= PT_LIST) break;
       }
       if (count > PT_LIST) bar = ALL, count = 0;
-      part.bar = bar, part.count = count, part.high = max(part.high, bar);
+      part.bar = bar, part.count = count, part.high = many ? max(largest(few), bar) : bar;
       if (count) {
         const uint32_t upto = sums_upto(counts), all = of_lane(upto, WAVE - 1);
         // where the lane's tokens of each step go, a byte each again
@@ -276,7 +279,6 @@ constexpr int RS_THREADS = 1024;
 constexpr int SA_PARTS = 256;   // of a row whose lists are put together
 constexpr int SA_LIST = 4096;   // tokens of the lists that are above all bars
 constexpr int SA_BINS = 256;
-constexpr int SA_COPIES = 2;    // of the bins
 constexpr int SA_TILES = 1024;  // that a row is summed up in
 
 struct SampleShared {
@@ -286,9 +288,10 @@ struct SampleShared {
     double tile[SA_TILES];
     uint32_t ties[SA_TILES];
   };
+  double weight[SA_LIST];
   uint32_t order[SA_LIST], id[SA_LIST];
   uint32_t start[SA_PARTS];
-  u64 digit[SA_COPIES][SA_BINS + 1];
+  u64 digit[SA_BINS];
   u64 of_wave[2][RS_THREADS / WAVE];
   u64 above, of;
   uint32_t found, last, place;
@@ -318,14 +321,14 @@ struct Group {
     __syncthreads();
     if (lane == WAVE - 1) s.of_wave[0][wave] = bits(upto);
     __syncthreads();
-    V all = 0, base = 0;
-#pragma unroll
-    for (int k = 0; k < WAVES; ++k) {
-      if (k == wave) base = all;
-      all += value<V>(s.of_wave[0][k]);
-    }
-    before += base, upto += base;
-    return all;
+    V total = lane < WAVES ? value<V>(s.of_wave[0][lane]) : 0;  // of the wavefronts up to the lane's
+    total += from_lanes<0x111, 0xf>(total);
+    total += from_lanes<0x112, 0xf>(total);
+    total += from_lanes<0x114, 0xf>(total);
+    total += from_lanes<0x118, 0xf>(total);
+    const V base = wave ? of_lane(total, wave - 1) : 0, here = of_lane(total, wave);
+    before += base, upto = lane == WAVE - 1 ? here : upto + base;
+    return of_lane(total, WAVES - 1);
   }
   template <class V>
   __device__ __forceinline__ V sum(V x) {
@@ -333,25 +336,13 @@ struct Group {
     return sum(x, before, upto);
   }
   // The largest x and y.
-  __device__ __forceinline__ void most(u64& x, u64& y) {
+  __device__ __forceinline__ void most(uint32_t& x, uint32_t& y) {
     x = max_of_lanes(x), y = max_of_lanes(y);
     __syncthreads();
-    if (lane == 0) s.of_wave[0][wave] = x, s.of_wave[1][wave] = y;
+    if (lane == 0) s.of_wave[0][wave] = (u64)x << 32 | y;
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < WAVES; ++k) x = max(x, s.of_wave[0][k]), y = max(y, s.of_wave[1][k]);
-  }
-  // The same for four of 32 bits.
-  __device__ __forceinline__ void most(uint32_t& x, uint32_t& y, uint32_t& z, uint32_t& u) {
-    x = max_of_lanes(x), y = max_of_lanes(y), z = max_of_lanes(z), u = max_of_lanes(u);
-    __syncthreads();
-    if (lane == 0) s.of_wave[0][wave] = (u64)x << 32 | y, s.of_wave[1][wave] = (u64)z << 32 | u;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < WAVES; ++k) {
-      const u64 v = s.of_wave[0][k], w = s.of_wave[1][k];
-      x = max(x, (uint32_t)(v >> 32)), y = max(y, (uint32_t)v), z = max(z, (uint32_t)(w >> 32)), u = max(u, (uint32_t)w);
-    }
+    const u64 v = lane < WAVES ? s.of_wave[0][lane] : 0;
+    x = max_of_lanes((uint32_t)(v >> 32)), y = max_of_lanes((uint32_t)v);
   }
 
   // The first thread at which the running sum of x satisfies enough(sum, sum of all), which 0 does not and which once true stays so; the last
@@ -423,34 +414,23 @@ struct RowSource {
     }
   }
 };
-// In registers, the same number of places to each of N threads: reading them from LDS for every question, one after the other with a
-// wavefront to each SIMD, takes three times as long.
-template <class T, int N>
+template <class T>
 struct ListSource {
-  static constexpr int LOW = RowSource<T>::LOW, MINE = SA_LIST / N;
   static constexpr bool LISTED = true;
-  uint32_t size, per, own;
-  uint32_t order[MINE];
-  double weight[MINE];
-  __device__ __forceinline__ ListSource(const SampleShared& s, uint32_t size_, const Weigher& w) : size(size_) {
-    per = (size + N - 1) / N, own = threadIdx.x * per;
-#pragma unroll
-    for (int k = 0; k < MINE; ++k) order[k] = k < (int)per && own + k < size ? s.order[own + k] : 0;
-#pragma unroll
-    for (int k = 0; k < MINE; ++k) weight[k] = k < (int)per && order[k] ? w(logit_of(order[k])) : 0.0;
-  }
-  template <int, class F>
+  static constexpr int LOW = RowSource<T>::LOW;
+  const SampleShared& s;
+  uint32_t size;
+  template <int N, class F>
   __device__ __forceinline__ void each(const Weigher&, F f) const {
-#pragma unroll
-    for (int k = 0; k < MINE; ++k)
-      if (k < (int)per) f(order[k], [&] { return weight[k]; }, own + k);  // an order of 0 past the last
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < size; i += N) f(s.order[i], [&] { return s.weight[i]; }, i);
   }
-  template <int, class F>
+  template <int N, class F>
   __device__ __forceinline__ void in_row(const Weigher&, uint32_t, uint32_t, F f) const {
-    bool more = true;
-#pragma unroll
-    for (int k = 0; k < MINE; ++k)
-      if (k < (int)per && more) more = f(order[k], [&] { return weight[k]; }, own + k);
+    const uint32_t per = (size + N - 1) / N, own = threadIdx.x * per, stop = min(own + per, size);
+#pragma unroll 1
+    for (uint32_t i = own; i < stop; ++i)
+      if (!f(s.order[i], [&] { return s.weight[i]; }, i)) break;
   }
 };
 
@@ -517,7 +497,7 @@ struct Sampler {
   __device__ __forceinline__ double sum(F take) {
     double sum = 0;
     source.template each<N>(w, [&](uint32_t o, auto weight, uint32_t) {
-      if (o && take(o)) sum += weight();
+      if (take(o)) sum += weight();
     });
     return g.sum(sum);
   }
@@ -527,43 +507,37 @@ struct Sampler {
   // `there` how many (how much) at it.
   __device__ __forceinline__ uint32_t reach(bool mass, uint32_t least, double target, double& above, double& there) {
     const double one = mass ? one_of(source.size) : 1.0, unit = 1 / one;
-    u64 largest = most, smallest = least;  // of the orders that it may be
+    uint32_t largest = most, smallest = least;  // of the orders that it may be
     above = 0;
 #pragma unroll 1
     while (true) {
-      const uint32_t apart = (uint32_t)(largest ^ smallest);
+      const uint32_t apart = largest ^ smallest;
       const int top = max(apart ? 32 - __builtin_clz(apart) : 0, Source::LOW), width = min(8, top - Source::LOW), shift = top - width;
-      const uint32_t prefix = top < 32 ? (uint32_t)largest >> top : 0;
+      const uint32_t prefix = top < 32 ? largest >> top : 0;
       __syncthreads();
-      for (int i = g.tid; i < SA_COPIES * (SA_BINS + 1); i += N) s.digit[0][i] = 0;
+      if (g.tid < SA_BINS) s.digit[g.tid] = 0;
       __syncthreads();
       source.template each<N>(w, [&](uint32_t o, auto weight, uint32_t) {
         if (o >= least && (top == 32 || o >> top == prefix))
-          atomicAdd(&s.digit[g.lane % SA_COPIES][o >> shift & ((1u << width) - 1)], mass ? fixed(weight() * one) : (u64)1);
+          atomicAdd(&s.digit[o >> shift & ((1u << width) - 1)], mass ? fixed(weight() * one) : (u64)1);
       });
       __syncthreads();
-      u64 x = 0;  // from the largest down
-      if (g.tid < SA_BINS) {
-#pragma unroll
-        for (int k = 0; k < SA_COPIES; ++k) x += s.digit[k][SA_BINS - 1 - g.tid];
-      }
+      const u64 x = g.tid < SA_BINS ? s.digit[SA_BINS - 1 - g.tid] : 0;  // from the largest down
       u64 before, all;
       const uint32_t digit = SA_BINS - 1 - g.first(x, [&](u64 upto, u64) { return upto && above + (double)upto * unit >= target; }, before, all);
       above += (double)before * unit;
-      there = 0;
-#pragma unroll
-      for (int k = 0; k < SA_COPIES; ++k) there += (double)s.digit[k][digit] * unit;
+      there = (double)s.digit[digit] * unit;
       const uint32_t found = prefix << width | digit;
       // the largest and the smallest that are left; the rest of the digits that they share is skipped
       largest = 0;
-      u64 inverse = 0;
+      uint32_t inverse = 0;
       source.template each<N>(w, [&](uint32_t o, auto, uint32_t) {
-        if (o >= least && o >> shift == found) largest = max(largest, (u64)o), inverse = max(inverse, (u64)(uint32_t)~o);
+        if (o >= least && o >> shift == found) largest = max(largest, o), inverse = max(inverse, ~o);
       });
       g.most(largest, inverse);
-      smallest = (uint32_t)~inverse;
+      smallest = ~inverse;
       if (!inverse) return most;  // nothing weighs anything
-      if (largest == smallest || !width) return (uint32_t)largest;
+      if (largest == smallest || !width) return largest;
     }
   }
 
@@ -647,54 +621,54 @@ __device__ inline void put_token(const tt_sample_args& a, int64_t r, uint32_t to
 // more than there is room for: then none are taken.  s.start[p]: where those of part p begin.
 template <class Threads>
 __device__ __forceinline__ uint32_t gather(Threads& g, const Part* parts, const Listed* lists, int n, uint32_t bar) {
-  constexpr int WAVES = Threads::WAVES, MANY = 8;  // lists of a wavefront that are on their way together
+  constexpr int WAVES = Threads::WAVES, MANY = 128 / WAVES;  // lists of a wavefront that are on their way together
   SampleShared& s = g.s;
   __syncthreads();
   if (g.tid < SA_PARTS) s.start[g.tid] = 0;
   __syncthreads();
   Listed entry[MANY];
-  uint32_t count[MANY];
-  auto take = [&](int from) {
-#pragma unroll
-    for (int k = 0; k < MANY; ++k) {
-      const int p = from + k * WAVES;
-      if (from + k * WAVES >= n) continue;
-      entry[k] = lists[(int64_t)p * PT_LIST + g.lane];  // past the count there is anything
-      count[k] = parts[p].count;
-    }
-  };
-  for (int from = g.wave; from < n; from += MANY * WAVES) {
-    take(from);
-#pragma unroll
-    for (int k = 0; k < MANY; ++k) {
-      if (from + k * WAVES >= n) continue;
-      const uint32_t some = __popcll(__ballot(g.lane < (int)count[k] && entry[k].order >= bar));
-      if (g.lane == 0) s.start[from + k * WAVES] = some;
-    }
-  }
-  __syncthreads();
-  uint32_t start, upto;
-  const uint32_t size = g.sum(g.tid < SA_PARTS ? s.start[g.tid] : 0, start, upto);
-  if (g.tid < SA_PARTS) s.start[g.tid] = start;
-  __syncthreads();
-  if (size <= SA_LIST) {
+  uint32_t count[MANY], start, upto, size = 0;
+  // the same loop counts what there is, and then takes it
+#pragma unroll 1
+  for (int take = 0; take < 2; ++take) {
+#pragma unroll 1
     for (int from = g.wave; from < n; from += MANY * WAVES) {
-      if (n > MANY * WAVES) take(from);
-      uint32_t start[MANY];
+      if (!take || n > MANY * WAVES) {
 #pragma unroll
-      for (int k = 0; k < MANY; ++k) start[k] = s.start[min(from + k * WAVES, SA_PARTS - 1)];
+        for (int k = 0; k < MANY; ++k) {
+          const int p = min(from + k * WAVES, n - 1);
+          entry[k] = lists[(int64_t)p * PT_LIST + g.lane];  // past the count there is anything
+          count[k] = from + k * WAVES < n ? parts[p].count : 0;
+        }
+      }
 #pragma unroll
       for (int k = 0; k < MANY; ++k) {
-        if (from + k * WAVES >= n) continue;
         const bool here = g.lane < (int)count[k] && entry[k].order >= bar;
         const u64 in = __ballot(here);
-        const uint32_t to = start[k] + __popcll(in & (((u64)1 << g.lane) - 1));
-        if (here) s.order[to] = entry[k].order, s.id[to] = entry[k].id;
+        if (!take) {
+          if (g.lane == 0 && in) s.start[from + k * WAVES] = __popcll(in);
+        } else if (here) {
+          const uint32_t to = s.start[from + k * WAVES] + __popcll(in & (((u64)1 << g.lane) - 1));
+          s.order[to] = entry[k].order, s.id[to] = entry[k].id;
+        }
       }
     }
+    __syncthreads();
+    if (take) break;
+    size = g.sum(g.tid < SA_PARTS ? s.start[g.tid] : 0, start, upto);
+    if (g.tid < SA_PARTS) s.start[g.tid] = start;
+    __syncthreads();
+    if (size > SA_LIST) break;
   }
-  __syncthreads();
   return size;
+}
+
+// The weights of a list.
+template <class Threads>
+__device__ __forceinline__ void weigh(Threads& g, uint32_t size, const Weigher& w) {
+#pragma unroll 1
+  for (uint32_t i = g.tid; i < size; i += Threads::THREADS) g.s.weight[i] = w(logit_of(g.s.order[i]));
+  __syncthreads();
 }
 
 // All tokens of a row that is short enough, as a list.
@@ -713,7 +687,34 @@ __device__ inline float most_of(const Part* parts, int64_t n) {
   return logit_of(max_of_lanes(best));
 }
 
-// The keys of the workgroup's threads, the largest first; `size` of them are not 0.  Bitonic: exchanges between threads whose numbers differ in one bit.
+// What the lane whose number differs in bit APART holds.
+template <int APART>
+__device__ inline uint32_t across(uint32_t v) {
+  const auto dpp = [](uint32_t x, auto ctrl) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, 0xf, 0xf, false);
+  };
+  if constexpr (APART == 1) return dpp(v, std::integral_constant<int, 0xB1>());         // within four: 1 0 3 2
+  else if constexpr (APART == 2) return dpp(v, std::integral_constant<int, 0x4E>());    // 2 3 0 1
+  else if constexpr (APART == 4)
+    return dpp(dpp(v, std::integral_constant<int, 0x141>()), std::integral_constant<int, 0x1B>());  // eight mirrored, then four
+  else if constexpr (APART == 8) return dpp(v, std::integral_constant<int, 0x128>());   // sixteen turned by eight
+  else if constexpr (APART == 16) {  // rows of 16 exchanged between two copies: the even ones twice, the odd ones twice
+    const auto both = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return threadIdx.x & 16 ? both[0] : both[1];
+  } else {
+    const auto both = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return threadIdx.x & 32 ? both[0] : both[1];
+  }
+}
+
+// One exchange of a bitonic sort: the first of the two takes the larger key, in every second run the smaller.
+template <int APART>
+__device__ inline u64 exchanged(u64 key, int tid, int run) {
+  const u64 other = (u64)across<APART>((uint32_t)(key >> 32)) << 32 | across<APART>((uint32_t)key);
+  return (!(tid & APART) == !(tid & run)) == (other > key) ? other : key;
+}
+
+// The keys of the workgroup's threads, the largest first; `size` of them are not 0.
 template <class Threads>
 __device__ __forceinline__ u64 sorted(Threads& g, u64 key, uint32_t size) {
   SampleShared& s = g.s;
@@ -721,20 +722,19 @@ __device__ __forceinline__ u64 sorted(Threads& g, u64 key, uint32_t size) {
   for (int run = 2; run < 2 * Threads::THREADS; run *= 2) {
     if (run / 2 >= (int)size) break;  // what is not 0 is sorted
 #pragma unroll 1
-    for (int apart = run / 2; apart; apart /= 2) {
-      u64 other;
-      if (apart < WAVE) {
-        other = __shfl_xor(key, apart);
-      } else {
-        __syncthreads();
-        s.key[g.tid] = key;
-        __syncthreads();
-        other = s.key[g.tid ^ apart];
-      }
-      // the first of the two takes the larger, in every second run the smaller
-      const bool larger = !(g.tid & apart) == !(g.tid & run);
-      key = larger == (other > key) ? other : key;
+    for (int apart = run / 2; apart >= WAVE; apart /= 2) {
+      __syncthreads();
+      s.key[g.tid] = key;
+      __syncthreads();
+      const u64 other = s.key[g.tid ^ apart];
+      key = (!(g.tid & apart) == !(g.tid & run)) == (other > key) ? other : key;
     }
+    if (run > 32) key = exchanged<32>(key, g.tid, run);
+    if (run > 16) key = exchanged<16>(key, g.tid, run);
+    if (run > 8) key = exchanged<8>(key, g.tid, run);
+    if (run > 4) key = exchanged<4>(key, g.tid, run);
+    if (run > 2) key = exchanged<2>(key, g.tid, run);
+    key = exchanged<1>(key, g.tid, run);
   }
   return key;
 }
@@ -746,30 +746,31 @@ struct Picked {
   u64 last;       // the key of the last one kept: its order, and the inverse of its place
 };
 
-// `complete`: there are no other tokens; `light`: the others weigh less than min_p; `above`: what tokens before the list weigh, all of them kept;
-// `whole`: what all tokens of the row weigh.
+// `bar`: the order that the list goes down to, all tokens being there if nothing is below; `above`: what tokens before the list weigh, all of
+// them kept; `whole`: what all tokens of the row weigh.  The list is shorter than the workgroup.
 template <class Threads>
-__device__ __forceinline__ Picked pick(Threads& g, uint32_t size, const Limits& l, const Weigher& w, bool complete, bool light, double above, double whole) {
+__device__ __forceinline__ Picked pick(Threads& g, uint32_t size, uint32_t top_k, const Limits& l, const Weigher& w, uint32_t bar, double above, double whole) {
   SampleShared& s = g.s;
   const uint32_t tid = g.tid;
-  const bool here = tid < size;
-  const uint32_t own = here ? s.order[tid] : 0;
-  const double weight = here ? w(logit_of(own)) : 0.0;
+  const bool here = tid < size, complete = bar <= NOTHING + 1;
+  const uint32_t own = here ? s.order[tid] : tid == size ? bar : 0;
+  const double weight = w(logit_of(own));
+  s.weight[tid] = weight;
   const u64 key = here ? (u64)own << 32 | ~tid : 0;  // the larger the earlier
   const u64 nth = sorted(g, key, size);
+  __syncthreads();
+  const bool light = l.by_weight && s.weight[size] < (double)l.min_p;  // what is below the bar
   double before, upto;
-  g.sum(nth ? w(logit_of((uint32_t)(nth >> 32))) : 0.0, before, upto);
+  g.sum(nth ? s.weight[~(uint32_t)nth] : 0.0, before, upto);
   before += above, upto += above;
-  const bool limit = l.top_k && l.top_k <= size;
-  const uint32_t most = limit ? (uint32_t)l.top_k : size;
-  if (tid == most - 1) s.above = bits(upto);
+  const bool limit = top_k && top_k <= size;
+  const uint32_t most = limit ? top_k : size;
+  if (tid == most - 1) s.above = bits(upto), s.found = tid;
   __syncthreads();
   const double of = value<double>(s.above);  // what the first `most` weigh
-  const double target = (double)l.top_p * (limit || (complete && l.top_k) ? of : whole);
-  const bool known = complete || limit || !l.top_k;  // what the nucleus is a share of
+  const double target = (double)l.top_p * (limit || (complete && top_k) ? of : whole);
+  const bool known = complete || limit || !top_k;  // what the nucleus is a share of
   const bool by_mass = l.by_mass && known && (complete || of >= target * (limit ? 1 : 1 + 1e-12));
-  if (tid == 0) s.found = most - 1;
-  __syncthreads();
   if (by_mass && upto >= target && (tid == 0 || before < target)) atomicMin(&s.found, tid);
   __syncthreads();
   if (tid == s.found) s.of = nth;
@@ -795,10 +796,9 @@ __global__ __launch_bounds__(DR_THREADS) void k_sample(tt_sample_args a, Space s
   const RowSource<T> row{static_cast<const T*>(a.logits) + r * a.logits_stride, (uint32_t)a.vocab};
   Group<DR_THREADS> g{s, tid, tid % WAVE, tid / WAVE};
 
-  uint32_t top = 0, bar = NOTHING + 1, high = NOTHING + 1, none = 0;  // the largest order; the highest of the bars and of the high ones
-  for (int p = tid * per; p < min((tid + 1) * per, n); ++p)
-    top = max(top, order_of(parts[p].most)), bar = max(bar, parts[p].bar), high = max(high, parts[p].high);
-  g.most(top, bar, high, none);
+  uint32_t top = 0, high = NOTHING + 1;  // the largest order and the highest of the high bars
+  for (int p = tid * per; p < min((tid + 1) * per, n); ++p) top = max(top, order_of(parts[p].most)), high = max(high, parts[p].high);
+  g.most(top, high);
   if (tid == 0) space.state[r] = DONE;
   if (top <= NOTHING) {
     if (tid == 0) put_token(a, r, ALL, 0, 1);
@@ -817,8 +817,8 @@ __global__ __launch_bounds__(DR_THREADS) void k_sample(tt_sample_args a, Space s
       uint32_t first = 0;
       for (int q = tid; q < n; q += DR_THREADS)
         if (order_of(parts[q].most) == top) first = max(first, ~(uint32_t)q);
-      uint32_t none_too = 0, nor_this = 0;
-      g.most(first, none, none_too, nor_this);
+      uint32_t none = 0;
+      g.most(first, none);
       p = ~first;
     } else {
       const uint32_t thread = g.first(whole, [&](double upto, double total) { return upto > (double)l.uniform * total; }, before, all);
@@ -830,18 +830,26 @@ __global__ __launch_bounds__(DR_THREADS) void k_sample(tt_sample_args a, Space s
         before += y;
       }
     }
-    token = locate(row, w, g, p * space.size, min((p + 1) * space.size, row.size), before,
-                   [&](uint32_t o, auto weight, uint32_t) { return l.single ? (o == top ? 1.0 : 0.0) : weight(); }, [&](double) { return goal; }, mine, some);
+    const uint32_t from = p * space.size;
+    const RowSource<T> part{row.row + from, min(space.size, row.size - from)};
+    gather_row(g, part);
+    if (l.single) {
+      for (uint32_t i = tid; i < part.size; i += DR_THREADS) s.weight[i] = s.order[i] == top ? 1.0 : 0.0;
+      __syncthreads();
+    } else {
+      weigh(g, part.size, w);
+    }
+    const ListSource<T> list{s, part.size};
+    token = from + locate(list, w, g, 0, part.size, before, [&](uint32_t, auto weight, uint32_t) { return weight(); }, [&](double) { return goal; }, mine, some);
     if (tid == 0) put_token(a, r, token, mine, all);
     return;
   }
   whole = g.sum(whole);
   uint32_t size = ALL;
-  if (row.size <= DR_THREADS) size = gather_row(g, row), high = NOTHING + 1;
+  if (row.size < DR_THREADS) size = gather_row(g, row), high = NOTHING + 1;
   else if (n <= SA_PARTS && high != ALL) size = gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, high);
-  if (size <= DR_THREADS) {
-    const bool complete = high == NOTHING + 1, light = l.by_weight && w(logit_of(high)) < (double)l.min_p;
-    const Picked some = pick(g, size, l, w, complete, light, 0, whole);
+  if (size < DR_THREADS) {
+    const Picked some = pick(g, size, (uint32_t)l.top_k, l, w, high, 0, whole);
     if (some.decided) {
       double before;
       const uint32_t thread = g.first(some.weight, [&](double sum, double total) { return sum > (double)l.uniform * total; }, before, all);
@@ -852,13 +860,13 @@ __global__ __launch_bounds__(DR_THREADS) void k_sample(tt_sample_args a, Space s
   __syncthreads();
   if (tid == 0) {
     space.whole[r] = whole;
-    s.found = WD_SLOTS;
-    if (space.slots && !l.top_k && n <= SA_PARTS) s.found = atomicAdd(space.slots_taken, 1u);
-    space.state[r] = s.found < WD_SLOTS ? s.found : LEFT;
-    if (s.found < WD_SLOTS) space.slots[s.found].row = r;
+    s.found = ALL;
+    if (space.slots && !l.top_k) s.found = atomicAdd(space.slots_taken, 1u);
+    space.state[r] = s.found < space.slot_count ? s.found : LEFT;
+    if (s.found < space.slot_count) space.slots[s.found].row = r;
   }
   __syncthreads();
-  if (s.found < WD_SLOTS)
+  if (s.found < space.slot_count)
     for (int i = tid; i < WD_BINS; i += DR_THREADS) space.slots[s.found].mass[i] = 0;
 }
 
@@ -952,7 +960,7 @@ __device__ __forceinline__ uint32_t last_bin(const u64* bin, double target, u64*
 template <class T>
 __global__ __launch_bounds__(PT_THREADS) void k_sample_bins(tt_sample_args a, Space space) {
   __shared__ u64 s_bin[WD_BINS];
-  const uint32_t slots = min(*space.slots_taken, (uint32_t)WD_SLOTS), across = (uint32_t)((space.per_row + WD_SEGMENT - 1) / WD_SEGMENT);
+  const uint32_t slots = min(*space.slots_taken, space.slot_count), across = (uint32_t)((space.per_row + WD_SEGMENT - 1) / WD_SEGMENT);
   for (uint32_t item = blockIdx.x; item < slots * across; item += gridDim.x) {
     Slot& slot = space.slots[item / across];
     const int64_t r = slot.row;
@@ -976,7 +984,7 @@ template <class T>
 __global__ __launch_bounds__(PT_THREADS) void k_sample_above(tt_sample_args a, Space space) {
   __shared__ u64 s_wave[PT_THREADS / WAVE];
   __shared__ uint32_t s_found;
-  const uint32_t slots = min(*space.slots_taken, (uint32_t)WD_SLOTS), across = (uint32_t)((space.per_row + WD_SEGMENT - 1) / WD_SEGMENT);
+  const uint32_t slots = min(*space.slots_taken, space.slot_count), across = (uint32_t)((space.per_row + WD_SEGMENT - 1) / WD_SEGMENT);
   for (uint32_t item = blockIdx.x; item < slots * across; item += gridDim.x) {
     const Slot& slot = space.slots[item / across];
     const int64_t r = slot.row;
@@ -1010,13 +1018,13 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
   double mine = 0, all = 0;
   uint32_t token, last = WD_BINS, size = 0;
   if (state == LEFT && n <= SA_PARTS) {
-    uint32_t bar = NOTHING + 1, none[3] = {0, 0, 0};
+    uint32_t bar = NOTHING + 1, none = 0;
     for (int p = tid; p < n; p += RS_THREADS) bar = max(bar, parts[p].bar);
-    g.most(bar, none[0], none[1], none[2]);
+    g.most(bar, none);
     if (row.size <= SA_LIST) size = gather_row(g, row), bar = NOTHING + 1;
     else size = bar == ALL ? ALL : gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, bar);
-    if (size <= RS_THREADS) {
-      const Picked some = pick(g, size, l, w, bar == NOTHING + 1, l.by_weight && w(logit_of(bar)) < min_p, 0, whole);
+    if (size < RS_THREADS) {
+      const Picked some = pick(g, size, (uint32_t)l.top_k, l, w, bar, 0, whole);
       if (some.decided) {
         double before;
         const uint32_t thread = g.first(some.weight, [&](double sum, double total) { return sum > (double)l.uniform * total; }, before, all);
@@ -1024,8 +1032,9 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
         return;
       }
     } else if (size <= SA_LIST) {
-      const ListSource<T, RS_THREADS> listed(s, size, w);
-      Sampler<ListSource<T, RS_THREADS>, Group<RS_THREADS>> list{listed, w, g, s, order_of(most)};
+      weigh(g, size, w);
+      const ListSource<T> listed{s, size};
+      Sampler<ListSource<T>, Group<RS_THREADS>> list{listed, w, g, s, order_of(most)};
       double by_mass = !l.by_mass ? -1 : l.top_k ? (double)l.top_p : target;
       bool decided = true;
       if (bar > NOTHING + 1) {
@@ -1069,8 +1078,7 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
     if (state == LEFT)
       for (int p = g.wave; p < n; p += g.WAVES) part_above(row, space, r * space.per_row + p, p, w, last, min_p);
     __syncthreads();  // a workgroup sees what it has written itself
-    u64 longest = 0, none = 0;
-    if (tid < n) longest = parts[tid].count;
+    uint32_t longest = tid < n ? parts[tid].count : 0, none = 0;
     g.most(longest, none);
     again = longest > PT_LIST;  // too many tokens of the same depth
     if (!again) size = gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, 0);
@@ -1086,24 +1094,23 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
     if (tid < n) sum = parts[tid].kept;
     if (size) {
       const double above = g.sum(tid < n ? parts[tid].sum : 0.0);
-      if (size <= RS_THREADS) {
-        Limits by_mass = l;
-        by_mass.top_k = 0;
-        const Picked some = pick(g, size, by_mass, w, true, false, above, whole);
+      if (size < RS_THREADS) {
+        const Picked some = pick(g, size, 0, l, w, 0, above, whole);
         kept.least = (uint32_t)(some.last >> 32), kept.until = ~(uint32_t)some.last;
       } else {
-        const ListSource<T, RS_THREADS> in_bin(s, size, w);
-        u64 largest = 0, none = 0;
-        for (uint32_t i = tid; i < size; i += RS_THREADS) largest = max(largest, (u64)s.order[i]);
+        weigh(g, size, w);
+        const ListSource<T> in_bin{s, size};
+        uint32_t largest = 0, none = 0;
+        for (uint32_t i = tid; i < size; i += RS_THREADS) largest = max(largest, s.order[i]);
         g.most(largest, none);
-        Sampler<ListSource<T, RS_THREADS>, Group<RS_THREADS>> list{in_bin, w, g, s, (uint32_t)largest};
+        Sampler<ListSource<T>, Group<RS_THREADS>> list{in_bin, w, g, s, largest};
         kept = list.kept(l, __builtin_fmax(target - above, 0.0));
       }
       if (kept.until < size) until = s.id[kept.until];
       if (tid < n) {
         const uint32_t end = s.start[tid] + parts[tid].count;
 #pragma unroll 1
-        for (uint32_t k = s.start[tid]; k < end; ++k) sum += kept.of(s.order[k], [&] { return w(logit_of(s.order[k])); }, k);
+        for (uint32_t k = s.start[tid]; k < end; ++k) sum += kept.of(s.order[k], [&] { return s.weight[k]; }, k);
       }
     }
     const uint32_t p = g.first(sum, [&](double upto, double total) { return upto > (double)l.uniform * total; }, before, all);
@@ -1132,8 +1139,9 @@ Space space_of(int64_t rows, int64_t vocab, void* at) {
   s.size = part_steps(rows, vocab) * PT_STEP;
   s.per_row = std::max((vocab + s.size - 1) / s.size, (int64_t)1);
   const int64_t batch = std::min(rows, std::max(PT_BATCH / s.per_row, (int64_t)1)), parts = batch * s.per_row;
-  // Many workgroups go over a row again where that is three more launches to a call that is long anyway.
-  const bool wide = parts >= 2048 && s.per_row >= 16 && s.per_row <= SA_PARTS;
+  // Many workgroups go over a row again, as many rows as there are slots, where it is too long to be listed whole: the row of 50,256 that takes
+  // 55 us by one takes 25 so, with 5 for the launches where none is left.
+  const bool wide = vocab > SA_LIST && s.per_row <= SA_PARTS;
   s.slots_taken = static_cast<uint32_t*>(at);
   s.whole = reinterpret_cast<double*>(static_cast<char*>(at) + 16);
   s.parts = reinterpret_cast<Part*>(s.whole + batch);
@@ -1142,7 +1150,8 @@ Space space_of(int64_t rows, int64_t vocab, void* at) {
   s.bytes = 16 + batch * 8 + parts * (int64_t)(sizeof(Part) + PT_LIST * sizeof(Listed)) + (batch + 1) / 2 * 8;
   if (wide) {
     s.slots = reinterpret_cast<Slot*>(s.state + (batch + 1) / 2 * 2);
-    s.bytes += WD_SLOTS * (int64_t)sizeof(Slot);
+    s.slot_count = (uint32_t)std::min(batch, (int64_t)WD_SLOTS);
+    s.bytes += s.slot_count * (int64_t)sizeof(Slot);
   }
   return s;
 }
@@ -1166,7 +1175,7 @@ void enqueue_sample(const tt_sample_args& a, hipStream_t st) {
     hipLaunchKernelGGL(k_sample<T>, dim3((uint32_t)some.rows), dim3(DR_THREADS), 0, st, some, space);
     if (!a.top_k && !a.top_p && !a.min_p) continue;  // no row is left
     if (space.slots && (a.top_p || a.min_p)) {
-      const int64_t items = std::min(some.rows, (int64_t)WD_SLOTS) * ((space.per_row + WD_SEGMENT - 1) / WD_SEGMENT);
+      const int64_t items = std::min(some.rows, (int64_t)space.slot_count) * ((space.per_row + WD_SEGMENT - 1) / WD_SEGMENT);
       const dim3 grid((uint32_t)std::min(items, (int64_t)1024));
       hipLaunchKernelGGL(k_sample_bins<T>, grid, dim3(PT_THREADS), 0, st, some, space);
       hipLaunchKernelGGL(k_sample_above<T>, grid, dim3(PT_THREADS), 0, st, some, space);
