@@ -431,8 +431,8 @@ PyObject* attend_cache(PyObject*, PyObject* const* v, Py_ssize_t n) {
     a.scale = c.real(v[7]);
     a.window = c.number(v[8]);
     a.softcap = c.real(v[9]);
-    if (c.ok && (a.window < 0 || !(a.softcap >= 0 && a.softcap <= 1e30)))
-      c.fail("a window of 0 or more and a softcap from 0 to 1e30 are needed");
+    if (c.ok && (a.window < 0 || !(a.softcap == 0 || (a.softcap >= 1e-6 && a.softcap <= 1e20))))
+      c.fail("a window of 0 or more and a softcap of 0 or from 1e-6 to 1e20 are needed");
     a.lse = (float*)c.mat(v[12], "lse", ScalarType::Float, &a.lse_stride, a.queries, a.heads);
     if (!c.ok) return 0;
     const int64_t bytes = step.attend_workspace(a.queries, a.heads, a.cache.heads, a.cache.dim);

@@ -197,12 +197,13 @@ struct AttendSpace {
 AttendSpace attend_space(const AttendShape& s, int64_t queries, int64_t dim, void* at) {
   AttendSpace w{};
   if (!s.workers) return w;
-  const int64_t pieces = 2 * s.workers * s.lanes * s.rows;
+  const bool joined = s.workers > 1;  // one worker puts everything out at once
+  const int64_t pieces = joined ? 2 * s.workers * s.lanes * s.rows : 0, ends = joined ? queries * s.lanes : 0;
   w.piece = static_cast<float*>(at);
   w.statistic = w.piece + pieces * padded(dim);
   w.pieces = reinterpret_cast<int2*>(w.statistic + 2 * pieces);
-  w.start = reinterpret_cast<int64_t*>(w.pieces + queries * s.lanes);
-  w.bytes = pieces * (padded(dim) + 2) * 4 + queries * s.lanes * 8;
+  w.start = reinterpret_cast<int64_t*>(w.pieces + ends);
+  w.bytes = pieces * (padded(dim) + 2) * 4 + ends * 8;
   if (s.bundle > 1) {
     w.item = reinterpret_cast<Item*>(w.start + AT_QUERIES + 1);
     w.order = reinterpret_cast<int32_t*>(w.item + AT_QUERIES);
@@ -266,6 +267,12 @@ constexpr uint32_t ALL = 0xFFFFFFFFu;
 
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
 
+// 1 - 2 / (1 + e^2y), off by 2^-23 or so; below 1/4, where that would be many steps, the series up to y^9, whose next term is 2^-27 of it.
+__device__ inline float tanh_of(float y) {
+  const float p = y * y, near = y * fmaf(p, fmaf(p, fmaf(p, fmaf(p, 62.0f / 2835, -17.0f / 315), 2.0f / 15), -1.0f / 3), 1.0f);
+  return fabsf(y) < 0.25f ? near : 1.0f - 2.0f / (1.0f + __builtin_amdgcn_exp2f(y * (2 * LOG2E)));
+}
+
 // One workgroup: a lane's heads, for some tokens of a query after the other.
 template <class T, bool EIGHT, int D, bool WHOLE>
 struct Attend {
@@ -318,13 +325,9 @@ struct Attend {
       if (c < here && (WHOLE || d < dim)) query[k] = *reinterpret_cast<const typename Words<4>::type*>(row + d);
     }
     float before = (float)a.scale * (cache.key_scale ? cache.key_scale[head] : 1.0f), after = 0;
-    const bool capped = (float)a.softcap > 0;
-    if (capped) {  // tanh(y) = 1 - 2 / (1 + 2^(2 y log2 e))
-      before = before / (float)a.softcap * (2 * LOG2E);
-      after = (float)a.softcap * LOG2E;
-    } else {
-      before *= LOG2E;
-    }
+    const bool capped = a.softcap > 0;
+    if (capped) before /= (float)a.softcap, after = (float)a.softcap * LOG2E;
+    else before *= LOG2E;
 
     const int32_t* table = a.table + (int64_t)q.row * a.table_stride;
     const char* keys = static_cast<const char*>(cache.keys) + head * cache.key_head_stride * SIZE;
@@ -433,7 +436,7 @@ struct Attend {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           x[k] = score[k / 4][k % 4] * before;
-          if (capped) x[k] = (1.0f - 2.0f / (1.0f + __builtin_amdgcn_exp2f(x[k]))) * after;
+          if (capped) x[k] = tanh_of(x[k]) * after;
         }
         if (there != 0xFFFFFFFFu) {
 #pragma unroll
@@ -735,7 +738,7 @@ __global__ __launch_bounds__(AT_THREADS, D == 256 ? 1 : D == 64 ? 3 : 2) void k_
     const int slot = 2 * worker + (nth > 0);
     const bool whole = at == begin && stop == end;
     // the worker of its last unit: the first one whose share reaches the item's end
-    if (tid == 0 && at == begin) space.pieces[lo * shape.lanes + unit] = int2{slot, (int)((end * sharers + all - 1) / all) - worker};
+    if (tid == 0 && at == begin && shape.workers > 1) space.pieces[lo * shape.lanes + unit] = int2{slot, (int)((end * sharers + all - 1) / all) - worker};
     const Item q = shape.bundle > 1 ? space.item[lo] : Item{s_seen[lo].row, 1, 0, s_seen[lo].from, s_seen[lo].upto};
     work.run(lo, q, q.from + (uint32_t)(at - begin) * AT_UNIT, stop == end ? q.upto : q.from + (uint32_t)(stop - begin) * AT_UNIT,
              whole ? -1 : slot);

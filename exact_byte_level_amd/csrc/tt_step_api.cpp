@@ -52,7 +52,7 @@ int tt_attend_cache(const tt_attend_args* args, hipStream_t stream) {
   const int64_t bytes = tt_attend_workspace(a.queries, a.heads, a.cache.heads, a.cache.dim);
   if (bytes < 0) return (int)bytes;
   if ((a.type != TT_F16 && a.type != TT_BF16) || (a.cache.type != a.type && a.cache.type != TT_E4M3)) return TT_EINVAL;
-  if (a.table_rows < 0 || a.width < 0 || a.window < 0 || !(a.softcap >= 0 && a.softcap <= 1e30)) return TT_EINVAL;
+  if (a.table_rows < 0 || a.width < 0 || a.window < 0 || !(a.softcap == 0 || (a.softcap >= 1e-6 && a.softcap <= 1e20))) return TT_EINVAL;
   if (a.table_rows > MAX_INT32 || a.width > MAX_INT32 / a.cache.block_size) return TT_ETOOBIG;
   if (a.queries == 0) return TT_OK;
   if (!a.query || !a.out || !a.lengths || (!a.table && a.table_rows > 0 && a.width > 0)) return TT_EINVAL;

@@ -81,7 +81,7 @@ typedef struct tt_attend_args {
   const int32_t* lengths;    /* [queries] tokens that each query sees, from its request's first on; not above 0: none */
   const int32_t* rows;       /* [queries] row of the table that each goes by; NULL: row i.  No row of it: sees nothing */
   double scale;              /* of the scores */
-  double softcap;            /* 0 .. 1e30; above 0: scores x become softcap * tanh(x / softcap) */
+  double softcap;            /* 0, or 1e-6 .. 1e20: scores x become softcap * tanh(x / softcap) */
   int64_t window;            /* above 0: only the last `window` of the tokens are seen */
   void* workspace;           /* tt_attend_workspace bytes, at 16 bytes; may be NULL if that is 0 */
   int64_t workspace_bytes;
@@ -94,7 +94,9 @@ typedef struct tt_attend_args {
  *
  * Scores, weights and sums are held in 32 bits, out is rounded once.  A query that
  * sees nothing, or whose scores are all -infinity, gets zeros and -infinity; what the
- * cache holds elsewhere, NaN included, has no effect.  Values that are seen have to be finite: an infinite one gives an infinity or NaN.
+ * cache holds elsewhere, NaN included, has no effect.  Values that are seen have to be
+ * finite: an infinite one gives infinities or NaN, and, where there are more queries than
+ * rows, to every query of its row.
  * A query after tt_plan_blocks sees out_lengths[r] tokens of row r, or, of several new
  * tokens of a row, positions + 1 of row row_of; places without a token (-1) give zeros.
  * Made for single tokens and short runs of them: every query reads its tokens.

@@ -64,7 +64,7 @@ def attend(query, keys, values, table, lengths, rows=None, scale=1.0, window=0, 
             off = np.max(np.abs(k) @ np.abs(query[i, h])) * abs(by) * (dim + 8) * 2.0**-23
             if softcap:
                 x = softcap * np.tanh(x / softcap)
-                off += softcap * 2.0**-21
+                off += 2.0**-20 * np.abs(x).max()  # of a tanh from 1/4 up; below that less
             top = x.max()
             if top == -np.inf:
                 continue

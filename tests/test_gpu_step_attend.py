@@ -151,7 +151,7 @@ def test_windows(window):
     check(make([1500, 300], 4, 1, 128, 24, torch.float16, F8, seed=4), window=window)
 
 
-@pytest.mark.parametrize("softcap", [0.5, 30.0, 50.0, 1e30])
+@pytest.mark.parametrize("softcap", [1e-6, 0.5, 30.0, 50.0, 1e4, 1e20])
 def test_softcaps(softcap):
     check(make([1, 20, 600], 4, 2, 128, 16, seed=3, strength=8.0), softcap=softcap)
     check(make([600], 4, 2, 64, 16, torch.float16, F8, seed=3, strength=8.0), softcap=softcap, window=100)
@@ -293,7 +293,7 @@ def test_refuses():
     bad = [dict(query=o["query"].float()), dict(query=o["query"].half()), dict(query=o["query"][:, :3]), dict(query=o["query"][..., :32]), dict(out=out[:1]),
            dict(out=out.half()), dict(table=o["table"].long()), dict(table=o["table"][:1]), dict(lengths=o["lengths"][:1]), dict(lengths=o["lengths"].long()),
            dict(rows=torch.zeros(3, **i32)), dict(rows=torch.zeros(2, dtype=torch.int64, device="cuda")), dict(window=-1), dict(softcap=-0.5),
-           dict(softcap=math.nan), dict(softcap=math.inf), dict(key_scale=torch.ones(4, device="cuda")), dict(lse=torch.zeros(2, 3, device="cuda")),
+           dict(softcap=math.nan), dict(softcap=math.inf), dict(softcap=1e-7), dict(softcap=1e21), dict(key_scale=torch.ones(4, device="cuda")), dict(lse=torch.zeros(2, 3, device="cuda")),
            dict(lse=torch.zeros(2, 4, dtype=torch.float16, device="cuda")), dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
            dict(workspace=torch.empty(1 << 24, dtype=torch.uint8, device="cuda")[1:]), dict(workspace=torch.empty(1 << 24, dtype=torch.int8, device="cuda")),
            dict(key_cache=o["key_cache"][:1]), dict(value_cache=o["value_cache"].half()), dict(table=None), dict(lengths=None), dict(table=o["table"].cpu())]

@@ -65,7 +65,7 @@ ATTEND = dict(query=P, query_stride=1024, query_head_stride=128, out=2 * P, out_
     (dict(queries=-1), tt.TT_EINVAL), (dict(heads=1), tt.TT_EINVAL), (dict(heads=7), tt.TT_EINVAL), (dict(heads=0), tt.TT_EINVAL),
     (dict(type=0), tt.TT_EINVAL), (dict(type=3), tt.TT_EINVAL), (dict(type=1), tt.TT_EINVAL), (dict(query=0), tt.TT_EINVAL),
     (dict(out=0), tt.TT_EINVAL), (dict(lengths=0), tt.TT_EINVAL), (dict(table=0), tt.TT_EINVAL), (dict(table_rows=-1), tt.TT_EINVAL),
-    (dict(width=-1), tt.TT_EINVAL), (dict(window=-1), tt.TT_EINVAL), (dict(softcap=-1.0), tt.TT_EINVAL), (dict(softcap=float("nan")), tt.TT_EINVAL),
+    (dict(width=-1), tt.TT_EINVAL), (dict(window=-1), tt.TT_EINVAL), (dict(softcap=-1.0), tt.TT_EINVAL), (dict(softcap=float("nan")), tt.TT_EINVAL), (dict(softcap=1e-7), tt.TT_EINVAL), (dict(softcap=1e21), tt.TT_EINVAL),
     (dict(workspace=0), tt.TT_EINVAL), (dict(workspace=P + 8), tt.TT_EINVAL), (dict(workspace_bytes=1000), tt.TT_EINVAL),
     (dict(heads=4098), tt.TT_ETOOBIG), (dict(queries=1 << 31), tt.TT_ETOOBIG), (dict(queries=1 << 28), tt.TT_ETOOBIG),
     (dict(table_rows=1 << 31), tt.TT_ETOOBIG), (dict(width=1 << 27), tt.TT_ETOOBIG),
