@@ -1,5 +1,6 @@
 // tt_cache_kernels.hip -- keys and values of a paged cache: written, and
 // attended to (declared in include/tt_step.h).
+#include "tt_lanes.h"
 #include "tt_step_kernels.h"
 
 #include <algorithm>
@@ -8,7 +9,6 @@
 namespace tt {
 namespace {
 
-constexpr int WAVE = 64;
 constexpr int64_t MAX_ITEMS = 0xFFFFFFFF;  // threads that a launch may have in a dimension of its grid
 
 __host__ __device__ inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -569,23 +569,11 @@ struct Attend {
 // Units that an item's tokens take; one that sees nothing has one too, to put out its zeros.
 __device__ inline int64_t units_of(uint32_t from, uint32_t upto) { return max((upto - from + AT_UNIT - 1) / AT_UNIT, 1u); }
 
-// Inclusive sums over a wavefront: shifts by 1, 2, 4, 8 in rows of 16, then the last lanes of rows 0 and 2, then of row 1.
-template <int CTRL, int ROWS>
-__device__ inline int64_t plus_lanes(int64_t v) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xf, false);
-  return v + (int64_t)((uint64_t)hi << 32 | lo);
-}
-__device__ inline int64_t wave_sums(int64_t v) {
-  v = plus_lanes<0x118, 0xf>(plus_lanes<0x114, 0xf>(plus_lanes<0x112, 0xf>(plus_lanes<0x111, 0xf>(v))));
-  return plus_lanes<0x143, 0xc>(plus_lanes<0x142, 0xa>(v));
-}
-
 // Sums over the workgroup, with the sum of all.
 template <int N>
 __device__ inline int64_t group_sums(int64_t v, int64_t* of_wave, int64_t& all) {
   const int lane = threadIdx.x % WAVE, wave = threadIdx.x / WAVE;
-  int64_t upto = wave_sums(v);
+  int64_t upto = (int64_t)sums_upto((u64)v);
   __syncthreads();
   if (lane == WAVE - 1) of_wave[wave] = upto;
   __syncthreads();
@@ -604,35 +592,30 @@ constexpr int BU_THREADS = AT_QUERIES;
 // no bundle reads more tokens than its queries do one by one.  By one workgroup, a query a thread.  301 queries of 40 rows
 // that see 1,024 tokens of 12 heads each take 133 us one by one.
 __global__ __launch_bounds__(BU_THREADS) void k_bundle(tt_attend_args a, AttendShape shape, AttendSpace space) {
-  __shared__ uint64_t s_key[BU_THREADS];
+  __shared__ u64 s_key[BU_THREADS];
   __shared__ int64_t s_wave[BU_THREADS / WAVE];
   __shared__ int32_t s_first[BU_THREADS + 1];
   __shared__ Seen s_seen[BU_THREADS];
-  const int tid = threadIdx.x, lane = tid % WAVE, wave = tid / WAVE, n = (int)a.queries;
-  uint64_t key = ~(uint64_t)0;
+  const int tid = threadIdx.x, n = (int)a.queries;
+  u64 key = 0;  // the largest first, so inverted
   if (tid < n) {
     s_seen[tid] = seen(a, tid);
     // rows are fewer than queries, so below 2^9
-    key = ((uint64_t)s_seen[tid].row << 32 | s_seen[tid].upto) << 9 | (uint64_t)tid;
+    key = ~(((u64)s_seen[tid].row << 32 | s_seen[tid].upto) << 9 | (u64)tid);
   }
-  // bitonic: exchanges between threads whose numbers differ in one bit
 #pragma unroll 1
   for (int run = 2; run / 2 < n; run *= 2) {
 #pragma unroll 1
-    for (int apart = run / 2; apart; apart /= 2) {
-      uint64_t other;
-      if (apart < WAVE) {
-        other = (uint64_t)__shfl_xor((unsigned long long)key, apart);
-      } else {
-        __syncthreads();
-        s_key[tid] = key;
-        __syncthreads();
-        other = s_key[tid ^ apart];
-      }
-      const bool smaller = !(tid & apart) == !(tid & run);
-      key = smaller == (other < key) ? other : key;
+    for (int apart = run / 2; apart >= WAVE; apart /= 2) {
+      __syncthreads();
+      s_key[tid] = key;
+      __syncthreads();
+      const u64 other = s_key[tid ^ apart];
+      key = (!(tid & apart) == !(tid & run)) == (other > key) ? other : key;
     }
+    key = exchanged_in_wave(key, tid, run);
   }
+  key = ~key;
   __syncthreads();
   s_key[tid] = key;
   __syncthreads();
@@ -672,7 +655,6 @@ __global__ __launch_bounds__(BU_THREADS) void k_bundle(tt_attend_args a, AttendS
   const int64_t upto = group_sums<BU_THREADS>(units, s_wave, sum);
   space.start[tid] = upto - units;  // past the last item: all units
   if (tid == 0) space.start[BU_THREADS] = sum;
-  (void)lane, (void)wave;
 }
 
 // Workgroups of the same lane share out the units of all items evenly, so that short and long requests do not wait for
