@@ -258,6 +258,13 @@ __device__ inline float one_of(uint32_t w, int k) {
   return (float)__builtin_bit_cast(pair, w)[k];
 }
 
+// 1 for each element of a word that is infinite or NaN: those whose exponent is all ones carry into the bit above; of e4m3 all ones but the sign.
+template <class T, bool EIGHT>
+__device__ inline uint32_t not_finite(uint32_t w) {
+  if constexpr (EIGHT) return ((w & 0x7F7F7F7Fu) + 0x01010101u) >> 7 & 0x01010101u;
+  else return ((w & 0x7FFF7FFFu) + (std::is_same<T, _Float16>::value ? 0x04000400u : 0x00800080u)) >> 15 & 0x00010001u;
+}
+
 __device__ inline float over_groups(float x, bool sum) {
   const float y = __shfl_xor(x, 16), z = sum ? x + y : fmaxf(x, y), u = __shfl_xor(z, 32);
   return sum ? z + u : fmaxf(z, u);
@@ -399,6 +406,21 @@ struct Attend {
       }
     };
 
+    // Columns j and j + 1 of the lane's values, each word of them as `f` has it, for a product over its eight tokens.
+    auto columns = [&](int j, auto f, u32x4& even, u32x4& odd) {
+      uint32_t pair[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (EIGHT) pair[k] = j % 4 ? widened<T, true>(f(value[k][j / 4])) : widened<T, false>(f(value[k][j / 4]));
+        else pair[k] = f(value[k][j / 2]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        even[k] = __builtin_amdgcn_perm(pair[2 * k + 1], pair[2 * k], 0x05040100);
+        odd[k] = __builtin_amdgcn_perm(pair[2 * k + 1], pair[2 * k], 0x07060302);
+      }
+    };
+
     f32x4 out[MINE];
 #pragma unroll
     for (int j = 0; j < MINE; ++j) out[j] = 0;
@@ -415,6 +437,7 @@ struct Attend {
     while (base < end) {
       const uint32_t there_next = addresses(entry, base + AT_UNIT);
       entry = entry_of(base + 2 * AT_UNIT);
+      const bool edge = __any(base < all_from || base + AT_TILE > all_upto);  // some queries of a bundle do not see all of the tile
       float x[8];
       {
         f32x4 score[2];
@@ -447,11 +470,42 @@ struct Attend {
               for (int w = 0; w < VWORDS; ++w) value[k][w] = 0;  // a weight of zero does not take out NaN
             }
         }
-        if (base < all_from || base + AT_TILE > all_upto) {
+        if (edge) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const uint32_t t = base + k / 4 * 16 + g * 4 + k % 4;
             if (t < own_from || t >= own_upto) x[k] = -__builtin_inff();
+          }
+          // Infinities and NaN among the values must not reach queries that do not see them, and would by their weights of
+          // zero: a product of ones tells which outputs see some, and they are taken out.
+          uint32_t some = 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+#pragma unroll
+            for (int w = 0; w < VWORDS; ++w) some |= not_finite<T, EIGHT>(value[k][w]);
+          if (__any(some != 0)) {
+            u32x4 seeing;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t t = base + k / 2 * 16 + g * 4 + k % 2 * 2;
+              seeing[k] = two<T>(t >= own_from && t < own_upto ? 1.0f : 0.0f, t + 1 >= own_from && t + 1 < own_upto ? 1.0f : 0.0f);
+            }
+            const uint32_t one = EIGHT ? 0x38 : two<T>(1.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < MINE; j += 2) {
+              u32x4 even, odd;
+              columns(j, [&](uint32_t w) { return not_finite<T, EIGHT>(w) * one; }, even, odd);
+              const f32x4 low = product<T>(even, seeing, f32x4{0, 0, 0, 0}), high = product<T>(odd, seeing, f32x4{0, 0, 0, 0});
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                out[j][r] = low[r] > 0 ? __builtin_nanf("") : out[j][r];
+                out[j + 1][r] = high[r] > 0 ? __builtin_nanf("") : out[j + 1][r];
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+              for (int w = 0; w < VWORDS; ++w) value[k][w] &= ~(not_finite<T, EIGHT>(value[k][w]) * (EIGHT ? 0xFFu : 0xFFFFu));
           }
         }
       }
@@ -487,18 +541,8 @@ struct Attend {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < MINE; j += 2) {
-          uint32_t pair[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if constexpr (EIGHT) pair[k] = j % 4 ? widened<T, true>(value[k][j / 4]) : widened<T, false>(value[k][j / 4]);
-            else pair[k] = value[k][j / 2];
-          }
           u32x4 even, odd;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            even[k] = __builtin_amdgcn_perm(pair[2 * k + 1], pair[2 * k], 0x05040100);
-            odd[k] = __builtin_amdgcn_perm(pair[2 * k + 1], pair[2 * k], 0x07060302);
-          }
+          columns(j, [](uint32_t w) { return w; }, even, odd);
           out[j] = product<T>(even, weight, out[j]);
           out[j] = product<T>(even, rest, out[j]);
           out[j + 1] = product<T>(odd, weight, out[j + 1]);

@@ -94,9 +94,8 @@ typedef struct tt_attend_args {
  *
  * Scores, weights and sums are held in 32 bits, out is rounded once.  A query that
  * sees nothing, or whose scores are all -infinity, gets zeros and -infinity; what the
- * cache holds elsewhere, NaN included, has no effect.  Values that are seen have to be
- * finite: an infinite one gives infinities or NaN, and, where there are more queries than
- * rows, to every query of its row.
+ * cache holds elsewhere, NaN included, has no effect.  Values that are seen are
+ * meant to be finite: an infinite one gives infinities or NaN to the queries that see it.
  * A query after tt_plan_blocks sees out_lengths[r] tokens of row r, or, of several new
  * tokens of a row, positions + 1 of row row_of; places without a token (-1) give zeros.
  * Made for single tokens and short runs of them: every query reads its tokens.

@@ -226,6 +226,31 @@ def test_nan_that_is_seen_comes_out():
     assert torch.isnan(out[1]).all() and torch.isfinite(out[0]).all()
 
 
+@pytest.mark.parametrize("src, dst", TYPES)
+@pytest.mark.parametrize("heads, kv, dim", [(2, 2, 64), (4, 2, 40), (8, 1, 128), (3, 1, 136), (2, 1, 256)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_values_that_are_not_finite_reach_only_who_sees_them(src, dst, heads, kv, dim, window):
+    """Queries of one row that see more and more of it: an infinity or NaN among its values goes into the outputs of those that
+    see it, at its elements, and into no other."""
+    lengths = [300, 60, 90, 91, 89, 130, 61, 92, 10, 299, 93, 40]
+    o = make(lengths, heads, kv, dim, 16, src, dst, rows=[0] * 9 + [1] * 3, seed=dim, garbage=0.5)
+    infinity = math.nan if dst == F8 else math.inf
+    for row, place, head, d, bad in ((0, 90, 0, 7, math.nan), (0, 60, kv - 1, dim - 1, infinity), (0, 9, 0, 0, -infinity), (1, 39, 0, 1, math.nan), (1, 92, 0, 2, infinity), (0, 299, 0, 3, math.nan)):
+        o["value_cache"].view(torch.uint8 if dst == F8 else torch.int16)[o["table"][row, place // 16], place % 16, head, d] = \
+            torch.tensor([bad], device="cuda").to(dst).view(torch.uint8 if dst == F8 else torch.int16)[0]
+    plain = {k: (v.cpu().numpy() if isinstance(v, torch.Tensor) else v) for k, v in o.items() if k not in ("query", "key_cache", "value_cache")}
+    with np.errstate(invalid="ignore"):
+        want, sums, slack, sums_slack = so.attend(host(o["query"]), host(o["key_cache"]), host(o["value_cache"]), scale=1 / math.sqrt(dim), window=window, **plain)
+    fine = np.isfinite(want)
+    assert not fine.all() and fine.mean() > 0.9
+    got, lse = tt.attend_cache(**o, lse=True, window=window)
+    near_sums(lse, sums, sums_slack)
+    g = host(got)
+    assert np.array_equal(np.isfinite(g), fine)
+    room = 1.02 * slack + torch.finfo(src).eps / 2 * (np.abs(want) + slack) + TINY[src] / 2
+    assert (np.abs(g[fine] - want[fine]) <= room[fine]).all()
+
+
 def test_strides_and_alignment():
     """Queries out of a wider projection, an output with gaps, caches that are parts of one tensor, at odd addresses."""
     for src, dst in TYPES:
