@@ -129,7 +129,10 @@ struct Eight {
   typedef T type __attribute__((ext_vector_type(8), aligned(alignof(T))));
 };
 
-// Q * 512 tokens a part.  256 x 262,144 float32 with limits take 56 us.
+// Q * 512 tokens a part, each read once.  By a wavefront alone: parts need nothing of each other, and with all of them in flight the
+// loads of one hide behind the weights of another.  What bounds it are these: a weight and its sum are 16 operations in 64 bits, at
+// a bit more than half the rate of those in 32.  192 x 100,256 bfloat16 without limits take 21 us, of which reading is 7
+// (38.5 MB at 5.6 TB/s); 256 x 262,144 float32 with limits 64, of which reading is 48.
 template <class T, int Q>
 __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, Space space) {
   constexpr int MINE = Q * 8;
@@ -241,7 +244,7 @@ struct SampleShared {
   uint32_t order[SA_LIST], id[SA_LIST];
   uint32_t start[SA_PARTS];
   u64 digit[SA_BINS];
-  u64 of_wave[2][RS_THREADS / WAVE];
+  u64 of_wave[RS_THREADS / WAVE];
   u64 above, of;
   uint32_t found, last, place;
 };
@@ -268,9 +271,9 @@ struct Group {
     upto = sums_upto(x);
     before = from_lanes<0x138, 0xf>(upto);  // of the lane before
     __syncthreads();
-    if (lane == WAVE - 1) s.of_wave[0][wave] = bits(upto);
+    if (lane == WAVE - 1) s.of_wave[wave] = bits(upto);
     __syncthreads();
-    V total = lane < WAVES ? value<V>(s.of_wave[0][lane]) : 0;  // of the wavefronts up to the lane's
+    V total = lane < WAVES ? value<V>(s.of_wave[lane]) : 0;  // of the wavefronts up to the lane's
     total += from_lanes<0x111, 0xf>(total);
     total += from_lanes<0x112, 0xf>(total);
     total += from_lanes<0x114, 0xf>(total);
@@ -288,9 +291,9 @@ struct Group {
   __device__ __forceinline__ void most(uint32_t& x, uint32_t& y) {
     x = max_of_lanes(x), y = max_of_lanes(y);
     __syncthreads();
-    if (lane == 0) s.of_wave[0][wave] = (u64)x << 32 | y;
+    if (lane == 0) s.of_wave[wave] = (u64)x << 32 | y;
     __syncthreads();
-    const u64 v = lane < WAVES ? s.of_wave[0][lane] : 0;
+    const u64 v = lane < WAVES ? s.of_wave[lane] : 0;
     x = max_of_lanes((uint32_t)(v >> 32)), y = max_of_lanes((uint32_t)v);
   }
 
@@ -934,7 +937,8 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
   const double whole = space.whole[r], target = (double)l.top_p * whole, min_p = l.by_weight ? (double)l.min_p : 0.0;
   double mine = 0, all = 0;
   uint32_t token, last = WD_BINS, size = 0;
-  if (state == LEFT && n <= SA_PARTS) {
+  // of rows that slots are for, those that found none go the same way as the others: which ones these are must not change a sum
+  if (state == LEFT && n <= SA_PARTS && (l.top_k || !space.slots)) {
     uint32_t bar = NOTHING + 1, none = 0;
     for (int p = tid; p < n; p += RS_THREADS) bar = max(bar, parts[p].bar);
     g.most(bar, none);
@@ -990,7 +994,7 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
       } else {
         bins = space.slots[state].mass;
       }
-      last = last_bin<WD_BINS / RS_THREADS>(bins, target * one, s.of_wave[0], &s.found);
+      last = last_bin<WD_BINS / RS_THREADS>(bins, target * one, s.of_wave, &s.found);
     }
     if (state == LEFT)
       for (int p = g.wave; p < n; p += g.WAVES) part_above(row, space, r * space.per_row + p, p, w, last, min_p);
