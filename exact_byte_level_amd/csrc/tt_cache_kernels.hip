@@ -108,7 +108,10 @@ __device__ inline void put_eight(typename Eight<I>::type x, const float* scale, 
   }
 }
 
-// Each thread moves eight keys and the eight values beside them, of `total` of the tokens from `first` on.
+// Each thread moves eight keys and the eight values beside them, of `total` of the tokens from `first` on: both loads are on their way
+// before the slot is known to be there.  Eight elements are 16 bytes of bfloat16, and of 8 bits what one lane can store at once.
+// Bound by memory: 48,000 tokens of 8 heads of 128 elements, bfloat16 to e4m3, take 60 us for 292 MB (4.9 TB/s, what a
+// large copy reaches; with divisions in place of the corrected products 69); 8 tokens 2.7 us, the launch and two dependent reads.
 template <class I, class O>
 __global__ __launch_bounds__(WR_THREADS) void k_write(tt_write_args a, Division by_token, Division by_head, Division by_block, int64_t first, uint32_t total) {
   const uint32_t at = blockIdx.x * WR_THREADS + threadIdx.x;
@@ -141,7 +144,18 @@ __global__ __launch_bounds__(WR_THREADS) void k_write(tt_write_args a, Division 
 //            of, 4 g + r of two tiles of 16: the weights need no exchange.  Lane (c, g) loads the same d of its eight
 //            tokens, D / 16 of them from c * D / 16 on, and product j takes every j-th: one byte permutation per pair.
 //
-// Keys and values so go from memory to registers without LDS, each read once.
+// Keys and values so go from memory to registers without LDS, each read once.  With sixteen rows of a product for the heads that
+// share a head of keys, most of which stand empty for few of them, the products are never what bounds it.
+//
+// Each wavefront has one tile's keys and values in registers and the next one's loads on their way while it computes.  Two or three wavefronts a
+// SIMD then keep 30 KB and more of a CU in flight.  What it measured:
+//   64 requests of up to 32,000 tokens, 64 heads on 8 of 128 elements, bfloat16   893 us for 5.13 GB: 5.7 TB/s, memory
+//   33 requests of up to 8,000, 16 heads on 4 of 256                              126 us for 663 MB: 5.3 TB/s, memory
+//   9 requests of up to 9,000, 28 heads on 4 of 128                               26.7 us for 104 MB: a third is the way to the first tile
+//   one request of 4,000, 32 heads on 8 of 128                                    10.5 us: that way alone, a tile or two a wavefront
+//   2 requests of 400,001, 16 heads on one of 128, e4m3                           46.8 us for 205 MB: 4.4 TB/s, widening to 16 bits and
+//     permutations beside the loads; three wavefronts a SIMD (49-54 us) and tiles of 64 tokens (52) were slower
+//   301 queries of 40 rows, 12 heads of 64, a window of 1,024, capped             39.7 us for 165 MB, in bundles
 
 constexpr int AT_THREADS = 256;
 constexpr int AT_WAVES = AT_THREADS / WAVE;
@@ -161,8 +175,10 @@ struct AttendShape {
 };
 
 // Tokens are dealt out where a workgroup for each query would not fill the card a few times over: 256 CUs take three workgroups each
-// of heads of up to 64 elements, two of 128, one of 256.  Where there are more queries than rows, some go by the
-// same row, and those that a product has room for are attended to together.
+// of heads of up to 64 elements, two of 128, one of 256 (that is what their registers leave room for).  On 8 heads of keys of 128
+// elements 64 requests of 2,000 to 32,000 tokens take 905 us dealt out and 1,121 by a workgroup each, which wait for the longest;
+// 256 of 300 to 4,000 tokens 477 and 488; 500 of up to 2,000 482 and 470.
+// Where there are more queries than rows, some go by the same row, and those that a product has room for are attended to together.
 AttendShape attend_shape(int64_t queries, int64_t heads, int64_t cache_heads, int64_t dim, int64_t table_rows, bool by_rows) {
   AttendShape s;
   s.group = (int)(heads / cache_heads);
@@ -170,7 +186,7 @@ AttendShape attend_shape(int64_t queries, int64_t heads, int64_t cache_heads, in
   s.lanes = cache_heads * s.parts;
   const int groups = padded(dim) == 256 ? 256 : padded(dim) == 64 ? 768 : 512;
   const bool shared = by_rows && queries > table_rows && queries <= AT_QUERIES && s.group <= AT_HEADS / 2;
-  const bool deal = shared || (queries <= AT_QUERIES && queries * s.lanes < 4096);
+  const bool deal = shared || (queries <= AT_QUERIES && queries * s.lanes <= 2048);
   s.workers = deal ? (int)std::max((int64_t)1, groups / s.lanes) : 0;
   s.bundle = shared ? AT_HEADS / s.group : 1;
   s.rows = std::min(s.group, AT_HEADS) * s.bundle;
@@ -633,8 +649,9 @@ __device__ inline int64_t group_sums(int64_t v, int64_t* of_wave, int64_t& all) 
 constexpr int BU_THREADS = AT_QUERIES;
 
 // Puts the queries of a call in the order of rows and, within a row, of their last tokens, and those of a row that see some of the same tokens into bundles: so
-// no bundle reads more tokens than its queries do one by one.  By one workgroup, a query a thread.  301 queries of 40 rows
-// that see 1,024 tokens of 12 heads each take 133 us one by one.
+// no bundle reads more tokens than its queries do one by one.  By one workgroup, a query a thread, which is why a call may have at
+// most as many.  A chain of 45 exchanges and three sums: 7.2 us for 301 queries of 40 rows.  Those, which see 1,024 tokens of 12
+// heads each, are attended to in 40 us after it, one by one in 133.
 __global__ __launch_bounds__(BU_THREADS) void k_bundle(tt_attend_args a, AttendShape shape, AttendSpace space) {
   __shared__ u64 s_key[BU_THREADS];
   __shared__ int64_t s_wave[BU_THREADS / WAVE];
@@ -702,7 +719,8 @@ __global__ __launch_bounds__(BU_THREADS) void k_bundle(tt_attend_args a, AttendS
 }
 
 // Workgroups of the same lane share out the units of all items evenly, so that short and long requests do not wait for
-// each other; where the cut goes through an item its pieces are joined by k_join.
+// each other; where the cut goes through an item its pieces are joined by k_join.  As many workgroups as the card holds at once: each
+// sums up the items by itself, which costs it less than a launch that does so would.
 template <class T, bool EIGHT, int D, bool WHOLE>
 __global__ __launch_bounds__(AT_THREADS, D == 256 ? 1 : D == 64 ? 3 : 2) void k_attend(tt_attend_args a, AttendShape shape, AttendSpace space,
                                                                                    Division by_block, int64_t first) {
@@ -772,8 +790,9 @@ __global__ __launch_bounds__(AT_THREADS, D == 256 ? 1 : D == 64 ? 3 : 2) void k_
   }
 }
 
-// The pieces of a query head together: the first one, and the first one of each worker after its own.  ACROSS threads go by the
-// elements, four each, of SPLIT workgroups a head; the others by the pieces, each with a maximum of its own.
+// The pieces of a query head together: the first one, and the first one of each worker after its own.  `across` threads go by the
+// elements, four each, of `split` workgroups a head; the others by the pieces, each with a maximum of its own.  Bound by the launch and two
+// dependent reads: 4.5-4.9 us for a few heads, 6 for 32 heads of up to 256 pieces, 9 for 4,096 heads.
 template <class T>
 __global__ __launch_bounds__(AT_THREADS) void k_join(tt_attend_args a, AttendShape shape, AttendSpace space, int wide, int split) {
   __shared__ f32x4 s_out[AT_THREADS];

@@ -94,7 +94,7 @@ constexpr int PT_THREADS = 256;
 constexpr int64_t PT_BATCH = 65536;  // parts of a launch
 constexpr int WD_SLOTS = 256;        // most rows of a launch that are gone over again by many workgroups
 constexpr int WD_BINS = 2048;
-constexpr int WD_SEGMENT = 8;        // parts of a workgroup
+constexpr int WD_SEGMENT = 4;        // parts of a workgroup: 256 x 262,144 take 124 us, with 8 or 2 131; 61 x 100,257 60, with 8 68
 
 struct Part {
   double sum;
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, S
 // -------------------------------------------------------------- a workgroup
 //
 // The draw from the lists is a chain of sums over a workgroup with little to do in between, which eight wavefronts get through
-// sooner than sixteen; going over a row again takes sixteen.
+// sooner than sixteen (one row of 50,256 23.5 us instead of 25.8); going over a row again takes sixteen.
 
 constexpr int DR_THREADS = 512;
 constexpr int RS_THREADS = 1024;
@@ -704,7 +704,8 @@ __device__ __forceinline__ Picked pick(Threads& g, uint32_t size, uint32_t top_k
 
 // A row by a workgroup, from its parts.  Without limits the part that the random number falls into is read again; with limits
 // the tokens above all high bars, if they are few, are sorted, which answers everything that is asked of them; if the last one kept is not
-// among them the row is left to be gone over again.
+// among them the row is left to be gone over again.  Bound by its chain of dependent steps: the bars, the lists, 45 exchanges, three
+// sums, 13 us for a row of 50,256, 15 for 256 rows of 262,144 at once; the radix selection that it took the place of was 40.
 template <class T>
 __global__ __launch_bounds__(DR_THREADS) void k_sample(tt_sample_args a, Space space) {
   __shared__ SampleShared s;
@@ -876,7 +877,8 @@ __device__ __forceinline__ uint32_t last_bin(const u64* bin, double target, u64*
   return min(last, (uint32_t)WD_BINS - 1);
 }
 
-// The rows in slots: the bins of their weights.
+// The rows in slots: the bins of their weights.  Each segment is summed up in LDS first.  Bound by the weights and by LDS atomics, 64 bits
+// each; for a third of 256 rows of 262,144 tokens 14 us, which come from the larger cache in good part.
 template <class T>
 __global__ __launch_bounds__(PT_THREADS) void k_sample_bins(tt_sample_args a, Space space) {
   __shared__ u64 s_bin[WD_BINS];
@@ -920,7 +922,9 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_above(tt_sample_args a, S
 }
 
 // The tokens of rows that are left, or whose parts know what is above their last bin: the bin's tokens are put in order, the part
-// is found, and the token in it.
+// is found, and the token in it.  A workgroup a row, since what each needs is little: a row whose bin is known takes 10 to 20 us, one
+// whose top_k is beyond its lists, or that has more tokens of one logit than these hold, several passes over it, 300 to
+// 500 us of 262,144.
 template <class T>
 __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Space space) {
   __shared__ SampleShared s;
@@ -1048,11 +1052,13 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
   if (tid == 0) put_token(a, r, token, mine, all);
 }
 
-// Parts of 2,048 tokens, which keep the card busy with a wavefront each and their lists short; where that would leave most of it
-// idle, of 512 or 1,024 as long as a row has at most 128.
+// Steps of 512 tokens that a part has.  Calls of 2^23 logits and more fill the card with parts of 2,048, whose lists are few.  Below that
+// smaller ones leave each wavefront less to do, as long as a row has at most 128 of them (more lists than that take longer to
+// put together): of 1,024 tokens for 61 x 100,257 float16 with all limits 54 us instead of 60, for 60 x 60,000 without any 12.2 instead
+// of 13.9; below 2^20 logits of 512 for one row of 50,256 23.5 instead of 33.
 uint32_t part_steps(int64_t rows, int64_t vocab) {
-  if (rows * vocab >= (int64_t)1 << 20) return 4;
-  return vocab <= 128 * PT_STEP ? 1 : vocab <= 256 * PT_STEP ? 2 : 4;
+  if (rows * vocab >= (int64_t)1 << 23 || vocab > 256 * PT_STEP) return 4;
+  return rows * vocab < (int64_t)1 << 20 && vocab <= 128 * PT_STEP ? 1 : 2;
 }
 
 Space space_of(int64_t rows, int64_t vocab, void* at) {

@@ -218,6 +218,22 @@ def test_the_same_twice():
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+def test_more_rows_gone_over_again_than_slots():
+    """Flat rows, whose nuclei are far below the lists: which of them find a slot depends on the order of workgroups, the answers do not."""
+    g = torch.Generator("cuda").manual_seed(9)
+    logits = torch.randn(700, 6000, device="cuda", generator=g).mul_(0.3)
+    u = torch.rand(700, device="cuda", generator=g)
+    o = dict(top_p=torch.full((700,), 0.9, device="cuda"))
+    check(logits[:40], u[:40].cpu().numpy(), top_p=np.full(40, 0.9, np.float32))
+    first = tt.sample_tokens(logits, u, logprobs=True, **o)
+    single = [tt.sample_tokens(logits[i:i + 100], u[i:i + 100], logprobs=True, top_p=o["top_p"][:100]) for i in range(0, 700, 100)]
+    shares = torch.cat([s[1] for s in single])
+    assert torch.equal(first[0], torch.cat([s[0] for s in single])) and ((first[1] - shares).abs() <= 2.0**-23 * shares.abs()).all()
+    for _ in range(5):
+        again = tt.sample_tokens(logits, u, logprobs=True, **o)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 def test_refuses():
     x, u, tokens = torch.zeros(3, 50, device="cuda"), torch.zeros(3, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
     bad = [dict(logits=x.double()), dict(logits=x.int()), dict(logits=x[0]), dict(logits=x.t()), dict(uniform=u[:2]), dict(uniform=u.double()), dict(uniform=u.cpu()),

@@ -56,7 +56,7 @@ CASES = [
     write(1), write(1 << 24), write((1 << 31) - 1, 1, 8), write(100_000, 4096, 256, 3, 0), write(5, 3, 24, 1, 1),
     attend(1, 1, 1), attend(1, 4096, 4096), attend(1, 4096, 1, 256), attend(512, 64, 8), attend(513, 64, 8), attend(511, 8, 1, 64), attend((1 << 31) - 1, 1, 1, 8),
     attend((1 << 19) - 1, 4096, 4096, 64), attend(1 << 19, 4095, 1, 256, 3), attend(301, 12, 12, 64, 1 + 1, True, 40), attend(512, 8, 1, 128, 3, True, 1),
-    attend(512, 17, 1, 128, 2, True, 1), attend(300, 4096, 4096, 64, 2, True, 4), attend(3, 8, 8, 8, 3, False, None, 1 << 20),
+    attend(512, 17, 1, 128, 2, True, 1), attend(256, 32, 8), attend(257, 32, 8), attend(513, 1, 1), attend(300, 4096, 4096, 64, 2, True, 4), attend(3, 8, 8, 8, 3, False, None, 1 << 20),
     sample(1, 1), sample(1 << 24, 1), sample(1 << 24, 2048), sample(1 << 11, 1 << 24), sample(1, 1 << 24, 2), sample(256, 262_144, 0), sample(256, 262_144, 1, False),
     sample(65_537, 512), sample(3, 524_289), sample(4096, 524_288), sample(5, 0)]
 
@@ -93,6 +93,8 @@ def test_how_calls_are_cut_up(results):
     assert groups(results, attend(512, 64, 8)) == [512 * 8]
     assert groups(results, attend(513, 64, 8)) == [513 * 8]
     assert groups(results, attend(511, 8, 1, 64))[0] == 768
+    assert groups(results, attend(256, 32, 8)) == [512, 256 * 32] and groups(results, attend(257, 32, 8)) == [257 * 8]
+    assert groups(results, attend(513, 1, 1)) == [513]
     assert groups(results, attend(301, 12, 12, 64, 2, True, 40)) == [1, 768, 301 * 12]
     assert len(groups(results, attend(512, 17, 1, 128, 2, True, 1))) == 2  # too many heads for two queries of a row in a product
     # without limits two launches, with them three, and two more where there is much to go over again
