@@ -79,7 +79,7 @@ def attend_cache_into(query, key_cache, value_cache, table, lengths, out, rows=N
     i; ``out`` is like the query.
 
     ``scale``: of the scores, by default ``1 / sqrt(dim)``; ``window``: above 0, only the last so many tokens are seen;
-    ``softcap``: above 0, scores are capped by a tanh; ``key_scale``, ``value_scale``: what write_cache_into divided by; ``lse``
+    ``softcap``: 0, or 1e-6 .. 1e20, by which scores are capped through a tanh; ``key_scale``, ``value_scale``: what write_cache_into divided by; ``lse``
     (float32 [N, heads]): receives the logarithm of each sum of weights.  ``workspace``: from attend_workspace; without it
     one is made."""
     bind = _bind or _start()
