@@ -66,6 +66,8 @@ struct Limits {
   int64_t top_k;                    // 0: none
   bool single, by_mass, by_weight;  // the first token alone; top_p limits; min_p limits
   __device__ __forceinline__ bool limited() const { return top_k || by_mass || by_weight; }
+  // The weight of the whole row is asked for: the nucleus is a share of it, or the draw goes by it.  After top_k it is a share of what that leaves.
+  __device__ __forceinline__ bool summed() const { return !single && !top_k && (by_mass || !by_weight); }
 };
 __device__ inline Limits limits_of(const tt_sample_args& a, int64_t r) {
   Limits l;
@@ -166,16 +168,18 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, S
   const uint32_t top = max_of_lanes(own);
   Part part{0, 0, logit_of(top), NOTHING + 1, 0, NOTHING + 1};
   if (top > NOTHING && !limits.single) {
-    const Weigher w(part.most, limits.temperature);
-    double sum = 0;
-    if (w.clear()) {
+    if (limits.summed()) {
+      const Weigher w(part.most, limits.temperature);
+      double sum = 0;
+      if (w.clear()) {
 #pragma unroll
-      for (int i = 0; i < MINE; ++i) sum += w.roughly(x[i]);
-    } else {
+        for (int i = 0; i < MINE; ++i) sum += w.roughly(x[i]);
+      } else {
 #pragma unroll
-      for (int i = 0; i < MINE; ++i) sum += w(x[i]);
+        for (int i = 0; i < MINE; ++i) sum += w(x[i]);
+      }
+      part.sum = sum_of_lanes(sum);
     }
-    part.sum = sum_of_lanes(sum);
     if (limits.limited()) {
       // A bar is the n-th largest of the lanes' maxima, n halved where the list would not hold what is not below it.  The high one leaves 300
       // to 400 tokens of a row; the other one, for where top_k may be more than that, about 64 ln 2 = 44 of a part, or half of that where the
@@ -729,7 +733,7 @@ __global__ __launch_bounds__(DR_THREADS) void k_sample(tt_sample_args a, Space s
   uint32_t token;
   const Weigher w(logit_of(top), l.temperature);
   auto weight_of = [&](int p) { return parts[p].sum > 0 ? parts[p].sum * w(parts[p].most) : 0.0; };
-  if (!l.single)
+  if (l.summed())
     for (int p = tid * per; p < min((tid + 1) * per, n); ++p) whole += weight_of(p);
   if (l.single || !l.limited()) {
     uint32_t p = 0;
