@@ -113,10 +113,17 @@ struct Slot {
   int64_t row;
   u64 mass[WD_BINS];
 };
+// What is known of a row that is not done.
+struct Row {
+  double whole;    // what all tokens weigh, if that is asked for
+  float most;      // the largest logit
+  uint32_t state;  // DONE, LEFT, or its slot
+  uint32_t last;   // with a slot: the bin that the nucleus ends in
+  uint32_t none;
+};
 struct Space {
   uint32_t* slots_taken;
-  double* whole;    // of rows that are not done: what all tokens weigh
-  uint32_t* state;  // of each row: DONE, LEFT, or its slot
+  Row* rows;
   Part* parts;
   Listed* lists;
   Slot* slots;  // nullptr: rows are gone over again by a workgroup each
@@ -636,13 +643,6 @@ __device__ __forceinline__ uint32_t gather_row(Threads& g, const RowSource<T>& r
   return row.size;
 }
 
-// The largest logit of a row's parts, by each wavefront.
-__device__ inline float most_of(const Part* parts, int64_t n) {
-  uint32_t best = 0;
-  for (int64_t p = threadIdx.x % WAVE; p < n; p += WAVE) best = max(best, order_of(parts[p].most));
-  return logit_of(max_of_lanes(best));
-}
-
 // The keys of the workgroup's threads, the largest first; `size` of them are not 0.
 template <class Threads>
 __device__ __forceinline__ u64 sorted(Threads& g, u64 key, uint32_t size) {
@@ -724,7 +724,7 @@ __global__ __launch_bounds__(DR_THREADS) void k_sample(tt_sample_args a, Space s
   uint32_t top = 0, high = NOTHING + 1;  // the largest order and the highest of the high bars
   for (int p = tid * per; p < min((tid + 1) * per, n); ++p) top = max(top, order_of(parts[p].most)), high = max(high, parts[p].high);
   g.most(top, high);
-  if (tid == 0) space.state[r] = DONE;
+  if (tid == 0) space.rows[r].state = DONE;
   if (top <= NOTHING) {
     if (tid == 0) put_token(a, r, ALL, 0, 1);
     return;
@@ -784,10 +784,9 @@ __global__ __launch_bounds__(DR_THREADS) void k_sample(tt_sample_args a, Space s
   }
   __syncthreads();
   if (tid == 0) {
-    space.whole[r] = whole;
     s.found = ALL;
     if (space.slots && !l.top_k) s.found = atomicAdd(space.slots_taken, 1u);
-    space.state[r] = s.found < space.slot_count ? s.found : LEFT;
+    space.rows[r] = Row{whole, logit_of(top), s.found < space.slot_count ? s.found : LEFT, WD_BINS, 0};
     if (s.found < space.slot_count) space.slots[s.found].row = r;
   }
   __syncthreads();
@@ -893,7 +892,7 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_bins(tt_sample_args a, Sp
     const Limits l = limits_of(a, r);
     if (!l.by_mass) continue;
     const RowSource<T> row{static_cast<const T*>(a.logits) + r * a.logits_stride, (uint32_t)a.vocab};
-    const Weigher w(most_of(space.parts + r * space.per_row, space.per_row), l.temperature);
+    const Weigher w(space.rows[r].most, l.temperature);
     const uint32_t from = item % across * WD_SEGMENT * space.size;
     for (int i = threadIdx.x; i < WD_BINS; i += PT_THREADS) s_bin[i] = 0;
     __syncthreads();
@@ -916,9 +915,10 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_above(tt_sample_args a, S
     const int64_t r = slot.row;
     const Limits l = limits_of(a, r);
     const RowSource<T> row{static_cast<const T*>(a.logits) + r * a.logits_stride, (uint32_t)a.vocab};
-    const Weigher w(most_of(space.parts + r * space.per_row, space.per_row), l.temperature);
-    const double target = (double)l.top_p * space.whole[r] * one_of((uint32_t)a.vocab);
+    const Weigher w(space.rows[r].most, l.temperature);
+    const double target = (double)l.top_p * space.rows[r].whole * one_of((uint32_t)a.vocab);
     const uint32_t last = l.by_mass ? last_bin<WD_BINS / PT_THREADS>(slot.mass, target, s_wave, &s_found) : WD_BINS;
+    if (item % across == 0 && threadIdx.x == 0) space.rows[r].last = last;
     const uint32_t stop = min((item % across + 1) * WD_SEGMENT, (uint32_t)space.per_row);
     for (uint32_t p = item % across * WD_SEGMENT + threadIdx.x / WAVE; p < stop; p += PT_THREADS / WAVE)
       part_above(row, space, r * space.per_row + p, p, w, last, l.by_weight ? (double)l.min_p : 0.0);
@@ -933,16 +933,17 @@ template <class T>
 __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Space space) {
   __shared__ SampleShared s;
   const int64_t r = blockIdx.x;
-  const uint32_t state = space.state[r];
+  const Row known = space.rows[r];
+  const uint32_t state = known.state;
   if (state == DONE) return;
   const int tid = threadIdx.x, n = (int)space.per_row;
   const Limits l = limits_of(a, r);
   const RowSource<T> row{static_cast<const T*>(a.logits) + r * a.logits_stride, (uint32_t)a.vocab};
   Group<RS_THREADS> g{s, tid, tid % WAVE, tid / WAVE};
   const Part* parts = space.parts + r * space.per_row;
-  const float most = most_of(parts, n);
+  const float most = known.most;
   const Weigher w(most, l.temperature);
-  const double whole = space.whole[r], target = (double)l.top_p * whole, min_p = l.by_weight ? (double)l.min_p : 0.0;
+  const double whole = known.whole, target = (double)l.top_p * whole, min_p = l.by_weight ? (double)l.min_p : 0.0;
   double mine = 0, all = 0;
   uint32_t token, last = WD_BINS, size = 0;
   // of rows that slots are for, those that found none go the same way as the others: which ones these are must not change a sum
@@ -991,18 +992,16 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
   bool again = l.top_k || n > SA_PARTS;
   if (!again) {
     if (l.by_mass) {
-      const double one = one_of((uint32_t)a.vocab);
-      const u64* bins = s.depth;
+      last = known.last;
       if (state == LEFT) {
+        const double one = one_of((uint32_t)a.vocab);
         __syncthreads();
         for (int i = tid; i < WD_BINS; i += RS_THREADS) s.depth[i] = 0;
         __syncthreads();
         add_to_bins(row, 0, row.size, RS_THREADS, w, one, s.depth);
         __syncthreads();
-      } else {
-        bins = space.slots[state].mass;
+        last = last_bin<WD_BINS / RS_THREADS>(s.depth, target * one, s.of_wave, &s.found);
       }
-      last = last_bin<WD_BINS / RS_THREADS>(bins, target * one, s.of_wave, &s.found);
     }
     if (state == LEFT)
       for (int p = g.wave; p < n; p += g.WAVES) part_above(row, space, r * space.per_row + p, p, w, last, min_p);
@@ -1074,13 +1073,12 @@ Space space_of(int64_t rows, int64_t vocab, void* at) {
   // 55 us by one takes 25 so, with 5 for the launches where none is left.
   const bool wide = vocab > SA_LIST && s.per_row <= SA_PARTS;
   s.slots_taken = static_cast<uint32_t*>(at);
-  s.whole = reinterpret_cast<double*>(static_cast<char*>(at) + 16);
-  s.parts = reinterpret_cast<Part*>(s.whole + batch);
+  s.rows = reinterpret_cast<Row*>(static_cast<char*>(at) + 16);
+  s.parts = reinterpret_cast<Part*>(s.rows + batch);
   s.lists = reinterpret_cast<Listed*>(s.parts + parts);
-  s.state = reinterpret_cast<uint32_t*>(s.lists + parts * PT_LIST);
-  s.bytes = 16 + batch * 8 + parts * (int64_t)(sizeof(Part) + PT_LIST * sizeof(Listed)) + (batch + 1) / 2 * 8;
+  s.bytes = 16 + batch * (int64_t)sizeof(Row) + parts * (int64_t)(sizeof(Part) + PT_LIST * sizeof(Listed));
   if (wide) {
-    s.slots = reinterpret_cast<Slot*>(s.state + (batch + 1) / 2 * 2);
+    s.slots = reinterpret_cast<Slot*>(s.lists + parts * PT_LIST);
     s.slot_count = (uint32_t)std::min(batch, (int64_t)WD_SLOTS);
     s.bytes += s.slot_count * (int64_t)sizeof(Slot);
   }
