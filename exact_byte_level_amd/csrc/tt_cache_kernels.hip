@@ -790,26 +790,29 @@ __global__ __launch_bounds__(AT_THREADS, D == 256 ? 1 : D == 64 ? 3 : 2) void k_
   }
 }
 
-// The pieces of a query head together: the first one, and the first one of each worker after its own.  `across` threads go by the
-// elements, four each, of `split` workgroups a head; the others by the pieces, each with a maximum of its own.  Bound by the launch and two
-// dependent reads: 4.5-4.9 us for a few heads, 6 for 32 heads of up to 256 pieces, 9 for 4,096 heads.
-template <class T>
+// The pieces of a query head together, by THREADS of a workgroup: the first one, and the first one of each worker after its own.  `across`
+// threads go by the elements, four each, of `split` workgroups a head; the others by the pieces, each with a maximum of its own. Bound by
+// the launch and two dependent reads: 4.7 us for a few heads, 6 for 32 heads of up to 256 pieces, 5.4 for 4,096.
+template <class T, int THREADS>
 __global__ __launch_bounds__(AT_THREADS) void k_join(tt_attend_args a, AttendShape shape, AttendSpace space, int wide, int split) {
   __shared__ f32x4 s_out[AT_THREADS];
   __shared__ float s_top[AT_THREADS], s_sum[AT_THREADS];
-  const int64_t id = blockIdx.x / split, i = id / a.heads;
+  constexpr int HEADS = AT_THREADS / THREADS;
+  const int at_block = threadIdx.x / THREADS * THREADS, tid = threadIdx.x - at_block;
+  const int64_t id = (int64_t)(blockIdx.x / split) * HEADS + threadIdx.x / THREADS, i = id / a.heads;
   const int h = (int)(id % a.heads), kv = h / shape.group, nth = h % shape.group;
   const int64_t unit = (int64_t)kv * shape.parts + nth / AT_HEADS;
-  const int32_t place = shape.bundle > 1 ? space.place[i] : (int32_t)(i * AT_HEADS);
+  const bool here = i < a.queries;
+  const int32_t place = shape.bundle > 1 ? (here ? space.place[i] : 0) : (int32_t)(i * AT_HEADS);
   const int64_t row = place % AT_HEADS * shape.group + nth % AT_HEADS;
-  const int2 of = space.pieces[place / AT_HEADS * shape.lanes + unit];
-  if (of.y == 1) return;
-  const int before = of.x / 2, tid = threadIdx.x, across = wide / 4 / split, side = AT_THREADS / across;
+  const int2 of = here ? space.pieces[place / AT_HEADS * shape.lanes + unit] : int2{0, 1};
+  const bool cut = of.y > 1;
+  const int before = of.x / 2, across = wide / 4 / split, side = THREADS / across;
   const int d = (blockIdx.x % split * across + tid % across) * 4;
   float top = -__builtin_inff(), sum = 0;
   f32x4 y = 0;
 #pragma unroll 4
-  for (int k = tid / across; k < of.y; k += side) {
+  for (int k = cut ? tid / across : of.y; k < of.y; k += side) {
     const int64_t at = ((k ? 2 * (before + k) : of.x) * shape.lanes + unit) * shape.rows + row;
     const float m = space.statistic[at * 2], l = space.statistic[at * 2 + 1];
     const f32x4 x = *reinterpret_cast<const f32x4*>(space.piece + at * wide + d);
@@ -817,16 +820,17 @@ __global__ __launch_bounds__(AT_THREADS) void k_join(tt_attend_args a, AttendSha
     const float old = __builtin_amdgcn_exp2f(top - less), by = __builtin_amdgcn_exp2f(m - less);
     y = y * old + x * by, sum = sum * old + l * by, top = most;
   }
-  s_out[tid] = y, s_top[tid] = top, s_sum[tid] = sum;
+  s_out[threadIdx.x] = y, s_top[threadIdx.x] = top, s_sum[threadIdx.x] = sum;
   __syncthreads();
-  if (tid >= across) return;
+  if (tid >= across || !cut) return;
   float most = top;
-  for (int k = 1; k < side; ++k) most = fmaxf(most, s_top[k * across + tid]);
+  for (int k = 1; k < side; ++k) most = fmaxf(most, s_top[at_block + k * across + tid]);
   const float less = most == -__builtin_inff() ? 0.0f : most;
   sum = 0, y = 0;
   for (int k = 0; k < side; ++k) {
-    const float by = __builtin_amdgcn_exp2f(s_top[k * across + tid] - less);
-    y += s_out[k * across + tid] * by, sum += s_sum[k * across + tid] * by;
+    const int at = at_block + k * across + tid;
+    const float by = __builtin_amdgcn_exp2f(s_top[at] - less);
+    y += s_out[at] * by, sum += s_sum[at] * by;
   }
   if (tid == 0 && blockIdx.x % split == 0 && a.lse) a.lse[i * a.lse_stride + h] = sum == 0 ? -__builtin_inff() : (most + __log2f(sum)) * LN2;
   if (d >= a.cache.dim) return;
@@ -904,9 +908,13 @@ hipError_t launch_attend(const tt_attend_args& a, hipStream_t st) {
   else enqueue_attend<__bf16, false>(a, shape, space, st);
   if (shape.workers > 1) {
     // few heads are joined by several workgroups each: 32 heads of 256 pieces take 10 us with one
-    const int split = a.queries * a.heads <= 128 ? padded(a.cache.dim) / 32 : 1;
-    auto* k = half ? k_join<_Float16> : k_join<__bf16>;
-    hipLaunchKernelGGL(k, dim3((uint32_t)(a.queries * a.heads * split)), dim3(AT_THREADS), 0, st, a, shape, space, padded(a.cache.dim), split);
+    const int64_t heads = a.queries * a.heads;
+    const int split = heads <= 128 ? padded(a.cache.dim) / 32 : 1;
+    // many by a wavefront each: 3,612 take 5.1 us so and 8.8 with a workgroup each, calls with 1,600 14.6 and 15.4, with 512 28.2 and 27.1
+    const bool many = heads >= 1024;
+    auto* k = many ? (half ? k_join<_Float16, WAVE> : k_join<__bf16, WAVE>) : (half ? k_join<_Float16, AT_THREADS> : k_join<__bf16, AT_THREADS>);
+    const int64_t groups = many ? div_up(heads, AT_THREADS / WAVE) : heads * split;
+    hipLaunchKernelGGL(k, dim3((uint32_t)groups), dim3(AT_THREADS), 0, st, a, shape, space, padded(a.cache.dim), many ? 1 : split);
   }
   return hipGetLastError();
 }

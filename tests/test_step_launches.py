@@ -93,9 +93,9 @@ def test_how_calls_are_cut_up(results):
     assert groups(results, attend(512, 64, 8)) == [512 * 8]
     assert groups(results, attend(513, 64, 8)) == [513 * 8]
     assert groups(results, attend(511, 8, 1, 64))[0] == 768
-    assert groups(results, attend(256, 32, 8)) == [512, 256 * 32] and groups(results, attend(257, 32, 8)) == [257 * 8]
+    assert groups(results, attend(256, 32, 8)) == [512, 256 * 32 // 4] and groups(results, attend(257, 32, 8)) == [257 * 8]
     assert groups(results, attend(513, 1, 1)) == [513]
-    assert groups(results, attend(301, 12, 12, 64, 2, True, 40)) == [1, 768, 301 * 12]
+    assert groups(results, attend(301, 12, 12, 64, 2, True, 40)) == [1, 768, 301 * 12 // 4]
     assert len(groups(results, attend(512, 17, 1, 128, 2, True, 1))) == 2  # too many heads for two queries of a row in a product
     # without limits two launches, with them three, and two more where there is much to go over again
     assert len(groups(results, sample(256, 262_144, 1, False))) == 2
