@@ -706,6 +706,31 @@ __device__ __forceinline__ Picked pick(Threads& g, uint32_t size, uint32_t top_k
   return p;
 }
 
+// Of a list of `size` tokens those that top_k may leave, all of its last order among them, with `bar` that order: how many there are. They
+// stay in the order of ids, which a few tokens a thread one behind the other keep.
+template <class Source, class Threads>
+__device__ __forceinline__ uint32_t shortened(const Source& source, Threads& g, const Weigher& w, uint32_t most, uint32_t top_k, uint32_t& bar) {
+  constexpr int MINE = SA_LIST / Threads::THREADS;
+  SampleShared& s = g.s;
+  double above, there;
+  Sampler<Source, Threads> list{source, w, g, s, most};
+  const uint32_t last = list.reach(false, bar > NOTHING + 1 ? bar : 0, top_k, above, there);
+  uint32_t order[MINE], id[MINE], count = 0, before, upto;
+#pragma unroll
+  for (int k = 0; k < MINE; ++k) {
+    const uint32_t i = g.tid * MINE + k;
+    order[k] = i < source.size ? s.order[i] : 0, id[k] = i < source.size ? s.id[i] : 0;
+    count += i < source.size && order[k] >= last;
+  }
+  const uint32_t size = g.sum(count, before, upto);
+#pragma unroll
+  for (int k = 0; k < MINE; ++k)
+    if (g.tid * MINE + k < source.size && order[k] >= last) s.order[before] = order[k], s.id[before++] = id[k];
+  __syncthreads();
+  bar = last;
+  return size;
+}
+
 // A row by a workgroup, from its parts.  Without limits the part that the random number falls into is read again; with limits
 // the tokens above all high bars, if they are few, are sorted, which answers everything that is asked of them; if the last one kept is not
 // among them the row is left to be gone over again.  Bound by its chain of dependent steps: the bars, the lists, 45 exchanges, three
@@ -953,6 +978,7 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
     g.most(bar, none);
     if (row.size <= SA_LIST) size = gather_row(g, row), bar = NOTHING + 1;
     else size = bar == ALL ? ALL : gather(g, parts, space.lists + r * space.per_row * PT_LIST, n, bar);
+    if (size >= RS_THREADS && size <= SA_LIST && l.top_k && l.top_k <= size) size = shortened(ListSource<T>{s, size}, g, w, order_of(most), (uint32_t)l.top_k, bar);
     if (size < RS_THREADS) {
       const Picked some = pick(g, size, (uint32_t)l.top_k, l, w, bar, 0, whole);
       if (some.decided) {
