@@ -650,8 +650,8 @@ constexpr int BU_THREADS = AT_QUERIES;
 
 // Puts the queries of a call in the order of rows and, within a row, of their last tokens, and those of a row that see some of the same tokens into bundles: so
 // no bundle reads more tokens than its queries do one by one.  By one workgroup, a query a thread, which is why a call may have at
-// most as many.  A chain of 45 exchanges and three sums: 7.2 us for 301 queries of 40 rows.  Those, which see 1,024 tokens of 12
-// heads each, are attended to in 40 us after it, one by one in 133.
+// most as many.  A chain of 45 exchanges and three sums: 7.2 us for 301 queries of 40 rows.  A call of these, which see 1,024 tokens of 12
+// heads each, takes 52 us with bundles, 108 without.
 __global__ __launch_bounds__(BU_THREADS) void k_bundle(tt_attend_args a, AttendShape shape, AttendSpace space) {
   __shared__ u64 s_key[BU_THREADS];
   __shared__ int64_t s_wave[BU_THREADS / WAVE];

@@ -96,7 +96,7 @@ constexpr int PT_THREADS = 256;
 constexpr int64_t PT_BATCH = 65536;  // parts of a launch
 constexpr int WD_SLOTS = 256;        // most rows of a launch that are gone over again by many workgroups
 constexpr int WD_BINS = 2048;
-constexpr int WD_SEGMENT = 4;        // parts of a workgroup: 256 x 262,144 take 124 us, with 8 or 2 131; 61 x 100,257 60, with 8 68
+constexpr int WD_SEGMENT = 4;        // parts of a workgroup: 256 x 262,144 take 110 us, with 8 or 2 114; 61 x 100,257 49, with 8 53
 
 struct Part {
   double sum;
@@ -140,8 +140,8 @@ struct Eight {
 
 // Q * 512 tokens a part, each read once.  By a wavefront alone: parts need nothing of each other, and with all of them in flight the
 // loads of one hide behind the weights of another.  What bounds it are these: a weight and its sum are 16 operations in 64 bits, at
-// a bit more than half the rate of those in 32.  192 x 100,256 bfloat16 without limits take 21 us, of which reading is 7
-// (38.5 MB at 5.6 TB/s); 256 x 262,144 float32 with limits 64, of which reading is 48.
+// a bit more than half the rate of those in 32.  192 x 100,256 bfloat16 without limits take 21.5 us, of which reading is 7
+// (38.5 MB at 5.6 TB/s); 256 x 262,144 float32, a third of whose rows are summed up, 54, of which reading is 48, and 64 if all are.
 template <class T, int Q>
 __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, Space space) {
   constexpr int MINE = Q * 8;
@@ -235,7 +235,7 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, S
 // -------------------------------------------------------------- a workgroup
 //
 // The draw from the lists is a chain of sums over a workgroup with little to do in between, which eight wavefronts get through
-// sooner than sixteen (one row of 50,256 23.5 us instead of 25.8); going over a row again takes sixteen.
+// sooner than sixteen (one row of 50,256 24.4 us instead of 25.6, 61 of 100,257 48.9 instead of 49.9); going over a row again takes sixteen.
 
 constexpr int DR_THREADS = 512;
 constexpr int RS_THREADS = 1024;
@@ -906,7 +906,7 @@ __device__ __forceinline__ uint32_t last_bin(const u64* bin, double target, u64*
 }
 
 // The rows in slots: the bins of their weights.  Each segment is summed up in LDS first.  Bound by the weights and by LDS atomics, 64 bits
-// each; for a third of 256 rows of 262,144 tokens 14 us, which come from the larger cache in good part.
+// each: 12.6 us for those of 256 rows of 262,144 tokens that need it, which come from the larger cache in good part.
 template <class T>
 __global__ __launch_bounds__(PT_THREADS) void k_sample_bins(tt_sample_args a, Space space) {
   __shared__ u64 s_bin[WD_BINS];
@@ -1083,8 +1083,8 @@ __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Sp
 
 // Steps of 512 tokens that a part has.  Calls of 2^23 logits and more fill the card with parts of 2,048, whose lists are few.  Below that
 // smaller ones leave each wavefront less to do, as long as a row has at most 128 of them (more lists than that take longer to
-// put together): of 1,024 tokens for 61 x 100,257 float16 with all limits 54 us instead of 60, for 60 x 60,000 without any 12.2 instead
-// of 13.9; below 2^20 logits of 512 for one row of 50,256 23.5 instead of 33.
+// put together): of 1,024 tokens for 61 x 100,257 float16 with all limits 49 us instead of 54.5, for 60 x 60,000 without any 12.8 instead
+// of 13.8; below 2^20 logits of 512 for one row of 50,256 24.4 instead of 31.5.
 uint32_t part_steps(int64_t rows, int64_t vocab) {
   if (rows * vocab >= (int64_t)1 << 23 || vocab > 256 * PT_STEP) return 4;
   return rows * vocab < (int64_t)1 << 20 && vocab <= 128 * PT_STEP ? 1 : 2;
@@ -1095,8 +1095,9 @@ Space space_of(int64_t rows, int64_t vocab, void* at) {
   s.size = part_steps(rows, vocab) * PT_STEP;
   s.per_row = std::max((vocab + s.size - 1) / s.size, (int64_t)1);
   const int64_t batch = std::min(rows, std::max(PT_BATCH / s.per_row, (int64_t)1)), parts = batch * s.per_row;
-  // Many workgroups go over a row again, as many rows as there are slots, where it is too long to be listed whole: the row of 50,256 that takes
-  // 55 us by one takes 25 so, with 5 for the launches where none is left.
+  // Many workgroups go over a row again, as many rows as there are slots, where it is too long to be listed whole: 61 x 100,257 with all
+  // limits take 49 us so and 113 by one each, 256 x 262,144 110 and 256, a row of 50,256 with a wide nucleus 29 and 42; where no row is
+  // left the launches cost 5.
   const bool wide = vocab > SA_LIST && s.per_row <= SA_PARTS;
   s.slots_taken = static_cast<uint32_t*>(at);
   s.rows = reinterpret_cast<Row*>(static_cast<char*>(at) + 16);
