@@ -952,8 +952,8 @@ __global__ __launch_bounds__(PT_THREADS) void k_sample_above(tt_sample_args a, S
 
 // The tokens of rows that are left, or whose parts know what is above their last bin: the bin's tokens are put in order, the part
 // is found, and the token in it.  A workgroup a row, since what each needs is little: a row whose bin is known takes 10 to 20 us, one
-// whose top_k is beyond its lists, or that has more tokens of one logit than these hold, several passes over it, 300 to
-// 500 us of 262,144.
+// whose top_k is beyond its lists, or that has more tokens of one logit than these hold, several passes over it: one row
+// of 262,144 380 to 470 us, 256 of them 540 to 990.
 template <class T>
 __global__ __launch_bounds__(RS_THREADS) void k_sample_rest(tt_sample_args a, Space space) {
   __shared__ SampleShared s;
