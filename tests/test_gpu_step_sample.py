@@ -218,6 +218,25 @@ def test_the_same_twice():
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("step", [0.0, 0.03125, 0.5])
+def test_lists_that_top_k_cuts_down(dtype, step):
+    """Limits of some hundred tokens in rows of which more are listed; many equal logits at the limit, fewer and more than a workgroup sorts; rows that
+    are listed whole, with NaN and -infinity among what top_k takes."""
+    rng, g = np.random.default_rng(11), torch.Generator("cuda").manual_seed(12)
+    for vocab in (3000, 70_000):
+        logits = torch.randn(12, vocab, device="cuda", generator=g).mul_(2)
+        if step:
+            logits = (logits / step).round_() * step
+        if vocab == 3000:
+            logits[3:6, 200:] = -float("inf")
+            logits[6:9, 500:] = float("nan")
+        k = rng.integers(257, 1100, 12)
+        for o in (dict(), dict(top_p=rng.uniform(0.8, 0.999, 12).astype(np.float32)), dict(min_p=np.full(12, 1e-3, np.float32)),
+                  dict(top_p=rng.uniform(0.8, 0.999, 12).astype(np.float32), min_p=np.full(12, 1e-4, np.float32), temperature=rng.uniform(0.5, 2, 12).astype(np.float32))):
+            check(logits.to(dtype), rng.random(12, dtype=np.float32), top_k=k, **o)
+
+
 def test_more_rows_gone_over_again_than_slots():
     """Flat rows, whose nuclei are far below the lists: which of them find a slot depends on the order of workgroups, the answers do not."""
     g = torch.Generator("cuda").manual_seed(9)
