@@ -43,21 +43,31 @@ __device__ inline double power_of_two(double t) {
 // Weights of a row: e^((x - top) / temperature); below 2^-1000 they count as zero.
 struct Weigher {
   float most;    // top as it was
-  float lowest;  // what is not above it weighs nothing
+  float lowest;  // the logit that weighs 2^-1000, as far as 32 bits tell
   double top, by;  // by = log2 e / temperature
   __device__ Weigher(float most_, float temperature) : most(most_), top(most_), by(1.4426950408889634 / (double)temperature) {
     lowest = (float)(top - 1000.0 / by);
   }
-  // (top itself apart, for an infinite one and for temperatures at which nothing else weighs; NaN is not above anything)
+  // log2 of the weight; NaN where there is none
+  __device__ double exponent(float x) const { return ((double)x - top) * by; }
+  // (top itself apart, for an infinite one and for temperatures at which nothing else weighs; NaN weighs nothing.  Rounded to 32 bits, `lowest`
+  // may lie many powers off where a step of the logits is as large as the temperature, so the exponent itself is compared)
   __device__ double operator()(float x) const {
-    const double y = power_of_two(((double)x - top) * by);
-    return x == most ? 1.0 : x > lowest ? y : 0.0;
+    const double t = exponent(x), y = power_of_two(t);
+    return x == most ? 1.0 : t >= -1000.0 ? y : 0.0;
   }
-  // Where the lowest is a number well below the top, sums that the top is in do not tell 2^-1000 from zero.
-  __device__ bool clear() const { return __builtin_fabsf(lowest) < __builtin_inff() && ((double)lowest - top) * by < -900.0; }
-  __device__ double roughly(float x) const { return power_of_two(((double)fmaxf(x, lowest) - top) * by); }
+  // Where the lowest is a number well below the top, sums that the top is in do not tell 2^-1000 from zero; and where it is not so far below that
+  // its power leaves the range, the smaller logits may be taken for it.
+  __device__ bool clear() const {
+    const double t = exponent(lowest);
+    return t < -900.0 && t >= -1010.0;
+  }
+  __device__ double roughly(float x) const { return power_of_two(exponent(fmaxf(x, lowest))); }
   // log2 of the weight, 0 down to -2^25.
-  __device__ float depth(float x) const { return x == most ? 0.0f : x > lowest ? (float)(((double)x - top) * by) : -33554432.0f; }
+  __device__ float depth(float x) const {
+    const double t = exponent(x);
+    return x == most ? 0.0f : t >= -1000.0 ? (float)t : -33554432.0f;
+  }
 };
 
 // What is asked of a row.
