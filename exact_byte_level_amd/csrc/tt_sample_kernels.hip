@@ -337,6 +337,7 @@ struct Group {
       __syncthreads();
     }
     before = value<V>(s.above);
+    __syncthreads();  // what was found has been read by all before the next search clears it
     return found;
   }
 };
