@@ -254,6 +254,12 @@ constexpr int SA_LIST = 4096;   // tokens of the lists that are above all bars
 constexpr int SA_BINS = 256;
 constexpr int SA_TILES = 1024;  // that a row is summed up in
 
+// What a wavefront has found.
+struct Hit {
+  u64 before;
+  uint32_t thread, kind;
+};
+
 struct SampleShared {
   union {
     u64 key[RS_THREADS];
@@ -266,8 +272,9 @@ struct SampleShared {
   uint32_t start[SA_PARTS];
   u64 digit[SA_BINS];
   u64 of_wave[RS_THREADS / WAVE];
+  Hit hit[RS_THREADS / WAVE];
   u64 above, of;
-  uint32_t found, last, place;
+  uint32_t found, place;
 };
 
 __device__ inline u64 bits(double v) { return (u64)__double_as_longlong(v); }
@@ -318,27 +325,23 @@ struct Group {
     x = max_of_lanes((uint32_t)(v >> 32)), y = max_of_lanes((uint32_t)v);
   }
 
-  // The first thread at which the running sum of x satisfies enough(sum, sum of all), which 0 does not and which once true stays so; the last
-  // one with an x above 0 if none does.  `before`: the sum of the threads before it.
+  // The first thread with an x above 0 at which the running sum of x satisfies enough(sum, sum of all), which 0 does not; the last one with an
+  // x above 0 if none does, since sums that are rounded may stay just below.  `before`: the sum of the threads before it.  Nor need rounded sums rise: a thread
+  // without anything may have one that is a step above that of the thread before it, so what it has itself is asked too.
+  // Each wavefront writes down its own such thread; that happens behind the barriers of a sum, so it cannot meet the reads of the search before.
   template <class V, class F>
   __device__ __forceinline__ uint32_t first(V x, F enough, V& before, V& all) {
-    if (tid == 0) s.found = ALL, s.last = 0;
     V at, upto;
     all = sum(x, at, upto);
-    if (enough(upto, all) && !enough(at, all)) s.found = tid, s.above = bits(at);
+    const u64 some = __ballot(x > 0), reached = __ballot(x > 0 && enough(upto, all));
+    if (lane == (reached ? __builtin_ctzll(reached) : some ? 63 - __builtin_clzll(some) : 0))
+      s.hit[wave] = Hit{bits(at), (uint32_t)tid, reached ? 2u : some ? 1u : 0u};
     __syncthreads();
-    uint32_t found = s.found;
-    if (found == ALL) {  // sums that are rounded may stay just below
-      const u64 some = __ballot(x > 0);
-      if (lane == 0 && some) atomicMax(&s.last, (uint32_t)(wave * WAVE + 63 - __builtin_clzll(some)));
-      __syncthreads();
-      found = s.last;
-      if (found == (uint32_t)tid) s.above = bits(at);
-      __syncthreads();
-    }
-    before = value<V>(s.above);
-    __syncthreads();  // what was found has been read by all before the next search clears it
-    return found;
+    const Hit hit = lane < WAVES ? s.hit[lane] : Hit{0, 0, 0};
+    const u64 found = __ballot(hit.kind == 2), other = __ballot(hit.kind == 1);
+    const int of = found ? __builtin_ctzll(found) : other ? 63 - __builtin_clzll(other) : 0;
+    before = value<V>(of_lane(hit.before, of));
+    return of_lane(hit.thread, of);
   }
 };
 
@@ -784,11 +787,12 @@ __global__ __launch_bounds__(DR_THREADS) void k_sample(tt_sample_args a, Space s
     } else {
       const uint32_t thread = g.first(whole, [&](double upto, double total) { return upto > (double)l.uniform * total; }, before, all);
       goal = (double)l.uniform * all;
-      p = thread * per;
-      for (uint32_t end = min(p + per, (uint32_t)n); p + 1 < end; ++p) {
-        const double y = weight_of(p);
-        if (before + y > goal) break;
-        before += y;
+      double upto = before;
+      for (uint32_t q = thread * per; q < min((thread + 1) * per, (uint32_t)n); ++q) {
+        const double y = weight_of(q);
+        if (!(y > 0)) continue;
+        p = q, before = upto, upto += y;
+        if (upto > goal) break;
       }
     }
     const uint32_t from = p * space.size;
