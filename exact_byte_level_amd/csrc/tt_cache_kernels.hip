@@ -286,6 +286,11 @@ __device__ inline float over_groups(float x, bool sum) {
   return sum ? z + u : fmaxf(z, u);
 }
 
+__device__ inline float across_groups_max(float x) {
+  const float y = fmaxf(x, __uint_as_float(across<16>(__float_as_uint(x))));
+  return fmaxf(y, __uint_as_float(across<32>(__float_as_uint(y))));
+}
+
 constexpr uint32_t ALL = 0xFFFFFFFFu;
 
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.693147180559945309417f;
@@ -305,6 +310,7 @@ struct Attend {
   static constexpr int LOADS = D / (4 * PER);      // of a token's key, by its four lanes
   static constexpr int MINE = D / 16;              // values of a token that a lane loads
   static constexpr int VWORDS = MINE * SIZE / 4;
+  static constexpr bool HALF = std::is_same<T, _Float16>::value;
   static constexpr int ROW = D + 4;                // of the output in LDS, so that 16 heads lie in other banks
 
   struct Shared {
@@ -441,6 +447,7 @@ struct Attend {
 #pragma unroll
     for (int j = 0; j < MINE; ++j) out[j] = 0;
     float top = -__builtin_inff(), sum = 0;
+    [[maybe_unused]] float peak = top;  // the largest score, where the reference may be below it
 
     int32_t entry = entry_of(base);
     uint32_t there = addresses(entry, base);
@@ -530,9 +537,25 @@ struct Attend {
       load_keys();
       __builtin_amdgcn_sched_barrier(0);
       {
-        // weights go by a maximum that may be 8 too low: they stay below 2^8, and most tiles leave it as it is
+        // weights go by a reference that is moved where a tile's largest score is far from it, which most tiles' are not: by a maximum that may be 8 too low,
+        // so that they stay below 2^8
         float most = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-        if (__any(most > top + 8.0f)) {
+        if constexpr (HALF) {
+          // Terms of float16 end at 2^-24, whatever the sum that they go into. So the reference goes down with the scores too: a tile's largest
+          // weight is 2^15 at most and 2^-3 at least, what its others lose is 2^-22 of that.  (Below 2^-48 of all a tile may have fewer bits, for the sums to stay
+          // in range.)
+          most = across_groups_max(most);
+          peak = fmaxf(peak, most);
+          const float to = fmaxf(most, peak - 48.0f) - 7.0f;
+          const bool move = to > top + 8.0f || (to < top - 10.0f && most > -__builtin_inff());
+          if (__any(move)) {
+            const float by = move ? __builtin_amdgcn_exp2f(top - to) : 1.0f;
+            top = move ? to : top;
+            sum *= by;
+#pragma unroll
+            for (int j = 0; j < MINE; ++j) out[j] *= by;
+          }
+        } else if (__any(most > top + 8.0f)) {
           most = fmaxf(over_groups(most, false), top);
           const float by = most == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top - most);
           top = most;
@@ -541,8 +564,8 @@ struct Attend {
           for (int j = 0; j < MINE; ++j) out[j] *= by;
         }
         const float less = top == -__builtin_inff() ? 0.0f : top;
-        // weights in two terms of 16 bits each, together good for 16 bits of mantissa and more: rounded to one they would
-        // cost as much as the output's own rounding
+        // weights in two terms of 16 bits each, together good for 16 bits of mantissa (float16: 22, down to 2^-25): rounded to one they
+        // would cost as much as the output's own rounding
         u32x4 weight, rest;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -573,7 +596,12 @@ struct Attend {
 
     // the wavefronts' parts together
     sum = over_groups(sum, true);
-    if (g == 0) s.top[wave][c] = top, s.sum[wave][c] = sum;
+    if constexpr (HALF) {
+      if (peak > -__builtin_inff()) sum *= __builtin_amdgcn_exp2f(top - peak);
+      if (g == 0) s.top[wave][c] = peak, s.sum[wave][c] = sum;
+    } else {
+      if (g == 0) s.top[wave][c] = top, s.sum[wave][c] = sum;
+    }
     __syncthreads();
     float all = s.top[0][c], total = 0;
 #pragma unroll
