@@ -46,6 +46,14 @@ def _handle(stream):
     return None if stream is None else stream.cuda_stream
 
 
+def _needs(x, name, dims):
+    """What a call takes sizes from before the binding has looked at it."""
+    if not isinstance(x, _torch.Tensor):
+        raise ValueError("%s: a tensor is needed" % name)
+    if x.dim() != dims:
+        raise ValueError("%s: a %d-d tensor is needed, got a %d-d one" % (name, dims, x.dim()))
+
+
 def _space(bytes, where, device):
     if bytes < 0:
         _check(bytes, where)
@@ -68,6 +76,8 @@ def attend_workspace(query, key_cache):
     """A workspace for attend_cache_into with tensors of these shapes, or None where none is needed."""
     if _bind is None:
         _start()
+    _needs(query, "query", 3)
+    _needs(key_cache, "key_cache", 4)
     return _space(_lib.tt_attend_workspace(query.shape[0], query.shape[1], key_cache.shape[2], key_cache.shape[3]),
                   "tt_attend_workspace", query.device)
 
@@ -111,6 +121,7 @@ def attend_cache(query, key_cache, value_cache, table, lengths, lse=False, strea
     as in attend_cache_into."""
     if _bind is None:
         _start()
+    _needs(query, "query", 3)
     with _on(stream):
         out = _torch.empty(query.shape, dtype=query.dtype, device=query.device)
         sums = _torch.empty(query.shape[:2], dtype=_torch.float32, device=query.device) if lse else None
@@ -154,6 +165,7 @@ def sample_workspace(logits):
     """A workspace for sample_tokens_into with logits of this shape, or None where none is needed."""
     if _bind is None:
         _start()
+    _needs(logits, "logits", 2)
     return _space(_lib.tt_sample_workspace(logits.shape[0], logits.shape[1]), "tt_sample_workspace", logits.device)
 
 
@@ -183,6 +195,7 @@ def sample_tokens(logits, uniform, logprobs=False, stream=None, **options):
     sample_tokens_into."""
     if _bind is None:
         _start()
+    _needs(logits, "logits", 2)
     with _on(stream):
         tokens = _torch.empty(logits.shape[0], dtype=_torch.int32, device=logits.device)
         shares = _torch.empty(logits.shape[0], dtype=_torch.float32, device=logits.device) if logprobs else None
