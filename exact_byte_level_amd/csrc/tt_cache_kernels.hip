@@ -178,7 +178,8 @@ struct AttendShape {
 // of heads of up to 64 elements, two of 128, one of 256 (that is what their registers leave room for).  On 8 heads of keys of 128
 // elements 64 requests of 2,000 to 32,000 tokens take 905 us dealt out and 1,121 by a workgroup each, which wait for the longest;
 // 256 of 300 to 4,000 tokens 477 and 488; 500 of up to 2,000 482 and 470.
-// Where there are more queries than rows, some go by the same row, and those that a product has room for are attended to together.
+// Where there are more queries than the table has rows, some go by the same row, and those that a product has room for are attended to together.
+// In a table with rows to spare the host cannot tell whether queries share one, and they go one by one.
 AttendShape attend_shape(int64_t queries, int64_t heads, int64_t cache_heads, int64_t dim, int64_t table_rows, bool by_rows) {
   AttendShape s;
   s.group = (int)(heads / cache_heads);

@@ -88,6 +88,9 @@ def attend_cache_into(query, key_cache, value_cache, table, lengths, out, rows=N
     not above 0: none) tokens of its row of ``table`` (int32 [R, width]), row ``rows[i]`` (int32 [N]) or, without them, row
     i; ``out`` is like the query.
 
+    Several queries of a row read its tokens together only where there are more queries than rows of ``table``, 512 at most: a table that is
+    cut to the rows in use serves them better.
+
     ``scale``: of the scores, by default ``1 / sqrt(dim)``; ``window``: above 0, only the last so many tokens are seen;
     ``softcap``: 0, or 1e-6 .. 1e20, by which scores are capped through a tanh; ``key_scale``, ``value_scale``: what write_cache_into divided by; ``lse``
     (float32 [N, heads]): receives the logarithm of each sum of weights.  ``workspace``: from attend_workspace; without it

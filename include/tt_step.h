@@ -79,7 +79,9 @@ typedef struct tt_attend_args {
   const int32_t* table;      /* [table_rows][width] blocks of each request; a token in a block outside the cache is not seen */
   int64_t table_stride, table_rows, width;  /* width * cache.block_size <= 2^31 - 1 */
   const int32_t* lengths;    /* [queries] tokens that each query sees, from its request's first on; not above 0: none */
-  const int32_t* rows;       /* [queries] row of the table that each goes by; NULL: row i.  No row of it: sees nothing */
+  /* [queries] row of the table that each goes by; NULL: row i.  No row of it: sees nothing.  Queries of a row read its tokens together where
+   * queries are more than table_rows, 512 at most, and no more than 8 heads of them share a head of keys; else each by itself. */
+  const int32_t* rows;
   double scale;              /* of the scores */
   double softcap;            /* 0, or 1e-6 .. 1e20: scores x become softcap * tanh(x / softcap) */
   int64_t window;            /* above 0: only the last `window` of the tokens are seen */
