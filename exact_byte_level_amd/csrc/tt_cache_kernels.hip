@@ -111,7 +111,7 @@ __device__ inline void put_eight(typename Eight<I>::type x, const float* scale, 
 // Each thread moves eight keys and the eight values beside them, of `total` of the tokens from `first` on: both loads are on their way
 // before the slot is known to be there.  Eight elements are 16 bytes of bfloat16, and of 8 bits what one lane can store at once.
 // Bound by memory: 48,000 tokens of 8 heads of 128 elements, bfloat16 to e4m3, take 60 us for 292 MB (4.9 TB/s, what a
-// large copy reaches; with divisions in place of the corrected products 69); 8 tokens 2.7 us, the launch and two dependent reads.
+// large copy reaches; with divisions in place of the corrected products 69); 8 tokens 2.3 us, the launch and two dependent reads.
 template <class I, class O>
 __global__ __launch_bounds__(WR_THREADS) void k_write(tt_write_args a, Division by_token, Division by_head, Division by_block, int64_t first, uint32_t total) {
   const uint32_t at = blockIdx.x * WR_THREADS + threadIdx.x;
@@ -149,13 +149,16 @@ __global__ __launch_bounds__(WR_THREADS) void k_write(tt_write_args a, Division 
 //
 // Each wavefront has one tile's keys and values in registers and the next one's loads on their way while it computes.  Two or three wavefronts a
 // SIMD then keep 30 KB and more of a CU in flight.  What it measured:
-//   64 requests of up to 32,000 tokens, 64 heads on 8 of 128 elements, bfloat16   893 us for 5.13 GB: 5.7 TB/s, memory
-//   33 requests of up to 8,000, 16 heads on 4 of 256                              126 us for 663 MB: 5.3 TB/s, memory
-//   9 requests of up to 9,000, 28 heads on 4 of 128                               26.7 us for 104 MB: a third is the way to the first tile
-//   one request of 4,000, 32 heads on 8 of 128                                    10.5 us: that way alone, a tile or two a wavefront
-//   2 requests of 400,001, 16 heads on one of 128, e4m3                           46.8 us for 205 MB: 4.4 TB/s, widening to 16 bits and
-//     permutations beside the loads; three wavefronts a SIMD (49-54 us) and tiles of 64 tokens (52) were slower
-//   301 queries of 40 rows, 12 heads of 64, a window of 1,024, capped             39.7 us for 165 MB, in bundles
+//   64 requests of up to 32,000 tokens, 64 heads on 8 of 128 elements, bfloat16   903 us for 5.13 GB: 5.7 TB/s, memory
+//   33 requests of up to 8,000, 16 heads on 4 of 256                              128 us for 663 MB: 5.2 TB/s, memory
+//   9 requests of up to 9,000, 28 heads on 4 of 128, float16                      27.5 us for 104 MB
+//   one request of 4,000, 32 heads on 8 of 128                                    10.9 us for 16 MB, a tile or two a wavefront
+//   2 requests of 400,001, 16 heads on one of 128, e4m3                           46.0 us for 205 MB: 4.4 TB/s; three wavefronts a SIMD (49-54 us)
+//     and tiles of 64 tokens (52) were slower
+//   301 queries of 40 rows, 12 heads of 64, a window of 1,024, capped, float16    40.2 us for 165 MB, in bundles
+// What all of these but the first have beside their bytes at 5.6 TB/s is the same 8 to 11 us: the way to the first tile (lengths, sums over them, table, addresses,
+// keys, each waiting for the one before) and the end.  Vector operations keep a SIMD busy for 12 to 14 percent of the first three's time, and
+// matrix operations for 3 to 6; with e4m3, which is widened, 25 and 7.
 
 constexpr int AT_THREADS = 256;
 constexpr int AT_WAVES = AT_THREADS / WAVE;
@@ -679,8 +682,8 @@ constexpr int BU_THREADS = AT_QUERIES;
 
 // Puts the queries of a call in the order of rows and, within a row, of their last tokens, and those of a row that see some of the same tokens into bundles: so
 // no bundle reads more tokens than its queries do one by one.  By one workgroup, a query a thread, which is why a call may have at
-// most as many.  A chain of 45 exchanges and three sums: 7.2 us for 301 queries of 40 rows.  A call of these, which see 1,024 tokens of 12
-// heads each, takes 52 us with bundles, 108 without.
+// most as many.  A chain of 45 exchanges and three sums: 7.3 us for 301 queries of 40 rows.  A call of these, which see 1,024 tokens of 12
+// heads each, takes 51 us with bundles, 108 without.
 __global__ __launch_bounds__(BU_THREADS) void k_bundle(tt_attend_args a, AttendShape shape, AttendSpace space) {
   __shared__ u64 s_key[BU_THREADS];
   __shared__ int64_t s_wave[BU_THREADS / WAVE];
@@ -821,7 +824,7 @@ __global__ __launch_bounds__(AT_THREADS, D == 256 ? 1 : D == 64 ? 3 : 2) void k_
 
 // The pieces of a query head together, by THREADS of a workgroup: the first one, and the first one of each worker after its own.  `across`
 // threads go by the elements, four each, of `split` workgroups a head; the others by the pieces, each with a maximum of its own. Bound by
-// the launch and two dependent reads: 4.7 us for a few heads, 6 for 32 heads of up to 256 pieces, 5.4 for 4,096.
+// the launch and two dependent reads: 5 us for a few heads, 6.7 for 32 heads of up to 256 pieces, 5.6 for 4,096.
 template <class T, int THREADS>
 __global__ __launch_bounds__(AT_THREADS) void k_join(tt_attend_args a, AttendShape shape, AttendSpace space, int wide, int split) {
   __shared__ f32x4 s_out[AT_THREADS];

@@ -150,9 +150,9 @@ struct Eight {
   typedef T type __attribute__((ext_vector_type(8), aligned(alignof(T))));
 };
 
-// Q * 512 tokens a part, each read once.  By a wavefront alone: parts need nothing of each other, and with all of them in flight the
-// loads of one hide behind the weights of another.  What bounds it are these: a weight and its sum are 16 operations in 64 bits, at
-// a bit more than half the rate of those in 32.  192 x 100,256 bfloat16 without limits take 21.5 us, of which reading is 7
+// Q * 512 tokens a part, each read once.  By a wavefront alone: parts need nothing of each other.  Most of a call's wavefronts are there at once, so
+// all load first and weigh then, and one hides little of the other.  What bounds it are the weights: one and its sum are 16 operations in 64 bits, at
+// a bit more than half the rate of those in 32.  192 x 100,256 bfloat16 without limits take 21.8 us, of which reading is 7
 // (38.5 MB at 5.6 TB/s); 256 x 262,144 float32, a third of whose rows are summed up, 54, of which reading is 48, and 64 if all are.
 template <class T, int Q>
 __global__ __launch_bounds__(PT_THREADS) void k_sample_parts(tt_sample_args a, Space space) {
@@ -923,7 +923,7 @@ __device__ __forceinline__ uint32_t last_bin(const u64* bin, double target, u64*
 }
 
 // The rows in slots: the bins of their weights.  Each segment is summed up in LDS first.  Bound by the weights and by LDS atomics, 64 bits
-// each: 12.6 us for those of 256 rows of 262,144 tokens that need it, which come from the larger cache in good part.
+// each: 12.4 us for those of 256 rows of 262,144 tokens that need it, which come from the larger cache in good part.
 template <class T>
 __global__ __launch_bounds__(PT_THREADS) void k_sample_bins(tt_sample_args a, Space space) {
   __shared__ u64 s_bin[WD_BINS];
