@@ -96,7 +96,8 @@ typedef struct tt_attend_args {
  *
  * Scores, maxima and sums are held in 32 bits.  A weight goes into its product as two terms
  * of the query's type: off by 2^-16 of it at most with TT_BF16; with TT_F16 by 2^-22 of it, or of the
- * largest weight among the 32 tokens that it is taken together with.  out is rounded once.  A query that
+ * largest weight among the 32 tokens that it is taken together with (of less than 2^-64 of
+ * the query's largest it has fewer bits).  out is rounded once.  A query that
  * sees nothing, or whose scores are all -infinity, gets zeros and -infinity; what the
  * cache holds elsewhere, NaN included, has no effect.  Values that are seen are
  * meant to be finite: an infinite one gives infinities or NaN to the queries that see it.
